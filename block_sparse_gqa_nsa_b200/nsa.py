@@ -29,6 +29,9 @@ ROUTE_GIVEN, ROUTE_SCORE, ROUTE_GEOMETRIC, ROUTE_ALL = 0, 1, 2, 3
 EXPORTS = ("lsrm_nsa_workspace_size", "lsrm_nsa_workspace_init", "lsrm_nsa_compress", "lsrm_route_score_topk",
            "lsrm_route_geometric", "lsrm_route_geometric_noalloc", "lsrm_route_camera", "lsrm_route_pooled_topk", "lsrm_nsa_cmp_attn", "lsrm_nsa_select_attn",
            "lsrm_nsa_window_attn", "lsrm_nsa_gate_combine", "lsrm_nsa_attend", "lsrm_nsa_mixture", "lsrm_nsa_forward", "lsrm_nsa_backward",
+           "lsrm_relpos_workspace_size", "lsrm_relpos_workspace_init", "lsrm_relpos_log_buckets",
+           "lsrm_relpos_forward", "lsrm_relpos_backward",
+           "lsrm_layer_norm_forward", "lsrm_layer_norm_workspace_size", "lsrm_layer_norm_backward",
            "lsrm_nsa_last_device_status", "lsrm_status_string", "lsrm_diag_exp2_poly")
 
 
@@ -58,6 +61,20 @@ def make_desc(n_tokens, n_blocks, max_block_len, n_q_heads, n_kv_heads, head_dim
                 int(top_k), int(window), float(scale), int(bool(pooled_q)), int(n_gates), nf, fp)
 
 
+class RelposDesc(ctypes.Structure):
+    """lsrm_relpos_desc (host struct)."""
+    _fields_ = [("n_q_tokens", ctypes.c_int64), ("n_k_tokens", ctypes.c_int64), ("n_segs", ctypes.c_int32),
+                ("n_q_heads", ctypes.c_int32), ("n_kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+                ("n_axes", ctypes.c_int32), ("n_buckets", ctypes.c_int32), ("max_distance", ctypes.c_int32),
+                ("scale", ctypes.c_float)]
+
+
+def make_relpos_desc(n_q_tokens, n_k_tokens, n_segs, n_q_heads, n_kv_heads, head_dim, n_axes, n_buckets,
+                     max_distance, scale=0.0) -> RelposDesc:
+    return RelposDesc(int(n_q_tokens), int(n_k_tokens), int(n_segs), int(n_q_heads), int(n_kv_heads), int(head_dim),
+                      int(n_axes), int(n_buckets), int(max_distance), float(scale))
+
+
 _lib = None
 
 
@@ -69,8 +86,9 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     if not os.path.exists(path):
         raise RuntimeError(f"{path} is not built; run `python -m block_sparse_gqa_nsa_b200.build`")
     lib = ctypes.CDLL(path)
-    vp, i32, sz = ctypes.c_void_p, ctypes.c_int32, ctypes.c_size_t
+    vp, i32, i64, sz = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t
     D = ctypes.POINTER(Desc)
+    R = ctypes.POINTER(RelposDesc)
     sigs = {
         "lsrm_nsa_workspace_size": ([D], sz),
         "lsrm_nsa_workspace_init": ([D, vp, sz, vp], ctypes.c_int),
@@ -88,6 +106,14 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
         "lsrm_route_camera": ([D, vp, vp, i32, i32, vp, i32, i32, i32, vp, i32, i32, vp, vp, vp], ctypes.c_int),
         "lsrm_nsa_forward": ([D, vp, vp, vp, vp, vp, vp, i32, vp, vp, vp, vp, vp, vp], ctypes.c_int),
         "lsrm_nsa_backward": ([D, vp, vp, vp, vp, vp, vp, i32, vp, vp, vp, vp, vp, vp, vp, vp, vp], ctypes.c_int),
+        "lsrm_relpos_workspace_size": ([R], sz),
+        "lsrm_relpos_workspace_init": ([R, vp, sz, vp], ctypes.c_int),
+        "lsrm_relpos_log_buckets": ([i32, i32, vp], ctypes.c_int),
+        "lsrm_relpos_forward": ([R] + [vp] * 12 + [sz, vp], ctypes.c_int),
+        "lsrm_relpos_backward": ([R] + [vp] * 17 + [sz, vp], ctypes.c_int),
+        "lsrm_layer_norm_forward": ([i64, i32, i32, vp, vp, vp, ctypes.c_float, vp, vp, vp, vp], ctypes.c_int),
+        "lsrm_layer_norm_workspace_size": ([i64, i32], sz),
+        "lsrm_layer_norm_backward": ([i64, i32, i32] + [vp] * 9 + [sz, vp], ctypes.c_int),
         "lsrm_nsa_last_device_status": ([vp, vp], ctypes.c_int),
         "lsrm_status_string": ([ctypes.c_int], ctypes.c_char_p),
         "lsrm_diag_exp2_poly": ([vp, vp, ctypes.c_int64, vp], ctypes.c_int),
@@ -304,3 +330,144 @@ def lsrm_diag_exp2_poly(x, y, stream=None):
     if x.numel() != y.numel():
         raise ValueError("x and y differ in size")
     _call("lsrm_diag_exp2_poly", _ptr(x), _ptr(y), ctypes.c_int64(x.numel()), _stream(stream))
+
+
+# ---- relative position bias and layer norm ---------------------------------------------------------
+# These calls check shapes as well, and run on the tensors' own device (its current stream unless
+# one is given), whichever device is current.
+
+def _check_all(device, *items):
+    """(tensor, name, dtype, shape) of each: the type, shape, contiguity and device the call needs."""
+    for t, name, dtype, shape in items:
+        if t.dtype != dtype:
+            raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
+        if t.shape != shape:
+            raise ValueError(f"{name}: expected {list(shape)}, got {list(t.shape)}")
+        if not t.is_contiguous():
+            raise ValueError(f"{name}: must be contiguous")
+        if t.device != device:
+            raise ValueError(f"{name}: on {t.device}, expected {device}")
+
+
+def _call_on(device: torch.device, name: str, stream, *args):
+    if device.type != "cuda":
+        raise ValueError(f"{name}: needs CUDA tensors")
+    if device.index == torch.cuda.current_device():
+        _call(name, *args, _stream(stream))
+    else:
+        with torch.cuda.device(device):
+            _call(name, *args, _stream(stream))
+
+
+def lsrm_relpos_workspace_size(desc: RelposDesc) -> int:
+    return int(load_library().lsrm_relpos_workspace_size(ctypes.byref(desc)))
+
+
+def lsrm_relpos_workspace_init(desc: RelposDesc, ws: torch.Tensor, stream=None):
+    _check(ws, torch.uint8, "ws")
+    _call_on(ws.device, "lsrm_relpos_workspace_init", stream, ctypes.byref(desc), ws.data_ptr(), ws.numel())
+
+
+def relpos_workspace(desc: RelposDesc, device=None, stream=None) -> torch.Tensor:
+    """Allocate (through torch) and initialise the workspace the relpos calls of this descriptor need."""
+    n = lsrm_relpos_workspace_size(desc)
+    if n == 0:
+        raise NsaError("lsrm_relpos_workspace_size", 1)
+    ws = torch.empty(n, dtype=torch.uint8, device=device or "cuda")
+    lsrm_relpos_workspace_init(desc, ws, stream)
+    return ws
+
+
+def lsrm_relpos_log_buckets(n_buckets: int, max_distance: int) -> torch.Tensor:
+    """Logarithmic buckets of the clamped distances -D..D: int32 [2 D + 1] on the host."""
+    out = torch.empty(2 * max(int(max_distance), 0) + 1, dtype=torch.int32)
+    _call("lsrm_relpos_log_buckets", int(n_buckets), int(max_distance), out.data_ptr())
+    return out
+
+
+def _relpos_checks(desc, off_q, off_k, pos_q, pos_k, bucket_of, table, q, k, v):
+    bf, i32 = torch.bfloat16, torch.int32
+    qs = (desc.n_q_tokens, desc.n_q_heads, desc.head_dim)
+    ks = (desc.n_k_tokens, desc.n_kv_heads, desc.head_dim)
+    segs = (desc.n_segs + 1,)
+    return qs, ks, [(off_q, "off_q", i32, segs), (off_k, "off_k", i32, segs),
+                    (pos_q, "pos_q", i32, (desc.n_q_tokens, desc.n_axes)),
+                    (pos_k, "pos_k", i32, (desc.n_k_tokens, desc.n_axes)),
+                    (bucket_of, "bucket_of", i32, (2 * desc.max_distance + 1,)),
+                    (table, "table", bf, (desc.n_axes, desc.n_buckets, desc.n_q_heads)),
+                    (q, "q", bf, qs), (k, "k", bf, ks), (v, "v", bf, ks)]
+
+
+def lsrm_relpos_forward(desc: RelposDesc, off_q, off_k, pos_q, pos_k, bucket_of, table, q, k, v, out, lse=None,
+                        ws=None, stream=None):
+    """Attention over ragged segments with a learned relative position bias by buckets; lse (optional)
+    fp32 [Nq][Hq] is what the backward needs."""
+    qs, ks, items = _relpos_checks(desc, off_q, off_k, pos_q, pos_k, bucket_of, table, q, k, v)
+    items.append((out, "out", torch.bfloat16, qs))
+    if lse is not None:
+        items.append((lse, "lse", torch.float32, qs[:2]))
+    if ws is not None:
+        items.append((ws, "ws", torch.uint8, ws.shape))
+    _check_all(q.device, *items)
+    _call_on(q.device, "lsrm_relpos_forward", stream, ctypes.byref(desc), *map(_ptr, (off_q, off_k, pos_q, pos_k,
+             bucket_of, table, q, k, v, out, lse, ws)), 0 if ws is None else ws.numel())
+
+
+def lsrm_relpos_backward(desc: RelposDesc, off_q, off_k, pos_q, pos_k, bucket_of, table, q, k, v, out, lse, dout,
+                         dq, dk, dv, dtable, ws, stream=None):
+    """Gradients of lsrm_relpos_forward with respect to q, k, v and the bias table."""
+    bf = torch.bfloat16
+    qs, ks, items = _relpos_checks(desc, off_q, off_k, pos_q, pos_k, bucket_of, table, q, k, v)
+    _check_all(q.device, *items, (out, "out", bf, qs), (lse, "lse", torch.float32, qs[:2]), (dout, "dout", bf, qs),
+               (dq, "dq", bf, qs), (dk, "dk", bf, ks), (dv, "dv", bf, ks), (dtable, "dtable", bf, table.shape),
+               (ws, "ws", torch.uint8, ws.shape))
+    _call_on(q.device, "lsrm_relpos_backward", stream, ctypes.byref(desc), *map(_ptr, (off_q, off_k, pos_q, pos_k,
+             bucket_of, table, q, k, v, out, lse, dout, dq, dk, dv, dtable, ws)), ws.numel())
+
+
+_LN_DTYPES = {torch.bfloat16: 0, torch.float32: 1}
+
+
+def _ln_rows(x):
+    if x.dtype not in _LN_DTYPES:
+        raise TypeError(f"x: expected torch.bfloat16 or torch.float32, got {x.dtype}")
+    if x.dim() < 1 or x.shape[-1] < 1:
+        raise ValueError("x: needs rows of at least one element")
+    return x.numel() // x.shape[-1], x.shape[-1]
+
+
+def lsrm_layer_norm_forward(x, gamma, beta, eps, y, mean=None, rstd=None, stream=None):
+    """Layer norm over the last axis of x; gamma / beta (or None) of x's type; mean / rstd (optional)
+    fp32, one per row, are what the backward needs.  y may be x."""
+    rows, width = _ln_rows(x)
+    items = [(x, "x", x.dtype, x.shape), (y, "y", x.dtype, x.shape)]
+    items += [(t, n, x.dtype, (width,)) for t, n in ((gamma, "gamma"), (beta, "beta")) if t is not None]
+    items += [(t, n, torch.float32, (rows,)) for t, n in ((mean, "mean"), (rstd, "rstd")) if t is not None]
+    _check_all(x.device, *items)
+    _call_on(x.device, "lsrm_layer_norm_forward", stream, rows, width, _LN_DTYPES[x.dtype], _ptr(x), _ptr(gamma),
+             _ptr(beta), float(eps), _ptr(y), _ptr(mean), _ptr(rstd))
+
+
+def lsrm_layer_norm_workspace_size(rows: int, width: int) -> int:
+    return int(load_library().lsrm_layer_norm_workspace_size(int(rows), int(width)))
+
+
+def layer_norm_workspace(rows: int, width: int, device=None) -> torch.Tensor:
+    """Allocate (through torch) the workspace lsrm_layer_norm_backward needs."""
+    n = lsrm_layer_norm_workspace_size(rows, width)
+    if n == 0:
+        raise NsaError("lsrm_layer_norm_workspace_size", 1)
+    return torch.empty(n, dtype=torch.uint8, device=device or "cuda")
+
+
+def lsrm_layer_norm_backward(dy, x, gamma, mean, rstd, dx, dgamma, dbeta, ws, stream=None):
+    """Gradients of lsrm_layer_norm_forward; dgamma / dbeta may be None.  dx may be dy or x."""
+    rows, width = _ln_rows(x)
+    items = [(x, "x", x.dtype, x.shape), (dy, "dy", x.dtype, x.shape), (dx, "dx", x.dtype, x.shape),
+             (mean, "mean", torch.float32, (rows,)), (rstd, "rstd", torch.float32, (rows,)),
+             (ws, "ws", torch.uint8, ws.shape)]
+    items += [(t, n, x.dtype, (width,)) for t, n in ((gamma, "gamma"), (dgamma, "dgamma"), (dbeta, "dbeta"))
+              if t is not None]
+    _check_all(x.device, *items)
+    _call_on(x.device, "lsrm_layer_norm_backward", stream, rows, width, _LN_DTYPES[x.dtype], _ptr(dy), _ptr(x),
+             _ptr(gamma), _ptr(mean), _ptr(rstd), _ptr(dx), _ptr(dgamma), _ptr(dbeta), _ptr(ws), ws.numel())

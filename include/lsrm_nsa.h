@@ -297,6 +297,100 @@ LSRM_API lsrm_status lsrm_nsa_backward(const lsrm_nsa_desc* desc, const int32_t*
                               const float* lse, const void* obr_or_null, const void* dout, void* dq, void* dk,
                               void* dv, void* dgates, void* ws, void* stream);
 
+/* ---- attention with a learned relative position bias by buckets ---------------------------------
+ *
+ * The layer's own attention knows where a token is only through its routing.  These calls are dense
+ * softmax attention over ragged segments (blocks, frames, streams) whose scores get a learned bias
+ * from the tokens' integer positions on 1 to 3 axes (lattice coordinates as lsrm_route_geometric
+ * takes them, frame numbers, patch rows and columns), and its backward with the gradient of the bias
+ * table (the pages' factorised position embedding, LSRM page, 方法, is per axis as well, but absolute).
+ * Segment s holds the queries off_q[s] .. off_q[s+1]-1 and the keys off_k[s] .. off_k[s+1]-1; every
+ * query of a segment attends every key of it.  With D = max_distance, tau = scale, g = h / (Hq/Hkv):
+ *   delta_a = clamp(pos_k[j][a] - pos_q[i][a], -D, D)
+ *   t[i,h,j] = tau q[i,h] . k[j,g] + sum_a table[a][bucket_of[delta_a + D]][h]
+ *   lse[i,h] = log sum_j exp(t[i,h,j]);  out[i,h] = sum_j exp(t[i,h,j] - lse[i,h]) v[j,g]
+ * A query whose segment has no key (or whose every t is -inf, by a table entry of -inf) gets out = 0
+ * and lse = -inf.  Queries and keys may be the same tensors (self attention: off_q = off_k, pos_q =
+ * pos_k) or not: one new token against a long past is a segment of one query. */
+typedef struct {
+  int64_t n_q_tokens;   /* Nq, 0..2^31-1 */
+  int64_t n_k_tokens;   /* Nk, 0..2^31-1 */
+  int32_t n_segs;       /* S >= 1 */
+  int32_t n_q_heads;    /* Hq, multiple of n_kv_heads */
+  int32_t n_kv_heads;   /* Hkv >= 1 */
+  int32_t head_dim;     /* d in {32, 64} */
+  int32_t n_axes;       /* position axes, 1..3 */
+  int32_t n_buckets;    /* 1..64 */
+  int32_t max_distance; /* D, 1..1023 */
+  float scale;          /* softmax scale tau; 0 -> 1/sqrt(d) */
+} lsrm_relpos_desc;
+
+/* Bytes of device workspace of the two calls below for this descriptor (a multiple of 256; 0 for a
+ * descriptor they do not take), and its initialisation (the status word; once after allocation).
+ * The calls keep nothing in it from one call to the next, apart from the status word, but calls that
+ * may overlap on the GPU (other streams, graphs replayed side by side) need a workspace each. */
+LSRM_API size_t lsrm_relpos_workspace_size(const lsrm_relpos_desc* desc);
+LSRM_API lsrm_status lsrm_relpos_workspace_init(const lsrm_relpos_desc* desc, void* ws, size_t ws_bytes, void* stream);
+
+/* Logarithmic buckets (host memory, no GPU work): bucket_of_host int32 [2 D + 1] by clamped distance
+ * delta + D.  Keys at or before the query (delta <= 0) take the first half of the buckets, keys after
+ * it the second half.  With half = n_buckets / 2, e = max(1, half / 2), m = half - e and n = |delta|:
+ * n < e has the bucket n, others min(half - 1, e + floor(m log(n / e) / log(D / e))), evaluated in
+ * whole numbers (n^m >= e^(m-b) D^b), so no distance falls on the wrong side of a border.  n_buckets
+ * even, 2..64; max_distance 1..1023; else LSRM_ERR_INVALID_ARG.  Any other table of bucket ids in
+ * [0, n_buckets) will do for the calls below. */
+LSRM_API lsrm_status lsrm_relpos_log_buckets(int32_t n_buckets, int32_t max_distance, int32_t* bucket_of_host);
+
+/* Forward.  off_q, off_k int32 [S+1] (ascending, within [0, Nq] / [0, Nk]); pos_q int32 [Nq][n_axes],
+ * pos_k int32 [Nk][n_axes] within [-2^29, 2^29]; bucket_of int32 [2 D + 1]; table bf16
+ * [n_axes][n_buckets][Hq] (added to the scaled scores as it is); q bf16 [Nq][Hq][d], k, v bf16
+ * [Nk][Hkv][d], out bf16 [Nq][Hq][d], all 16-byte aligned; lse_or_null fp32 [Nq][Hq].  Rows that
+ * belong to no segment are left as they were.  Segment bounds, positions or bucket ids outside their
+ * ranges raise LSRM_ERR_BOUNDS in the device status (the bounds and distances are clipped, such a
+ * bucket counts as bias 0); nothing outside the arrays is read or written.  Errors:
+ * LSRM_ERR_INVALID_ARG (descriptor, null or misaligned pointer), LSRM_ERR_UNSUPPORTED (head_dim; a
+ * problem of more than 2^31 - 1 CTAs), LSRM_ERR_WORKSPACE (missing, not 256-byte aligned, or fewer
+ * than lsrm_relpos_workspace_size bytes). */
+LSRM_API lsrm_status lsrm_relpos_forward(const lsrm_relpos_desc* desc, const int32_t* off_q, const int32_t* off_k,
+                                         const int32_t* pos_q, const int32_t* pos_k, const int32_t* bucket_of,
+                                         const void* table, const void* q, const void* k, const void* v, void* out,
+                                         float* lse_or_null, void* ws, size_t ws_bytes, void* stream);
+
+/* Backward of L = sum(out * dout): dq bf16 [Nq][Hq][d], dk, dv bf16 [Nk][Hkv][d], dtable bf16
+ * [n_axes][n_buckets][Hq] (all overwritten; dk, dv of keys without queries and the entries of buckets
+ * that no pair has are 0).  out and lse are the forward's; dout bf16 [Nq][Hq][d].  All sums have a
+ * fixed order: results are reproducible bit for bit.  Errors as above. */
+LSRM_API lsrm_status lsrm_relpos_backward(const lsrm_relpos_desc* desc, const int32_t* off_q, const int32_t* off_k,
+                                          const int32_t* pos_q, const int32_t* pos_k, const int32_t* bucket_of,
+                                          const void* table, const void* q, const void* k, const void* v,
+                                          const void* out, const float* lse, const void* dout, void* dq, void* dk,
+                                          void* dv, void* dtable, void* ws, size_t ws_bytes, void* stream);
+
+/* ---- layer norm ----------------------------------------------------------------------------------
+ * Rows of `width` elements (per-head query / key rows, hidden rows), contiguous, of the type dtype
+ * (LSRM_BF16 or LSRM_F32, the type of every void pointer of the call):
+ *   mean = sum(x) / C;  rstd = 1 / sqrt(sum((x - mean)^2) / C + eps);  y = (x - mean) rstd gamma + beta
+ * in fp32.  gamma_or_null / beta_or_null [C] (NULL: 1 / 0); mean_or_null, rstd_or_null fp32 [rows]
+ * (what the backward needs).  y may be x.  rows >= 0, width >= 1, eps >= 0 and finite, else
+ * LSRM_ERR_INVALID_ARG; more than 2^31 - 1 CTAs: LSRM_ERR_UNSUPPORTED. */
+enum { LSRM_BF16 = 0, LSRM_F32 = 1 };
+LSRM_API lsrm_status lsrm_layer_norm_forward(int64_t rows, int32_t width, int32_t dtype, const void* x,
+                                             const void* gamma_or_null, const void* beta_or_null, float eps, void* y,
+                                             float* mean_or_null, float* rstd_or_null, void* stream);
+
+/* Bytes of device workspace of lsrm_layer_norm_backward (any type; nothing in it needs initialising
+ * or is kept between calls); 0 for rows < 0 or width < 1. */
+LSRM_API size_t lsrm_layer_norm_workspace_size(int64_t rows, int32_t width);
+
+/* Backward: with xh = (x - mean) rstd and g = dy gamma, dx = rstd (g - mean(g) - xh mean(g xh)),
+ * dgamma = sum over rows of dy xh, dbeta = sum over rows of dy (summed in fp32 in a fixed order:
+ * reproducible bit for bit; 0 when there are no rows).  dgamma_or_null and dbeta_or_null [C] may be
+ * NULL.  dx may be dy or x.  ws: 256-byte aligned, else LSRM_ERR_WORKSPACE. */
+LSRM_API lsrm_status lsrm_layer_norm_backward(int64_t rows, int32_t width, int32_t dtype, const void* dy, const void* x,
+                                              const void* gamma_or_null, const float* mean, const float* rstd,
+                                              void* dx, void* dgamma_or_null, void* dbeta_or_null, void* ws,
+                                              size_t ws_bytes, void* stream);
+
 /* Diagnostic (no counterpart in the pages): y[i] = 2^x[i] as the attention kernels' FMA-pipe
  * polynomial computes it (the exponentials of the softmax that do not go to the hardware ex2).
  * x and y are device float arrays of n elements (caller-owned); valid for x <= 127, and inputs
