@@ -28,8 +28,17 @@ constexpr int kChunk = 64;  // keys a stage
 constexpr int kStages = 3;
 constexpr float kSlack = 8.0f;
 
+#ifndef RP_NT32
+#define RP_NT32 4
+#define RP_NT64 4
+#define RP_MB32 4
+#define RP_MB64 2
+#endif
 template <int D, int NA, int NW>
 struct FwdCfg {
+  static constexpr int NT = D == 32 ? RP_NT32 : RP_NT64;  // column groups a score tile
+  static constexpr int CW = 2 * NT, kCols = 8 * NT;
+  static constexpr int kMinCtas = (D == 32 ? RP_MB32 : RP_MB64) * 4 / NW;
   static constexpr int kRows = 32 * NW, kThreads = 32 * NW;
   static constexpr int kTile = kChunk * D / 8;  // 16-byte pieces of a K or V stage
   static constexpr size_t kFixed = (size_t)kStages * (2 * kTile * 16 + kChunk * NA * 4);
@@ -56,7 +65,7 @@ __device__ __forceinline__ void move_reference(RowState<MT>& st, float (&o)[MT][
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const float m = quad_max(fmaxf(mx[mt][i], st.m[mt][i]));
-      const float f = st.m[mt][i] == -INFINITY ? 0.0f : fast_exp2((st.m[mt][i] - m) * kLog2e);
+      const float f = st.m[mt][i] == -INFINITY ? 0.0f : ex2((st.m[mt][i] - m) * kLog2e);
       st.m[mt][i] = m;
       st.l[mt][i] *= f;
 #pragma unroll
@@ -68,7 +77,7 @@ __device__ __forceinline__ void move_reference(RowState<MT>& st, float (&o)[MT][
 }
 
 template <int D, int NA, int NW>
-__global__ void __launch_bounds__(32 * NW) rp_fwd_kernel(const Params p) {
+__global__ void __launch_bounds__(32 * NW, FwdCfg<D, NA, NW>::kMinCtas) rp_fwd_kernel(const Params p) {
   using C = FwdCfg<D, NA, NW>;
   extern __shared__ __align__(16) unsigned char smem_raw[];
   uint4* ks = reinterpret_cast<uint4*>(smem_raw);
@@ -95,8 +104,8 @@ __global__ void __launch_bounds__(32 * NW) rp_fwd_kernel(const Params p) {
   auto load = [&](int c) {
     if (c < c1) {
       const int st = c % kStages, k0 = klo + c * kChunk, n = min(kChunk, khi - k0);
-      load_tile<D, kChunk, C::kThreads>(ks + st * C::kTile, p.k, k0, n, p.Hkv, hk, tid);
-      load_tile<D, kChunk, C::kThreads>(vs + st * C::kTile, p.v, k0, n, p.Hkv, hk, tid);
+      load_tile<D, C::CW, kChunk, C::kThreads>(ks + st * C::kTile, p.k, k0, n, p.Hkv, hk, tid);
+      load_tile<D, C::CW, kChunk, C::kThreads>(vs + st * C::kTile, p.v, k0, n, p.Hkv, hk, tid);
       // positions past the end repeat the last key's, so they do not widen the tile's range
       for (int i = tid; i < kChunk * NA; i += C::kThreads)
         cp_async4(ps + st * kChunk * NA + i, p.pos_k + (size_t)(k0 + min(i / NA, n - 1)) * NA + i % NA, true);
@@ -155,123 +164,85 @@ __global__ void __launch_bounds__(32 * NW) rp_fwd_kernel(const Params p) {
     const uint4* vt = vs + (c % kStages) * C::kTile;
     const int* pt = ps + (c % kStages) * kChunk * NA;
 #pragma unroll 1
-    for (int half = 0; half < 2; ++half) {
-      const int kb = half * 32, left = nk - c * kChunk - kb;  // keys from here on
+    for (int kb = 0; kb < kChunk; kb += C::kCols) {
+      const int left = nk - c * kChunk - kb;  // keys from here on
       if (left <= 0 || wrow >= qhi) break;
-      float s[2][4][4];
+      float s[2][C::NT][4];
 #pragma unroll
-      for (int n = 0; n < 4; ++n) {
+      for (int n = 0; n < C::NT; ++n) {
         uint32_t b[D / 8];
-        load_b_rows<D>(b, kt, kb + n * 8, lane);
+        load_b_rows<D, C::CW>(b, kt, kb, n, lane);
 #pragma unroll
         for (int mt = 0; mt < 2; ++mt) {
 #pragma unroll
           for (int e = 0; e < 4; ++e) s[mt][n][e] = 0.0f;
 #pragma unroll
-          for (int d = 0; d < D / 16; ++d) mma_bf16_16816(s[mt][n], qa[mt][d], b + 2 * d);
+          for (int d = 0; d < D / 16; ++d) mma16816(s[mt][n], qa[mt][d], b + 2 * d);
         }
       }
-      if (left < 32) {
+      int mode[NA], one[NA];
 #pragma unroll
-        for (int n = 0; n < 4; ++n)
+      for (int a = 0; a < NA; ++a)
+        mode[a] = axis_mode<NA, C::kCols>(pt + kb * NA + a, q_lo[a], q_hi[a], false, p.maxd, lane, one[a], p.status);
+      float base[2][2];
+      const bool fold = add_bias<NA, 2, C::NT, 1>(s, base, mode, one, pt + kb * NA, lut, top, qp, p.scale, tq);
+      if (left < C::kCols) {
+#pragma unroll
+        for (int n = 0; n < C::NT; ++n)
 #pragma unroll
           for (int e = 0; e < 2; ++e)
-            if (n * 8 + 2 * tq + e >= left)
+            if (tq * C::CW + 2 * n + e >= left)
 #pragma unroll
               for (int mt = 0; mt < 2; ++mt) s[mt][n][e] = s[mt][n][2 + e] = -INFINITY;
       }
-      // distances of the 32 x 32 tile
-      int uni[NA];
-      bool all_uni = true;
-      float ub = 0.0f;
-#pragma unroll
-      for (int a = 0; a < NA; ++a) {
-        const int x = pt[(kb + lane) * NA + a];
-        const int lo = __reduce_min_sync(0xffffffffu, x), hi = __reduce_max_sync(0xffffffffu, x);
-        if (lo < -kPosLimit || hi > kPosLimit) raise_status(p.status, LSRM_ERR_BOUNDS);
-        uni[a] = uniform_index(lo, hi, q_lo[a], q_hi[a], p.maxd);
-        all_uni = all_uni && uni[a] >= 0;
-        if (uni[a] >= 0) ub += lut[a * (top + 1) + uni[a]];
-      }
-      all_uni = all_uni && fabsf(ub) < kFoldLimit;
-      float mul = p.scale, mx[2][2];
-      if (!all_uni) {
-        // scores in natural units with their own bias
-#pragma unroll
-        for (int mt = 0; mt < 2; ++mt)
-#pragma unroll
-          for (int n = 0; n < 4; ++n)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) s[mt][n][e] = fmaf(s[mt][n][e], p.scale, ub);
-#pragma unroll
-        for (int a = 0; a < NA; ++a) {
-          if (uni[a] >= 0) continue;
-          const float* la = lut + a * (top + 1);
-#pragma unroll
-          for (int n = 0; n < 4; ++n)
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              const int x = pt[(kb + n * 8 + 2 * tq + e) * NA + a];
-#pragma unroll
-              for (int mt = 0; mt < 2; ++mt)
-#pragma unroll
-                for (int i = 0; i < 2; ++i) s[mt][n][2 * i + e] += la[clamp_index(x, qp[mt][i][a], top)];
-            }
-        }
-        mul = 1.0f;
-        ub = 0.0f;
-      }
+      float mx[2][2];
 #pragma unroll
       for (int mt = 0; mt < 2; ++mt)
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          float x = fmaxf(s[mt][0][2 * i], s[mt][0][2 * i + 1]);
+          float x = fmax3(s[mt][0][2 * i], s[mt][0][2 * i + 1], s[mt][1][2 * i]);
+          x = fmaxf(x, s[mt][1][2 * i + 1]);
 #pragma unroll
-          for (int n = 1; n < 4; ++n) x = fmaxf(fmaxf(x, s[mt][n][2 * i]), s[mt][n][2 * i + 1]);
-          mx[mt][i] = fmaf(x, mul, ub);
+          for (int n = 2; n < C::NT; ++n) x = fmax3(x, s[mt][n][2 * i], s[mt][n][2 * i + 1]);
+          mx[mt][i] = fold ? fmaf(x, p.scale, base[mt][i]) : x;
         }
       move_reference<2, D / 8>(st, o, mx);
-      // P = exp(t - m): with the bias in the scores the subtraction comes first (exact for equal
-      // scores of any size); with a bias common to the tile everything folds into one multiply-add
-      uint32_t pa[2][2][4];
+      // P = exp(t - m): with the bias in the scores the subtraction comes first (exact for equal scores
+      // of any size); with a bias common to a row everything folds into one multiply-add
+      uint32_t pa[2][C::NT / 2][4];
 #pragma unroll
       for (int mt = 0; mt < 2; ++mt)
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           const float m = st.m[mt][i] == -INFINITY ? 0.0f : st.m[mt][i];
-          float pr[8];
-          if (all_uni) {
-            const float x = p.scale * kLog2e, cst = (ub - m) * kLog2e;
+          const float x = fold ? p.scale * kLog2e : kLog2e, cst = (base[mt][i] - m) * kLog2e;
+          float sum0 = 0.0f, sum1 = 0.0f;
 #pragma unroll
-            for (int n = 0; n < 4; ++n) {
-              pr[2 * n] = fast_exp2(fmaf(s[mt][n][2 * i], x, cst));
-              pr[2 * n + 1] = fast_exp2(fmaf(s[mt][n][2 * i + 1], x, cst));
+          for (int n = 0; n < C::NT; ++n) {
+            float p0 = s[mt][n][2 * i], p1 = s[mt][n][2 * i + 1];
+            if (fold) {
+              ffma2(p0, p1, p0, p1, x, cst);
+            } else {
+              fadd2_acc(p0, p1, -m, -m);
+              fmul2(p0, p1, p0, p1, x, x);
             }
-          } else {
-#pragma unroll
-            for (int n = 0; n < 4; ++n) {
-              pr[2 * n] = fast_exp2((s[mt][n][2 * i] - m) * kLog2e);
-              pr[2 * n + 1] = fast_exp2((s[mt][n][2 * i + 1] - m) * kLog2e);
-            }
+            p0 = ex2(p0);
+            p1 = ex2(p1);
+            fadd2_acc(sum0, sum1, p0, p1);
+            pa[mt][n >> 1][(n & 1) * 2 + i] = pack2(p0, p1);
           }
-          float sum = 0.0f;
-#pragma unroll
-          for (int n = 0; n < 4; ++n) {
-            sum += pr[2 * n] + pr[2 * n + 1];
-            pa[mt][n >> 1][(n & 1) * 2 + i] = pack_bf16x2(pr[2 * n], pr[2 * n + 1]);
-          }
-          st.l[mt][i] += sum;
+          st.l[mt][i] += sum0 + sum1;
         }
 #pragma unroll
-      for (int j = 0; j < 2; ++j)
+      for (int j = 0; j < C::NT / 2; ++j)
 #pragma unroll
         for (int dc = 0; dc < D / 8; dc += 2) {
           uint32_t b[4];
-          load_b_cols<D>(b, vt, kb + j * 16, dc, lane);
+          load_b_cols<D, C::CW>(b, vt, kb, j, dc, lane);
 #pragma unroll
           for (int mt = 0; mt < 2; ++mt) {
-            mma_bf16_16816(o[mt][dc], pa[mt][j], b);
-            mma_bf16_16816(o[mt][dc + 1], pa[mt][j], b + 2);
+            mma16816(o[mt][dc], pa[mt][j], b);
+            mma16816(o[mt][dc + 1], pa[mt][j], b + 2);
           }
         }
     }
@@ -291,7 +262,7 @@ __global__ void __launch_bounds__(32 * NW) rp_fwd_kernel(const Params p) {
 #pragma unroll
         for (int n = 0; n < D / 8; ++n)
           *reinterpret_cast<uint32_t*>(p.out + at * D + n * 8 + 2 * tq) =
-              pack_bf16x2(o[mt][n][2 * i] * inv, o[mt][n][2 * i + 1] * inv);
+              pack2(o[mt][n][2 * i] * inv, o[mt][n][2 * i + 1] * inv);
         if (tq == 0 && p.lse != nullptr) p.lse[at] = lse;
       } else {
         const size_t pat = (size_t)split * p.Nq * p.Hq + at;
@@ -351,8 +322,8 @@ __global__ void __launch_bounds__(kFewThreads) rp_few_kernel(const Params p) {
   auto load = [&](int c) {
     if (c < c1) {
       const int st = ((c - c0) / kFewWarps) % kStages, k0 = klo + c * kFewKeys, n = min(kFewKeys, khi - k0);
-      load_tile<D, kFewKeys, 32>(ring + st * 2 * C::kTile, p.k, k0, n, p.Hkv, hk, lane);
-      load_tile<D, kFewKeys, 32>(ring + (st * 2 + 1) * C::kTile, p.v, k0, n, p.Hkv, hk, lane);
+      load_tile<D, 8, kFewKeys, 32>(ring + st * 2 * C::kTile, p.k, k0, n, p.Hkv, hk, lane);
+      load_tile<D, 8, kFewKeys, 32>(ring + (st * 2 + 1) * C::kTile, p.v, k0, n, p.Hkv, hk, lane);
 #pragma unroll
       for (int i = lane; i < kFewKeys * NA; i += 32)
         cp_async4(ps + st * kFewKeys * NA + i, p.pos_k + (size_t)(k0 + min(i / NA, n - 1)) * NA + i % NA, true);
@@ -427,11 +398,11 @@ __global__ void __launch_bounds__(kFewThreads) rp_few_kernel(const Params p) {
 #pragma unroll
     for (int n = 0; n < 4; ++n) {
       uint32_t b[D / 8];
-      load_b_rows<D>(b, kt, n * 8, lane);
+      load_b_rows<D, 8>(b, kt, 0, n, lane);
 #pragma unroll
       for (int e = 0; e < 4; ++e) s[n][e] = 0.0f;
 #pragma unroll
-      for (int d = 0; d < D / 16; ++d) mma_bf16_16816(s[n], qa[d], b + 2 * d);
+      for (int d = 0; d < D / 16; ++d) mma16816(s[n], qa[d], b + 2 * d);
     }
     float ub[2] = {0.0f, 0.0f};
     int uni[NA];
@@ -440,7 +411,8 @@ __global__ void __launch_bounds__(kFewThreads) rp_few_kernel(const Params p) {
       const int x = pt[lane * NA + a];
       const int lo = __reduce_min_sync(0xffffffffu, x), hi = __reduce_max_sync(0xffffffffu, x);
       if (lo < -kPosLimit || hi > kPosLimit) raise_status(p.status, LSRM_ERR_BOUNDS);
-      uni[a] = uniform_index(lo, hi, q_lo[a], q_hi[a], p.maxd);
+      const int near = clamp_index(lo - q_hi[a], p.maxd, top), far = clamp_index(hi - q_lo[a], p.maxd, top);
+      uni[a] = near == far ? near : -1;
       if (uni[a] >= 0) {
         ub[0] += bias_at(a, uni[a], hh[0]);
         ub[1] += bias_at(a, uni[a], hh[1]);
@@ -457,7 +429,7 @@ __global__ void __launch_bounds__(kFewThreads) rp_few_kernel(const Params p) {
       for (int n = 0; n < 4; ++n)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          const int x = pt[(n * 8 + 2 * tq + e) * NA + a];
+          const int x = pt[(tq * 8 + 2 * n + e) * NA + a];
 #pragma unroll
           for (int i = 0; i < 2; ++i) s[n][2 * i + e] += bias_at(a, clamp_index(x, qp[i][a], top), hh[i]);
         }
@@ -467,7 +439,7 @@ __global__ void __launch_bounds__(kFewThreads) rp_few_kernel(const Params p) {
       for (int n = 0; n < 4; ++n)
 #pragma unroll
         for (int e = 0; e < 2; ++e)
-          if (n * 8 + 2 * tq + e >= left) s[n][e] = s[n][2 + e] = -INFINITY;
+          if (tq * 8 + 2 * n + e >= left) s[n][e] = s[n][2 + e] = -INFINITY;
     }
     float mx[1][2];
 #pragma unroll
@@ -485,9 +457,9 @@ __global__ void __launch_bounds__(kFewThreads) rp_few_kernel(const Params p) {
       float sum = 0.0f;
 #pragma unroll
       for (int n = 0; n < 4; ++n) {
-        const float a = fast_exp2((s[n][2 * i] - m) * kLog2e), b = fast_exp2((s[n][2 * i + 1] - m) * kLog2e);
+        const float a = ex2((s[n][2 * i] - m) * kLog2e), b = ex2((s[n][2 * i + 1] - m) * kLog2e);
         sum += a + b;
-        pa[n >> 1][(n & 1) * 2 + i] = pack_bf16x2(a, b);
+        pa[n >> 1][(n & 1) * 2 + i] = pack2(a, b);
       }
       st.l[0][i] += sum;
     }
@@ -496,9 +468,9 @@ __global__ void __launch_bounds__(kFewThreads) rp_few_kernel(const Params p) {
 #pragma unroll
       for (int dc = 0; dc < D / 8; dc += 2) {
         uint32_t b[4];
-        load_b_cols<D>(b, vt, j * 16, dc, lane);
-        mma_bf16_16816(o[0][dc], pa[j], b);
-        mma_bf16_16816(o[0][dc + 1], pa[j], b + 2);
+        load_b_cols<D, 8>(b, vt, 0, j, dc, lane);
+        mma16816(o[0][dc], pa[j], b);
+        mma16816(o[0][dc + 1], pa[j], b + 2);
       }
     __syncwarp();
   }
@@ -532,7 +504,7 @@ __global__ void __launch_bounds__(kFewThreads) rp_few_kernel(const Params p) {
 #pragma unroll
     for (int w = 0; w < kFewWarps; ++w) {
       const float mw = jm[w * 16 + r];
-      const float f = mw == -INFINITY && jl[w * 16 + r] == 0.0f ? 0.0f : fast_exp2((mw - m) * kLog2e);
+      const float f = mw == -INFINITY && jl[w * 16 + r] == 0.0f ? 0.0f : ex2((mw - m) * kLog2e);
       l = fmaf(f, jl[w * 16 + r], l);
       x = fmaf(f, jo[(w * 16 + r) * D + d], x);
       y = fmaf(f, jo[(w * 16 + r) * D + d + 1], y);
@@ -540,7 +512,7 @@ __global__ void __launch_bounds__(kFewThreads) rp_few_kernel(const Params p) {
     const float inv = l == 0.0f ? 0.0f : 1.0f / l, lse = l == 0.0f ? -INFINITY : m + logf(l);
     const size_t to = (size_t)(row0 + t) * p.Hq + h0 + head;
     if (p.splits == 1) {
-      *reinterpret_cast<uint32_t*>(p.out + to * D + d) = pack_bf16x2(x * inv, y * inv);
+      *reinterpret_cast<uint32_t*>(p.out + to * D + d) = pack2(x * inv, y * inv);
       if (d == 0 && p.lse != nullptr) p.lse[to] = lse;
     } else {
       const size_t pat = (size_t)split * p.Nq * p.Hq + to;
@@ -575,7 +547,7 @@ __global__ void __launch_bounds__(kJoinThreads) rp_join_kernel(const Params p) {
     for (int s = 0; s < p.splits; ++s) {
       const float2 ml = p.ml_part[s * stride + at];
       if (ml.y == 0.0f) continue;  // no key
-      const float f = ml.y * fast_exp2((ml.x - m) * kLog2e);
+      const float f = ml.y * ex2((ml.x - m) * kLog2e);
       const float4 x = *reinterpret_cast<const float4*>(p.o_part + (s * stride + at) * D + d);
       l += f;
       o.x = fmaf(f, x.x, o.x);
@@ -585,7 +557,7 @@ __global__ void __launch_bounds__(kJoinThreads) rp_join_kernel(const Params p) {
     }
     const float inv = l == 0.0f ? 0.0f : 1.0f / l;
     *reinterpret_cast<uint2*>(p.out + at * D + d) =
-        make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
+        make_uint2(pack2(o.x * inv, o.y * inv), pack2(o.z * inv, o.w * inv));
     if (d == 0 && p.lse != nullptr) p.lse[at] = l == 0.0f ? -INFINITY : m + logf(l);
   }
 }
@@ -608,6 +580,8 @@ static lsrm_status run_fwd(const Params& p, long long ctas, cudaStream_t s) {
   return launched();
 }
 
+lsrm_status launch_fwd_tc(const Params& p, int D, int NA, long long ctas, cudaStream_t s);
+
 template <int D, int NA>
 static lsrm_status run_shape(const Params& p, const FwdPlan& f, cudaStream_t s) {
   lsrm_status st;
@@ -616,6 +590,8 @@ static lsrm_status run_shape(const Params& p, const FwdPlan& f, cudaStream_t s) 
     if (!allow_smem(rp_few_kernel<D, NA>, bytes)) return LSRM_ERR_CUDA;
     rp_few_kernel<D, NA><<<(unsigned)f.ctas, kFewThreads, bytes, s>>>(p);
     st = launched();
+  } else if (f.rows == 256) {
+    st = launch_fwd_tc(p, D, NA, f.ctas, s);
   } else if (f.rows == 64) {
     st = run_fwd<D, NA, 2>(p, f.ctas, s);
   } else {

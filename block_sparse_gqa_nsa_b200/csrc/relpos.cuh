@@ -11,7 +11,7 @@
 
 #include <climits>
 
-#include "lsrm_common.cuh"
+#include "tc_ptx.cuh"
 
 namespace lsrm {
 namespace rp {
@@ -20,8 +20,35 @@ constexpr int kPosLimit = 1 << 29;  // positions lie in [-2^29, 2^29], so differ
 constexpr int kMaxBuckets = 64;
 constexpr int kMaxDistance = 1023;
 constexpr int kMaxAxes = 3;
+using tc::fadd2_acc;
+using tc::ffma2;
+using tc::fmax3;
+using tc::fmul2;
+
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
+
+// Arithmetic without side effects, so not `asm volatile`: volatile statements keep their order, and a
+// kernel that interleaves exponentials, packing and products would wait out each one's latency in turn.
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;\n" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;\n" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+__device__ __forceinline__ void mma16816(float* c, const uint32_t* a, const uint32_t* b) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+      "{%0,%1,%2,%3};\n"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]));
+}
+
+// In a rarely taken branch: keeps it a branch, where the compiler would rather do both sides and select
+__device__ __forceinline__ void keep_branch() { asm volatile("" ::: "memory"); }
 
 struct Params {
   const int32_t* off_q;
@@ -43,7 +70,7 @@ struct Params {
   uint16_t* dv;
   uint16_t* dtable;
   float* delta;  // backward: Delta per (query, head)
-  float* tab_part;  // backward: table gradient per (query tile, head)
+  float* tab_part;  // backward: table gradient per (key tile, part of its queries, head)
   float* kv_part;   // backward: dK / dV per split
   float* corr;      // backward: log2 of what exp(t - lse) sums to per (query, head), 0 for all but huge |lse|
   float* o_part;    // forward: output per key split, and its softmax reference and sum
@@ -66,16 +93,18 @@ __device__ __forceinline__ void seg_bounds(const int32_t* off, int s, int n, int
 
 // Tiles of R rows cut from the segments, numbered without a prefix sum: segment s starts at tile
 // off[s] / R + s, which leaves it at least ceil(len / R) numbers, and all numbers are below
-// n / R + segments.  The segment of a number is found by bisection; numbers behind a segment's last
-// tile are empty.
+// n / R + segments.  The segment of a number is the last one that starts at or before it, found by a
+// search with 32 probes a round (the warp's lanes), so 1000 segments take two dependent reads; whole
+// warps only.  Numbers behind a segment's last tile are empty.
 __device__ __forceinline__ int seg_of_tile(const int32_t* off, int S, int n, int R, int tile, int& first) {
-  int lo = 0, hi = S - 1;  // the last segment that starts at or before the tile
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (min(max(off[mid], 0), n) / R + mid <= tile)
-      lo = mid;
-    else
-      hi = mid - 1;
+  const int lane = threadIdx.x & 31;
+  int lo = 0, len = S;  // the segment lies in [lo, lo + len)
+  while (len > 1) {
+    const int step = (len + 31) >> 5, mid = lo + lane * step;
+    const bool before = lane * step < len && min(max(off[mid], 0), n) / R + mid <= tile;
+    const int k = max(31 - __clz(__ballot_sync(0xffffffffu, before)), 0);  // the last probe at or before it
+    len = min(step, lo + len - (lo + k * step));
+    lo += k * step;
   }
   first = min(max(off[lo], 0), n) / R + lo;
   return lo;
@@ -105,15 +134,23 @@ __device__ __forceinline__ void fill_lut(const Params& p, float* lut, int h, int
 __device__ __forceinline__ int clamp_index(int x, int y, int top) { return __viaddmin_s32_relu(x, y, top); }
 
 // ---- tiles in shared memory ----
-// rows of D bf16 in 16-byte pieces, swizzled so that the eight rows of an 8x8 matrix lie in
-// different banks (64-byte rows: two rows fill the 32 banks; 128-byte rows: one)
-template <int D>
+// A score tile of 8 NT columns: the accumulator layout gives the lane with tq = lane % 4 the columns
+// 2 tq, 2 tq + 1 of each of the NT groups of 8.  Which stored row a column stands for is free (the
+// softmax and the sums do not care), so column 2 tq + e of group n is stored row tq CW + 2 n + e with
+// CW = 2 NT: a lane then holds CW consecutive tokens, whose positions often are the same on an axis
+// (one look-up for all of them) and load as vectors.
+//
+// Rows of D bf16 lie in 16-byte pieces, swizzled so that the eight rows of one 8x8 matrix (0, 1, CW,
+// CW + 1, 2 CW, .. behind 2 n) fall into different banks.
+template <int D, int CW>
 __device__ __forceinline__ int piece(int row, int c) {
-  return D == 32 ? row * 4 + (c ^ ((row >> 1) & 3)) : row * 8 + (c ^ (row & 7));
+  constexpr int kShift = CW == 16 ? 4 : 3;
+  static_assert(CW == 16 || CW == 8, "64 or 32 columns a tile");
+  return D == 32 ? row * 4 + (c ^ ((row >> kShift) & 3)) : row * 8 + (c ^ ((row & 1) | ((row >> (kShift - 1)) & 6)));
 }
 
-// rows [r0, r0 + n) of a [tokens][heads][D] tensor, head h; rows past n_valid are filled with zeros
-template <int D, int ROWS, int NT>
+// rows [r0, r0 + n_valid) of a [tokens][heads][D] tensor, head h; rows past n_valid are filled with zeros
+template <int D, int CW, int ROWS, int NT>
 __device__ __forceinline__ void load_tile(uint4* dst, const uint16_t* src, int r0, int n_valid, int heads, int h,
                                           int tid) {
   constexpr int kPieces = D / 8;
@@ -121,7 +158,7 @@ __device__ __forceinline__ void load_tile(uint4* dst, const uint16_t* src, int r
   for (int i = tid; i < ROWS * kPieces; i += NT) {
     const int r = i / kPieces, c = i % kPieces;
     const bool ok = r < n_valid;
-    cp_async16(dst + piece<D>(r, c), src + ((size_t)(r0 + (ok ? r : 0)) * heads + h) * D + c * 8, ok);
+    cp_async16(dst + piece<D, CW>(r, c), src + ((size_t)(r0 + (ok ? r : 0)) * heads + h) * D + c * 8, ok);
   }
 }
 __device__ __forceinline__ void cp_async4(void* smem, const void* gmem, bool pred) {
@@ -129,20 +166,21 @@ __device__ __forceinline__ void cp_async4(void* smem, const void* gmem, bool pre
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;\n" ::"r"(smem_u32(smem)), "l"(gmem), "r"(n));
 }
 
-// B operand for X Y^T: the 8 rows at `row` (n) by all of D (k): b[2 * ks], b[2 * ks + 1] per k step
-template <int D>
-__device__ __forceinline__ void load_b_rows(uint32_t* b, const uint4* tile, int row, int lane) {
+// B operand for X Y^T: column group n (8 columns) by all of D (k): b[2 * ks], b[2 * ks + 1] per k step
+template <int D, int CW>
+__device__ __forceinline__ void load_b_rows(uint32_t* b, const uint4* tile, int row0, int n, int lane) {
+  const int row = row0 + ((lane & 7) >> 1) * CW + 2 * n + (lane & 1);
 #pragma unroll
   for (int c = 0; c < D / 8; c += 4) {
-    const uint32_t a = smem_u32(tile + piece<D>(row + (lane & 7), c + (lane >> 3)));
+    const uint32_t a = smem_u32(tile + piece<D, CW>(row, c + (lane >> 3)));
     ldmatrix_x4(b[c], b[c + 1], b[c + 2], b[c + 3], a);
   }
 }
-// B operand for P Y: the 16 rows at `row` (k) by columns [8 c, 8 c + 16) (two n tiles)
-template <int D>
-__device__ __forceinline__ void load_b_cols(uint32_t* b, const uint4* tile, int row, int c, int lane) {
-  const uint32_t a = smem_u32(tile + piece<D>(row + (lane & 15), c + (lane >> 4)));
-  ldmatrix_x4_trans(b[0], b[1], b[2], b[3], a);
+// B operand for P Y: column groups 2 j and 2 j + 1 (16 rows of Y, k) by columns [8 c, 8 c + 16) of Y
+template <int D, int CW>
+__device__ __forceinline__ void load_b_cols(uint32_t* b, const uint4* tile, int row0, int j, int c, int lane) {
+  const int row = row0 + ((lane & 7) >> 1) * CW + 2 * (2 * j + ((lane >> 3) & 1)) + (lane & 1);
+  ldmatrix_x4_trans(b[0], b[1], b[2], b[3], smem_u32(tile + piece<D, CW>(row, c + (lane >> 4))));
 }
 // A operand straight from global memory: rows g and g + 8 of a 16-row tile; row pointers may be null
 template <int D>
@@ -167,14 +205,33 @@ __device__ __forceinline__ float quad_max(float v) {
   return fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 2));
 }
 
-// ---- distances that are the same for a whole tile ----
-// Index into the bias table when every (row, column) pair of the tile has the same clamped distance
-// on this axis, else -1: all pairs at or past +-maxd, or both position ranges single values.
-__device__ __forceinline__ int uniform_index(int k_lo, int k_hi, int q_lo, int q_hi, int maxd) {
-  const int lo = clamp_index(k_lo - q_hi, maxd, 2 * maxd), hi = clamp_index(k_hi - q_lo, maxd, 2 * maxd);
-  return lo == hi ? lo : -1;
-}
+// ---- what a tile's distances have in common ----
+// Per axis, for a warp's tile of 32 or 64 columns (wide = 64) whose column positions are xs[col * NA]:
+//   kOne   every (row, column) pair has one clamped distance (all pairs at or past +-maxd, or single
+//          positions): one look-up for the tile;
+//   kLane  each lane's CW columns have one position: one look-up per row;
+//   kFour  aligned runs of four columns have one position: one look-up per row and run;
+//   kEach  a look-up per pair.
+// Lattice orders (bricks, patches, frames) make the slow axes kLane or kFour; distances past
+// max_distance make kOne.  The tests cost about 20 instructions a tile and axis.
+enum : int { kOne = 0, kLane = 1, kFour = 2, kEach = 3 };
 
+template <int NA, int COLS>
+__device__ __forceinline__ int axis_mode(const int* xs, int row_lo, int row_hi, bool rows_are_keys, int maxd, int lane,
+                                         int& one, uint32_t* status) {
+  constexpr int CW = COLS / 4;
+  const int x0 = xs[lane * NA], x1 = COLS == 64 ? xs[(lane + 32) * NA] : x0;
+  const int lo = __reduce_min_sync(0xffffffffu, min(x0, x1)), hi = __reduce_max_sync(0xffffffffu, max(x0, x1));
+  if (lo < -kPosLimit || hi > kPosLimit) raise_status(status, LSRM_ERR_BOUNDS);
+  const int a = clamp_index(rows_are_keys ? row_lo - hi : lo - row_hi, maxd, 2 * maxd);
+  const int b = clamp_index(rows_are_keys ? row_hi - lo : hi - row_lo, maxd, 2 * maxd);
+  one = a;
+  if (a == b) return kOne;
+  uint32_t same = __ballot_sync(0xffffffffu, x0 == __shfl_down_sync(0xffffffffu, x0, 1));
+  if (COLS == 64) same &= __ballot_sync(0xffffffffu, x1 == __shfl_down_sync(0xffffffffu, x1, 1));
+  constexpr uint32_t kLaneMask = CW == 16 ? 0x7fff7fffu : 0x7f7f7f7fu, kFourMask = 0x77777777u;
+  return (same & kLaneMask) == kLaneMask ? kLane : (same & kFourMask) == kFourMask ? kFour : kEach;
+}
 
 // A bias common to a tile folds into the exponent's multiply-add only while it is small beside
 // fp32's spacing: past this a score is added to it first, so that scores the addition swallows (a
@@ -183,19 +240,97 @@ __device__ __forceinline__ int uniform_index(int k_lo, int k_hi, int q_lo, int q
 // the row's sum, so the backward normalises such rows anew.
 constexpr float kFoldLimit = 1e4f;
 
+// The bias of a lane's MT x 2 rows by CW columns: what is constant per row goes to base, the rest is
+// added to the scores s, which become s * scale + bias when there is a rest (or when base is too
+// large to fold).  Returns whether base holds it all.  SIGN: column positions count up (+1, columns are
+// keys: rowc = maxd - pos_q) or down (-1, columns are queries: rowc = maxd + pos_k).
+template <int NA, int MT, int NT, int SIGN>
+__device__ __forceinline__ bool add_bias(float (&s)[MT][NT][4], float (&base)[MT][2], const int (&mode)[NA],
+                                         const int (&one)[NA], const int* xs, const float* lut, int top,
+                                         const int (&rowc)[MT][2][NA], float scale, int tq) {
+  constexpr int CW = 2 * NT;
+  const int* mine = xs + tq * CW * NA;
+  int worst = kOne;
+  float ub = 0.0f;
+#pragma unroll
+  for (int a = 0; a < NA; ++a) {
+    worst = max(worst, mode[a]);
+    if (mode[a] == kOne) ub += lut[a * (top + 1) + one[a]];
+  }
+  bool small = fabsf(ub) < kFoldLimit;
+#pragma unroll
+  for (int mt = 0; mt < MT; ++mt) base[mt][0] = base[mt][1] = ub;
+  if (worst == kOne && small) return true;
+#pragma unroll
+  for (int a = 0; a < NA; ++a) {
+    if (mode[a] != kLane) continue;
+    const int x = SIGN * mine[a];
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) base[mt][i] += lut[a * (top + 1) + clamp_index(x, rowc[mt][i][a], top)];
+  }
+  if (worst <= kLane) {
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) small = small && fabsf(base[mt][0]) < kFoldLimit && fabsf(base[mt][1]) < kFoldLimit;
+    if (__all_sync(0xffffffffu, small)) return true;
+  }
+#pragma unroll
+  for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+        ffma2(s[mt][n][2 * i], s[mt][n][2 * i + 1], s[mt][n][2 * i], s[mt][n][2 * i + 1], scale, base[mt][i]);
+#pragma unroll
+  for (int a = 0; a < NA; ++a) {
+    const float* la = lut + a * (top + 1);
+    if (mode[a] == kFour) {
+#pragma unroll
+      for (int r = 0; r < NT / 2; ++r) {
+        const int x = SIGN * mine[4 * r * NA + a];
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const float b = la[clamp_index(x, rowc[mt][i][a], top)];
+            fadd2_acc(s[mt][2 * r][2 * i], s[mt][2 * r][2 * i + 1], b, b);
+            fadd2_acc(s[mt][2 * r + 1][2 * i], s[mt][2 * r + 1][2 * i + 1], b, b);
+          }
+      }
+    } else if (mode[a] == kEach) {
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        const int x0 = SIGN * mine[2 * n * NA + a], x1 = SIGN * mine[(2 * n + 1) * NA + a];
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+            fadd2_acc(s[mt][n][2 * i], s[mt][n][2 * i + 1], la[clamp_index(x0, rowc[mt][i][a], top)],
+                      la[clamp_index(x1, rowc[mt][i][a], top)]);
+      }
+    }
+  }
+  return false;
+}
+
 // ---- launch plans and the workspace (host) ----
 constexpr int kSms = 148;
 
 struct FwdPlan {
-  int rows;  // queries a CTA: 128, 64, or 0 for the kernel of few rows
+  int rows;  // queries a CTA: 256 (tensor-memory kernel), 128, 64, or 0 for the kernel of few rows
   int splits;
   long long ctas;
 };
 struct BwdPlan {
-  int splits;  // of the (head, query chunk) loop of the key pass
+  bool exact;   // short segments: 64 queries a CTA and the exact Delta in dq as well
+  int kv_rows;  // keys a CTA: 64 or 128
+  int splits;   // of the key pass over heads and query chunks: a divisor of G, or a multiple of it
+  int g;
   long long dq_tiles, kv_tiles;
+  int parts() const { return splits > g ? splits / g : 1; }  // table sums per (key tile, head)
 };
-constexpr int kBwdRows = 64;
+constexpr int kExactKeys = 256;
 
 inline FwdPlan fwd_plan(const lsrm_relpos_desc& d) {
   FwdPlan f{};
@@ -209,12 +344,12 @@ inline FwdPlan fwd_plan(const lsrm_relpos_desc& d) {
     busy = ((mean_q + t - 1) / t) * (Nq < S ? Nq : S) * d.n_kv_heads * hgroups;
     chunks = (mean_k + 127) / 128;  // four warps of 32 keys
   } else {
-    f.rows = mean_q <= 64 ? 64 : 128;
+    f.rows = mean_q <= 64 ? 64 : mean_q <= 96 ? 128 : 256;
     f.ctas = (Nq / f.rows + S) * d.n_q_heads;
     busy = ((mean_q + f.rows - 1) / f.rows) * S * d.n_q_heads;
     chunks = (mean_k + 63) / 64;
   }
-  const long long want = 3 * kSms, most = chunks / 4;
+  const long long want = (f.rows == 256 ? 2 : 3) * kSms, most = chunks / 4;
   long long sp = busy > 0 && busy < want ? want / busy : 1;
   if (sp > most) sp = most;
   if (sp > 64) sp = 64;
@@ -228,19 +363,24 @@ inline BwdPlan bwd_plan(const lsrm_relpos_desc& d) {
   BwdPlan b{};
   const long long S = d.n_segs, G = d.n_q_heads / d.n_kv_heads;
   const long long mean_q = (d.n_q_tokens + S - 1) / S, mean_k = (d.n_k_tokens + S - 1) / S;
-  b.dq_tiles = d.n_q_tokens / kBwdRows + S;
-  b.kv_tiles = d.n_k_tokens / kBwdRows + S;
-  const long long busy = ((mean_k + kBwdRows - 1) / kBwdRows) * S * d.n_kv_heads;
-  const long long qchunks = (mean_q + 63) / 64, most = G * (qchunks > 0 ? qchunks : 1);
+  b.g = (int)G;
+  b.exact = mean_k <= kExactKeys || mean_q <= 64;
+  b.kv_rows = d.head_dim == 32 && mean_k > 64 ? 128 : 64;
+  const int q_rows = b.exact ? 64 : 128;
+  b.dq_tiles = d.n_q_tokens / q_rows + S;
+  b.kv_tiles = d.n_k_tokens / b.kv_rows + S;
+  const long long busy = ((mean_k + b.kv_rows - 1) / b.kv_rows) * S * d.n_kv_heads;
+  const long long qchunks = (mean_q + 63) / 64;
   long long sp = busy > 0 ? (3 * kSms + busy - 1) / busy : 1;
+  if (sp > 64 * G) sp = 64 * G;
   if (sp < G) {
     while (G % sp) ++sp;  // whole heads, evenly
   } else {
-    sp = (sp + G - 1) / G * G;
+    sp = sp / G;          // chunks of one head
+    if (sp > qchunks) sp = qchunks;
+    sp = (sp < 1 ? 1 : sp) * G;
   }
-  if (sp > most) sp = most;
-  if (sp > 128) sp = 128;
-  b.splits = (int)(sp < 1 ? 1 : sp);
+  b.splits = (int)sp;
   return b;
 }
 
@@ -262,7 +402,7 @@ inline Ws ws_layout(const lsrm_relpos_desc& d) {
   w.delta = o;
   w.corr = up256(w.delta + rows * 4);
   w.tab_part = up256(w.corr + rows * 4);
-  w.kv_part = up256(w.tab_part + (size_t)b.dq_tiles * d.n_q_heads * d.n_axes * d.n_buckets * 4);
+  w.kv_part = up256(w.tab_part + (size_t)b.kv_tiles * b.parts() * d.n_q_heads * d.n_axes * d.n_buckets * 4);
   const size_t kv = b.splits > 1 ? (size_t)b.splits * 2 * d.n_k_tokens * d.n_kv_heads * D : 0;
   const size_t bwd = up256(w.kv_part + kv * 4);
   w.total = fwd > bwd ? fwd : bwd;

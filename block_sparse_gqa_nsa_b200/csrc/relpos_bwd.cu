@@ -1,48 +1,58 @@
 // Backward of the attention with a learned relative position bias by buckets (relpos.cuh has the
-// forward).  With P = exp(t - lse), dP = dO V^T, Delta = sum_d dO o, dS = P (dP - Delta):
+// forward).  With P = exp(t - lse), dP = dO V^T, Delta = sum_j P dP, dS = P (dP - Delta):
 //   dq = scale dS K,  dk = scale sum_heads dS^T q,  dv = sum_heads P^T dO,
 //   dtable[a][b][h] = sum over the pairs (i, j) of head h with bucket_of[delta_a + D] = b of dS_ij
 //
 // Two passes over the scores, each with its own tile of rows kept in registers from the scores to
 // the products (mma.sync: P and dS go from the accumulator layout to the operand layout in place):
-//   * rp_dq_kernel: 64 queries of one head a CTA, keys streaming: dq and the table's gradient.
-//   * rp_dkv_kernel: 64 keys of one KV head a CTA, the queries of its heads streaming: dk, dv.
+//   * rp_dq_kernel: queries of one head a CTA, keys streaming: dq, and Delta for the other pass;
+//   * rp_dkv_kernel: keys of one KV head a CTA, the queries of its heads streaming: dk, dv and the
+//     table's gradient.
+//
+// Delta.  sum_d dO o with the forward's out is off by that output's bf16 rounding, which a gradient
+// that adds up a whole row of dS (the table's) or few keys (short segments) would show.  With D~ that
+// value, the row sum of P (dP - D~) is exactly Delta - D~, so the dq pass adds up what it computes
+// anyway and hands the exact Delta to the key pass.  Its own dq takes the correction - (Delta - D~) P K
+// where segments are short (kExact: one more product); past kExactKeys keys it is below dq's rounding.
 //
 // The table's gradient: every thread has its own column of NA x buckets sums in shared memory, so
 // the sums need no atomics; a tile that lies on one distance adds its sum once (kept in a register
-// until the bucket changes), other tiles add score by score.  CTAs write their sums per (query tile,
-// head) and rp_table_kernel adds them in a fixed order.  dk and dv of a key are summed over the heads
-// of its group inside a CTA, or over a fixed number of splits joined by rp_dkv_join_kernel in order.
-// Nothing depends on scheduling: a second run gives the same bits.
+// until the bucket changes), runs of queries on one position add their sums, others score by score.
+// CTAs write their sums per (key tile, head) and rp_table_kernel adds them in a fixed order.  dk and dv
+// of a key are summed over the heads of its group inside a CTA, or over a fixed number of splits joined
+// by rp_dkv_join_kernel in order.  Nothing depends on scheduling: a second run gives the same bits.
 //
 // Sums are fp32.  P and dS are rounded to bf16 as operands of the products whose other operand is
-// bf16; dtable adds the unrounded dS.
+// bf16; dtable and Delta add the unrounded values.
 #include "relpos.cuh"
 
 namespace lsrm {
 namespace rp {
 
 constexpr int kBThreads = 128, kBChunk = 64, kBStages = 3;
+constexpr int kBNT = 4, kBCW = 8, kBCols = 32;  // columns of a score tile
 
 template <int D, int NA>
 struct BwdCfg {
   static constexpr int kTile = kBChunk * D / 8;
   static constexpr size_t kRing = (size_t)kBStages * (2 * kTile * 16 + kBChunk * NA * 4);
   __host__ __device__ static size_t lut(int maxd) { return (((size_t)NA * (2 * maxd + 1) * 4) + 15) & ~(size_t)15; }
-  static size_t smem_dq(int maxd, int nb) {
-    return kRing + lut(maxd) + (size_t)NA * nb * kBThreads * 4 + (((size_t)2 * maxd + 1 + 15) & ~(size_t)15);
+  static size_t smem_dq(int maxd) { return kRing + lut(maxd); }
+  static size_t smem_dkv(int maxd, int nb) {
+    return kRing + (size_t)kBStages * kBChunk * 12 + lut(maxd) + (size_t)NA * nb * kBThreads * 4 +
+           (((size_t)2 * maxd + 1 + 15) & ~(size_t)15);
   }
-  static size_t smem_dkv(int maxd) { return kRing + (size_t)kBStages * kBChunk * 12 + lut(maxd); }
 };
 
 // Rows whose |LSE| is so large that fp32 lost the logarithm of their sum beside the largest score
 // (every key masked by a huge finite bias): corr = log2 sum_j exp(t - lse), a row at a time, lanes over
-// keys.  The warp's rows are wrow .. wrow + 15; lane (g, .) holds the LSE of rows g and g + 8.
+// keys.  The tile's rows are wrow .. wrow + 15; lane (g, .) holds the LSE of rows g and g + 8.
 template <int D, int NA>
-__device__ __noinline__ void huge_rows(const Params& p, const float* lut, const float* lse, float* corr, int wrow,
-                                       int h, int hk, int klo, int khi, int lane) {
+__device__ __noinline__ float2 huge_rows(const Params& p, const float* lut, float lse0, float lse1, int wrow, int h,
+                                         int hk, int klo, int khi, int lane) {
+  float2 corr = make_float2(0.0f, 0.0f);
   for (int r = 0; r < 16; ++r) {
-    const float l = __shfl_sync(0xffffffffu, lse[r >> 3], (r & 7) * 4);
+    const float l = __shfl_sync(0xffffffffu, r < 8 ? lse0 : lse1, (r & 7) * 4);
     if (!(fabsf(l) >= kFoldLimit) || l == INFINITY) continue;
     const size_t row = wrow + r;
     const uint16_t* q = p.q + (row * p.Hq + h) * D;
@@ -55,43 +65,39 @@ __device__ __noinline__ void huge_rows(const Params& p, const float* lut, const 
       for (int a = 0; a < NA; ++a)
         t += lut[a * (2 * p.maxd + 1) + clamp_index(p.pos_k[(size_t)j * NA + a], p.maxd - p.pos_q[row * NA + a],
                                                     2 * p.maxd)];
-      sum += fast_exp2((t - l) * kLog2e);
+      sum += ex2((t - l) * kLog2e);
     }
     for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    if ((lane >> 2) == (r & 7)) corr[r >> 3] = log2f(sum);
+    if ((lane >> 2) == (r & 7)) (r < 8 ? corr.x : corr.y) = log2f(sum);
   }
+  return corr;
 }
 
-template <int D, int NA>
+template <int D, int NA, int MT, bool kExact>
 __global__ void __launch_bounds__(kBThreads) rp_dq_kernel(const Params p) {
   using C = BwdCfg<D, NA>;
+  constexpr int kRows = 64 * MT;
   extern __shared__ __align__(16) unsigned char smem_raw[];
   uint4* ks = reinterpret_cast<uint4*>(smem_raw);
   uint4* vs = ks + kBStages * C::kTile;
   int* ps = reinterpret_cast<int*>(vs + kBStages * C::kTile);
   float* lut = reinterpret_cast<float*>(smem_raw + C::kRing);
-  float* hist = reinterpret_cast<float*>(smem_raw + C::kRing + C::lut(p.maxd));  // [NA * NB][threads]
-  uint8_t* bk = reinterpret_cast<uint8_t*>(hist + (size_t)NA * p.NB * kBThreads);
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, tq = lane & 3;
-  const int h = blockIdx.x % p.Hq, tile = blockIdx.x / p.Hq, hk = h / p.G, bins = NA * p.NB;
-  float* tab_part = p.tab_part + (size_t)blockIdx.x * bins;
+  const int h = blockIdx.x % p.Hq, tile = blockIdx.x / p.Hq, hk = h / p.G;
   int first, qlo, qhi, klo, khi;
-  const int seg = seg_of_tile(p.off_q, p.S, p.Nq, kBwdRows, tile, first);
+  const int seg = seg_of_tile(p.off_q, p.S, p.Nq, kRows, tile, first);
   seg_bounds(p.off_q, seg, p.Nq, qlo, qhi, p.status);
-  const int row0 = qlo + (tile - first) * kBwdRows;
-  if (tile < first || row0 >= qhi) {
-    for (int i = tid; i < bins; i += kBThreads) tab_part[i] = 0.0f;
-    return;
-  }
+  const int row0 = qlo + (tile - first) * kRows;
+  if (tile < first || row0 >= qhi) return;
   seg_bounds(p.off_k, seg, p.Nk, klo, khi, p.status);
   const int nk = khi - klo, chunks = (nk + kBChunk - 1) / kBChunk, top = 2 * p.maxd;
 
   auto load = [&](int c) {
     if (c < chunks) {
       const int st = c % kBStages, k0 = klo + c * kBChunk, n = min(kBChunk, khi - k0);
-      load_tile<D, kBChunk, kBThreads>(ks + st * C::kTile, p.k, k0, n, p.Hkv, hk, tid);
-      load_tile<D, kBChunk, kBThreads>(vs + st * C::kTile, p.v, k0, n, p.Hkv, hk, tid);
+      load_tile<D, kBCW, kBChunk, kBThreads>(ks + st * C::kTile, p.k, k0, n, p.Hkv, hk, tid);
+      load_tile<D, kBCW, kBChunk, kBThreads>(vs + st * C::kTile, p.v, k0, n, p.Hkv, hk, tid);
       for (int i = tid; i < kBChunk * NA; i += kBThreads)
         cp_async4(ps + st * kBChunk * NA + i, p.pos_k + (size_t)(k0 + min(i / NA, n - 1)) * NA + i % NA, true);
     }
@@ -100,79 +106,73 @@ __global__ void __launch_bounds__(kBThreads) rp_dq_kernel(const Params p) {
   load(0);
   load(1);
   fill_lut<NA>(p, lut, h, tid, kBThreads);
-  for (int i = tid; i < top + 1; i += kBThreads) {
-    const int b = p.bucket_of[i];
-    bk[i] = (uint8_t)(b < 0 || b >= p.NB ? 255 : b);
-  }
-  for (int b = 0; b < bins; ++b) hist[b * kBThreads + tid] = 0.0f;  // the thread's own column
 
-  uint32_t qa[D / 16][4], da[D / 16][4];
-  int qp[2][NA], q_lo[NA], q_hi[NA];
-  float lse[2], delta[2], corr[2];
-  const int wrow = row0 + warp * 16;
-  {
-    const uint16_t *q0 = nullptr, *q1 = nullptr, *d0 = nullptr, *d1 = nullptr, *o0 = nullptr, *o1 = nullptr;
-    const int r = wrow + g;
-    const size_t a0 = ((size_t)r * p.Hq + h), a1 = ((size_t)(r + 8) * p.Hq + h);
-    if (r < qhi) q0 = p.q + a0 * D, d0 = p.dout + a0 * D, o0 = p.o_in + a0 * D;
-    if (r + 8 < qhi) q1 = p.q + a1 * D, d1 = p.dout + a1 * D, o1 = p.o_in + a1 * D;
-    load_a_rows<D>(qa, q0, q1, lane);
-    load_a_rows<D>(da, d0, d1, lane);
+  uint32_t qa[MT][D / 16][4], da[MT][D / 16][4];
+  int qp[MT][2][NA], q_lo[NA], q_hi[NA];
+  float lse[MT][2], delta[MT][2], corr[MT][2], rest[MT][2];
+  const int wrow = row0 + warp * 16 * MT;
+#pragma unroll
+  for (int a = 0; a < NA; ++a) q_lo[a] = INT32_MAX, q_hi[a] = INT32_MIN;
+  bool huge = false;
+#pragma unroll
+  for (int mt = 0; mt < MT; ++mt) {
+    const int r = wrow + mt * 16 + g;
+    const size_t a0 = ((size_t)r * p.Hq + h) * D, a1 = ((size_t)(r + 8) * p.Hq + h) * D;
+    const bool l0 = r < qhi, l1 = r + 8 < qhi;
+    load_a_rows<D>(qa[mt], l0 ? p.q + a0 : nullptr, l1 ? p.q + a1 : nullptr, lane);
+    load_a_rows<D>(da[mt], l0 ? p.dout + a0 : nullptr, l1 ? p.dout + a1 : nullptr, lane);
     uint32_t oa[D / 16][4];
-    load_a_rows<D>(oa, o0, o1, lane);
-    delta[0] = delta[1] = 0.0f;
+    load_a_rows<D>(oa, l0 ? p.o_in + a0 : nullptr, l1 ? p.o_in + a1 : nullptr, lane);
+    delta[mt][0] = delta[mt][1] = 0.0f;
 #pragma unroll
     for (int d = 0; d < D / 16; ++d)
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        const float lo = bf16_to_f32((uint16_t)da[d][e]) * bf16_to_f32((uint16_t)oa[d][e]);
-        delta[e & 1] += fmaf(__uint_as_float(da[d][e] & 0xffff0000u), __uint_as_float(oa[d][e] & 0xffff0000u), lo);
+        const float lo = bf16_to_f32((uint16_t)da[mt][d][e]) * bf16_to_f32((uint16_t)oa[d][e]);
+        delta[mt][e & 1] +=
+            fmaf(__uint_as_float(da[mt][d][e] & 0xffff0000u), __uint_as_float(oa[d][e] & 0xffff0000u), lo);
       }
-#pragma unroll
-    for (int a = 0; a < NA; ++a) q_lo[a] = INT32_MAX, q_hi[a] = INT32_MIN;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const int ri = r + 8 * i;
-      const size_t at = (size_t)ri * p.Hq + h;
-      delta[i] = quad_sum(delta[i]);
-      lse[i] = ri < qhi ? p.lse_in[at] : INFINITY;
-      if (lse[i] == -INFINITY) lse[i] = INFINITY;  // a row without keys: P = 0
-      if (ri < qhi && tq == 0) p.delta[at] = delta[i];
+      delta[mt][i] = quad_sum(delta[mt][i]);
+      corr[mt][i] = rest[mt][i] = 0.0f;
+      lse[mt][i] = ri < qhi ? p.lse_in[(size_t)ri * p.Hq + h] : INFINITY;
+      if (lse[mt][i] == -INFINITY) lse[mt][i] = INFINITY;  // a row without keys: P = 0
+      huge = huge || (fabsf(lse[mt][i]) >= kFoldLimit && lse[mt][i] != INFINITY);
 #pragma unroll
       for (int a = 0; a < NA; ++a) {
         const int x = p.pos_q[(size_t)min(ri, qhi - 1) * NA + a];
-        qp[i][a] = p.maxd - x;
+        qp[mt][i][a] = p.maxd - x;
         q_lo[a] = min(q_lo[a], x);
         q_hi[a] = max(q_hi[a], x);
       }
     }
+  }
 #pragma unroll
-    for (int a = 0; a < NA; ++a) {
-      q_lo[a] = __reduce_min_sync(0xffffffffu, q_lo[a]);
-      q_hi[a] = __reduce_max_sync(0xffffffffu, q_hi[a]);
-      if (q_lo[a] < -kPosLimit || q_hi[a] > kPosLimit) raise_status(p.status, LSRM_ERR_BOUNDS);
-    }
+  for (int a = 0; a < NA; ++a) {
+    q_lo[a] = __reduce_min_sync(0xffffffffu, q_lo[a]);
+    q_hi[a] = __reduce_max_sync(0xffffffffu, q_hi[a]);
+    if (q_lo[a] < -kPosLimit || q_hi[a] > kPosLimit) raise_status(p.status, LSRM_ERR_BOUNDS);
   }
   __syncthreads();  // the bias table
-  corr[0] = corr[1] = 0.0f;
-  if (__any_sync(0xffffffffu, (fabsf(lse[0]) >= kFoldLimit && lse[0] != INFINITY) ||
-                                  (fabsf(lse[1]) >= kFoldLimit && lse[1] != INFINITY)))
-    huge_rows<D, NA>(p, lut, lse, corr, wrow, h, hk, klo, khi, lane);
+  if (__any_sync(0xffffffffu, huge)) {
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const int ri = wrow + g + 8 * i;
-    if (ri < qhi && tq == 0) p.corr[(size_t)ri * p.Hq + h] = corr[i];
+    for (int mt = 0; mt < MT; ++mt) {
+      const float2 x = huge_rows<D, NA>(p, lut, lse[mt][0], lse[mt][1], wrow + mt * 16, h, hk, klo, khi, lane);
+      corr[mt][0] = x.x, corr[mt][1] = x.y;
+    }
   }
-  float dq[D / 8][4];
+  float dq[MT][D / 8][4], pk[kExact ? MT : 1][kExact ? D / 8 : 1][4];
 #pragma unroll
-  for (int n = 0; n < D / 8; ++n)
+  for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-    for (int e = 0; e < 4; ++e) dq[n][e] = 0.0f;
-  // the running sum of tiles on one distance, and its bucket
-  float run[NA];
-  int run_b[NA];
+    for (int n = 0; n < D / 8; ++n)
 #pragma unroll
-  for (int a = 0; a < NA; ++a) run[a] = 0.0f, run_b[a] = 255;
+      for (int e = 0; e < 4; ++e) {
+        dq[mt][n][e] = 0.0f;
+        if (kExact) pk[kExact ? mt : 0][kExact ? n : 0][e] = 0.0f;
+      }
 
   for (int c = 0; c < chunks; ++c) {
     cp_async_wait<1>();
@@ -180,141 +180,454 @@ __global__ void __launch_bounds__(kBThreads) rp_dq_kernel(const Params p) {
     load(c + 2);
     const uint4* kt = ks + (c % kBStages) * C::kTile;
     const uint4* vt = vs + (c % kBStages) * C::kTile;
-    const int* pt = ps + (c % kBStages) * kBChunk * NA;
 #pragma unroll 1
-    for (int half = 0; half < 2; ++half) {
-      const int kb = half * 32, left = nk - c * kBChunk - kb;
+    for (int kb = 0; kb < kBChunk; kb += kBCols) {
+      const int left = nk - c * kBChunk - kb;
       if (left <= 0 || wrow >= qhi) break;
-      float s[4][4], dp[4][4];
+      const int* pt = ps + (c % kBStages) * kBChunk * NA + kb * NA;
+      float s[MT][kBNT][4], dp[MT][kBNT][4];
 #pragma unroll
-      for (int n = 0; n < 4; ++n) {
+      for (int n = 0; n < kBNT; ++n) {
         uint32_t b[D / 8];
-        load_b_rows<D>(b, kt, kb + n * 8, lane);
+        load_b_rows<D, kBCW>(b, kt, kb, n, lane);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) s[n][e] = dp[n][e] = 0.0f;
+        for (int mt = 0; mt < MT; ++mt) {
 #pragma unroll
-        for (int d = 0; d < D / 16; ++d) mma_bf16_16816(s[n], qa[d], b + 2 * d);
-        load_b_rows<D>(b, vt, kb + n * 8, lane);
+          for (int e = 0; e < 4; ++e) s[mt][n][e] = dp[mt][n][e] = 0.0f;
 #pragma unroll
-        for (int d = 0; d < D / 16; ++d) mma_bf16_16816(dp[n], da[d], b + 2 * d);
-      }
-      int uni[NA];
-      bool all_uni = true;
-      float ub = 0.0f;
-#pragma unroll
-      for (int a = 0; a < NA; ++a) {
-        const int x = pt[(kb + lane) * NA + a];
-        const int lo = __reduce_min_sync(0xffffffffu, x), hi = __reduce_max_sync(0xffffffffu, x);
-        if (lo < -kPosLimit || hi > kPosLimit) raise_status(p.status, LSRM_ERR_BOUNDS);
-        uni[a] = uniform_index(lo, hi, q_lo[a], q_hi[a], p.maxd);
-        all_uni = all_uni && uni[a] >= 0;
-        if (uni[a] >= 0) ub += lut[a * (top + 1) + uni[a]];
-      }
-      all_uni = all_uni && fabsf(ub) < kFoldLimit;
-      if (!all_uni) {
-#pragma unroll
-        for (int n = 0; n < 4; ++n)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) s[n][e] = fmaf(s[n][e], p.scale, ub);
-#pragma unroll
-        for (int a = 0; a < NA; ++a) {
-          if (uni[a] >= 0) continue;
-          const float* la = lut + a * (top + 1);
-#pragma unroll
-          for (int n = 0; n < 4; ++n)
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              const int x = pt[(kb + n * 8 + 2 * tq + e) * NA + a];
-#pragma unroll
-              for (int i = 0; i < 2; ++i) s[n][2 * i + e] += la[clamp_index(x, qp[i][a], top)];
-            }
+          for (int d = 0; d < D / 16; ++d) mma16816(s[mt][n], qa[mt][d], b + 2 * d);
         }
+        load_b_rows<D, kBCW>(b, vt, kb, n, lane);
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+          for (int d = 0; d < D / 16; ++d) mma16816(dp[mt][n], da[mt][d], b + 2 * d);
       }
-      // s becomes dS
+      int mode[NA], one[NA];
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const float x = p.scale * kLog2e, cst = fmaf(ub - lse[i], kLog2e, -corr[i]);
+      for (int a = 0; a < NA; ++a)
+        mode[a] = axis_mode<NA, kBCols>(pt + a, q_lo[a], q_hi[a], false, p.maxd, lane, one[a], p.status);
+      float base[MT][2];
+      const bool fold = add_bias<NA, MT, kBNT, 1>(s, base, mode, one, pt, lut, top, qp, p.scale, tq);
+      if (left < kBCols) {
+        keep_branch();
 #pragma unroll
-        for (int n = 0; n < 4; ++n)
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const float t = s[n][2 * i + e];
-            const float pr = fast_exp2(all_uni ? fmaf(t, x, cst) : fmaf(t - lse[i], kLog2e, -corr[i]));
-            s[n][2 * i + e] = pr * (dp[n][2 * i + e] - delta[i]);
-          }
-      }
-      if (left < 32) {
-#pragma unroll
-        for (int n = 0; n < 4; ++n)
+        for (int n = 0; n < kBNT; ++n)
 #pragma unroll
           for (int e = 0; e < 2; ++e)
-            if (n * 8 + 2 * tq + e >= left) s[n][e] = s[n][2 + e] = 0.0f;
+            if (tq * kBCW + 2 * n + e >= left)
+#pragma unroll
+              for (int mt = 0; mt < MT; ++mt) s[mt][n][e] = s[mt][n][2 + e] = -INFINITY;
       }
-      // the table's gradient
+      uint32_t sa[MT][2][4], pa[MT][2][4];
 #pragma unroll
-      for (int a = 0; a < NA; ++a) {
-        if (uni[a] >= 0) {
-          const int b = bk[uni[a]];
-          if (b != run_b[a]) {
-            if (run_b[a] != 255) hist[(a * p.NB + run_b[a]) * kBThreads + tid] += run[a];
-            run[a] = 0.0f;
-            run_b[a] = b;
-          }
-          float sum = 0.0f;
+      for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-          for (int n = 0; n < 4; ++n) sum += (s[n][0] + s[n][1]) + (s[n][2] + s[n][3]);
-          run[a] += sum;
-        } else {
+        for (int i = 0; i < 2; ++i) {
+          const float x = fold ? p.scale * kLog2e : kLog2e, l = lse[mt][i];
+          const float cst = fmaf(fold ? base[mt][i] - l : -l, kLog2e, -corr[mt][i]);
+          float sum0 = 0.0f, sum1 = 0.0f;
 #pragma unroll
-          for (int n = 0; n < 4; ++n)
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              const int x = pt[(kb + n * 8 + 2 * tq + e) * NA + a];
-#pragma unroll
-              for (int i = 0; i < 2; ++i) {
-                const int b = bk[clamp_index(x, qp[i][a], top)];
-                if (b != 255) hist[(a * p.NB + b) * kBThreads + tid] += s[n][2 * i + e];
-              }
+          for (int n = 0; n < kBNT; ++n) {
+            float p0 = s[mt][n][2 * i], p1 = s[mt][n][2 * i + 1];
+            if (fold) {
+              ffma2(p0, p1, p0, p1, x, cst);
+            } else {  // the subtraction first: exact for scores of any size
+              fadd2_acc(p0, p1, -l, -l);
+              ffma2(p0, p1, p0, p1, kLog2e, -corr[mt][i]);
             }
+            p0 = ex2(p0);
+            p1 = ex2(p1);
+            if (kExact) pa[mt][n >> 1][(n & 1) * 2 + i] = pack2(p0, p1);
+            float d0 = dp[mt][n][2 * i], d1 = dp[mt][n][2 * i + 1];
+            fadd2_acc(d0, d1, -delta[mt][i], -delta[mt][i]);
+            fmul2(d0, d1, d0, d1, p0, p1);
+            fadd2_acc(sum0, sum1, d0, d1);
+            sa[mt][n >> 1][(n & 1) * 2 + i] = pack2(d0, d1);
+          }
+          rest[mt][i] += sum0 + sum1;
         }
-      }
-      uint32_t sa[2][4];
-#pragma unroll
-      for (int n = 0; n < 4; ++n)
-#pragma unroll
-        for (int i = 0; i < 2; ++i) sa[n >> 1][(n & 1) * 2 + i] = pack_bf16x2(s[n][2 * i], s[n][2 * i + 1]);
 #pragma unroll
       for (int j = 0; j < 2; ++j)
 #pragma unroll
         for (int dc = 0; dc < D / 8; dc += 2) {
           uint32_t b[4];
-          load_b_cols<D>(b, kt, kb + j * 16, dc, lane);
-          mma_bf16_16816(dq[dc], sa[j], b);
-          mma_bf16_16816(dq[dc + 1], sa[j], b + 2);
+          load_b_cols<D, kBCW>(b, kt, kb, j, dc, lane);
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt) {
+            mma16816(dq[mt][dc], sa[mt][j], b);
+            mma16816(dq[mt][dc + 1], sa[mt][j], b + 2);
+            if (kExact) {
+              mma16816(pk[kExact ? mt : 0][kExact ? dc : 0], pa[mt][j], b);
+              mma16816(pk[kExact ? mt : 0][kExact ? dc + 1 : 0], pa[mt][j], b + 2);
+            }
+          }
         }
     }
   }
 #pragma unroll
-  for (int a = 0; a < NA; ++a)
-    if (run_b[a] != 255) hist[(a * p.NB + run_b[a]) * kBThreads + tid] += run[a];
+  for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const int r = wrow + g + 8 * i;
-    if (r >= qhi) continue;
-    uint16_t* to = p.dq + ((size_t)r * p.Hq + h) * D + 2 * tq;
+    for (int i = 0; i < 2; ++i) {
+      const float more = quad_sum(rest[mt][i]);  // Delta - D~
+      const int r = wrow + mt * 16 + g + 8 * i;
+      if (r >= qhi) continue;
+      const size_t at = (size_t)r * p.Hq + h;
+      if (tq == 0) {
+        p.delta[at] = delta[mt][i] + more;
+        p.corr[at] = corr[mt][i];
+      }
+      uint16_t* to = p.dq + at * D + 2 * tq;
+#pragma unroll
+      for (int n = 0; n < D / 8; ++n) {
+        float x = dq[mt][n][2 * i], y = dq[mt][n][2 * i + 1];
+        if (kExact) {
+          x = fmaf(-more, pk[kExact ? mt : 0][kExact ? n : 0][2 * i], x);
+          y = fmaf(-more, pk[kExact ? mt : 0][kExact ? n : 0][2 * i + 1], y);
+        }
+        *reinterpret_cast<uint32_t*>(to + n * 8) = pack2(x * p.scale, y * p.scale);
+      }
+    }
+}
+
+// hist[b0] += v0, hist[b1] += v1 (entries of the thread's own column) with both reads ahead of both
+// writes: one latency for two, and right when the buckets are the same
+__device__ __forceinline__ void add_two(float* col, int b0, float v0, int b1, float v1) {
+  const float h0 = col[b0 * kBThreads], h1 = col[b1 * kBThreads];
+  col[b1 * kBThreads] = h1 + v1;
+  col[b0 * kBThreads] = h0 + v0 + (b0 == b1 ? v1 : 0.0f);
+}
+
+// the (head, query chunk) range of a split: whole heads, or an even part of one head's chunks
+__device__ __forceinline__ void split_range(const Params& p, int split, int chunks, int& h0, int& h1, int& c0, int& c1,
+                                            int& part) {
+  if (p.splits <= p.G) {
+    const int n = p.G / p.splits;
+    h0 = split * n, h1 = h0 + n, c0 = 0, c1 = chunks, part = 0;
+  } else {
+    const int f = p.splits / p.G, n = (chunks + f - 1) / f;
+    h0 = split / f, h1 = h0 + 1, part = split % f;
+    c0 = min(part * n, chunks), c1 = min(c0 + n, chunks);
+  }
+}
+
+template <int D, int NA, int MT>
+__global__ void __launch_bounds__(kBThreads) rp_dkv_kernel(const Params p) {
+  using C = BwdCfg<D, NA>;
+  constexpr int kRows = 64 * MT;
+  extern __shared__ __align__(16) unsigned char smem_raw[];
+  uint4* qs = reinterpret_cast<uint4*>(smem_raw);
+  uint4* ds = qs + kBStages * C::kTile;
+  int* ps = reinterpret_cast<int*>(ds + kBStages * C::kTile);
+  float* ls = reinterpret_cast<float*>(smem_raw + C::kRing);  // [stage][3][chunk]: LSE, Delta, corr
+  float* lut = ls + kBStages * 3 * kBChunk;
+  float* hist = lut + C::lut(p.maxd) / 4;  // [NA * NB][threads]
+  uint8_t* bk = reinterpret_cast<uint8_t*>(hist + (size_t)NA * p.NB * kBThreads);
+
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, tq = lane & 3;
+  const int bins = NA * p.NB;
+  int unit = blockIdx.x;
+  const int split = unit % p.splits;
+  unit /= p.splits;
+  const int hk = unit % p.Hkv, tile = unit / p.Hkv;
+  int first, qlo = 0, qhi = 0, klo, khi;
+  const int seg = seg_of_tile(p.off_k, p.S, p.Nk, kRows, tile, first);
+  seg_bounds(p.off_k, seg, p.Nk, klo, khi, p.status);
+  const int row0 = klo + (tile - first) * kRows;
+  const bool empty = tile < first || row0 >= khi;
+  if (!empty) seg_bounds(p.off_q, seg, p.Nq, qlo, qhi, p.status);
+  const int nq = qhi - qlo, chunks = (nq + kBChunk - 1) / kBChunk, top = 2 * p.maxd;
+  int h0, h1, c0, c1, part;
+  split_range(p, split, chunks, h0, h1, c0, c1, part);
+  const int parts = p.splits > p.G ? p.splits / p.G : 1;
+  float* tab_part = p.tab_part + (((size_t)tile * parts + part) * p.Hq + hk * p.G) * bins;  // + head * bins
+  if (empty) {
+    for (int i = h0 * bins + tid; i < h1 * bins; i += kBThreads) tab_part[i] = 0.0f;
+    return;
+  }
+  const int nc = c1 - c0, steps = (h1 - h0) * nc;
+
+  auto load = [&](int it) {
+    if (it < steps) {
+      const int h = hk * p.G + h0 + it / nc, q0 = qlo + (c0 + it % nc) * kBChunk, n = min(kBChunk, qhi - q0);
+      const int st = it % kBStages;
+      load_tile<D, kBCW, kBChunk, kBThreads>(qs + st * C::kTile, p.q, q0, n, p.Hq, h, tid);
+      load_tile<D, kBCW, kBChunk, kBThreads>(ds + st * C::kTile, p.dout, q0, n, p.Hq, h, tid);
+      for (int i = tid; i < kBChunk * NA; i += kBThreads)
+        cp_async4(ps + st * kBChunk * NA + i, p.pos_q + (size_t)(q0 + min(i / NA, n - 1)) * NA + i % NA, true);
+      for (int i = tid; i < 3 * kBChunk; i += kBThreads) {
+        const float* src = i < kBChunk ? p.lse_in : i < 2 * kBChunk ? p.delta : p.corr;
+        cp_async4(ls + st * 3 * kBChunk + i, src + (size_t)(q0 + min(i % kBChunk, n - 1)) * p.Hq + h, true);
+      }
+    }
+    cp_async_commit();
+  };
+  load(0);
+  load(1);
+  for (int i = tid; i < top + 1; i += kBThreads) {
+    const int b = p.bucket_of[i];
+    bk[i] = (uint8_t)(b < 0 || b >= p.NB ? 255 : b);
+  }
+  for (int b = 0; b < bins; ++b) hist[b * kBThreads + tid] = 0.0f;  // the thread's own column
+  float* col = hist + tid;
+
+  uint32_t ka[MT][D / 16][4], va[MT][D / 16][4];
+  int kp[MT][2][NA], k_lo[NA], k_hi[NA];
+  const int wrow = row0 + warp * 16 * MT;
+#pragma unroll
+  for (int a = 0; a < NA; ++a) k_lo[a] = INT32_MAX, k_hi[a] = INT32_MIN;
+#pragma unroll
+  for (int mt = 0; mt < MT; ++mt) {
+    const int r = wrow + mt * 16 + g;
+    const size_t a0 = ((size_t)r * p.Hkv + hk) * D, a1 = ((size_t)(r + 8) * p.Hkv + hk) * D;
+    load_a_rows<D>(ka[mt], r < khi ? p.k + a0 : nullptr, r + 8 < khi ? p.k + a1 : nullptr, lane);
+    load_a_rows<D>(va[mt], r < khi ? p.v + a0 : nullptr, r + 8 < khi ? p.v + a1 : nullptr, lane);
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int a = 0; a < NA; ++a) {
+        const int x = p.pos_k[(size_t)min(r + 8 * i, khi - 1) * NA + a];
+        kp[mt][i][a] = p.maxd + x;
+        k_lo[a] = min(k_lo[a], x);
+        k_hi[a] = max(k_hi[a], x);
+      }
+  }
+#pragma unroll
+  for (int a = 0; a < NA; ++a) {
+    k_lo[a] = __reduce_min_sync(0xffffffffu, k_lo[a]);
+    k_hi[a] = __reduce_max_sync(0xffffffffu, k_hi[a]);
+  }
+  float dk[MT][D / 8][4], dv[MT][D / 8][4];
+#pragma unroll
+  for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
     for (int n = 0; n < D / 8; ++n)
-      *reinterpret_cast<uint32_t*>(to + n * 8) = pack_bf16x2(dq[n][2 * i] * p.scale, dq[n][2 * i + 1] * p.scale);
-  }
-  __syncthreads();
-  for (int b = warp; b < bins; b += kBThreads / 32) {
-    float x = 0.0f;
 #pragma unroll
-    for (int t = 0; t < kBThreads; t += 32) x += hist[b * kBThreads + t + lane];
+      for (int e = 0; e < 4; ++e) dk[mt][n][e] = dv[mt][n][e] = 0.0f;
+  // the running sum of tiles on one distance, and its bucket
+  float run[NA];
+  int run_b[NA];
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
-    if (lane == 0) tab_part[b] = x;
+  for (int a = 0; a < NA; ++a) run[a] = 0.0f, run_b[a] = 255;
+  // the head's sums of the CTA's threads to global memory, and the columns back to 0
+  auto flush = [&](int head) {
+#pragma unroll
+    for (int a = 0; a < NA; ++a) {
+      if (run_b[a] != 255) col[(a * p.NB + run_b[a]) * kBThreads] += run[a];
+      run[a] = 0.0f;
+      run_b[a] = 255;
+    }
+    __syncthreads();
+    for (int b = warp; b < bins; b += kBThreads / 32) {
+      float x = 0.0f;
+#pragma unroll
+      for (int t = 0; t < kBThreads; t += 32) {
+        x += hist[b * kBThreads + t + lane];
+        hist[b * kBThreads + t + lane] = 0.0f;
+      }
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+      if (lane == 0) tab_part[head * bins + b] = x;
+    }
+    __syncthreads();
+  };
+
+  for (int it = 0; it < steps; ++it) {
+    const int head = h0 + it / nc, cc = it % nc;
+    cp_async_wait<1>();
+    __syncthreads();
+    load(it + 2);
+    if (cc == 0) {  // the barriers since the last head's tiles ended the old table's use
+      fill_lut<NA>(p, lut, hk * p.G + head, tid, kBThreads);
+      __syncthreads();
+    }
+    const int st = it % kBStages;
+    const uint4* qt = qs + st * C::kTile;
+    const uint4* dt = ds + st * C::kTile;
+#pragma unroll 1
+    for (int qb = 0; qb < kBChunk; qb += kBCols) {
+      const int left = nq - (c0 + cc) * kBChunk - qb;
+      if (left <= 0 || wrow >= khi) break;
+      const int* pt = ps + st * kBChunk * NA + qb * NA;
+      const float* lt = ls + st * 3 * kBChunk + qb + tq * kBCW;
+      float s[MT][kBNT][4], dp[MT][kBNT][4];
+#pragma unroll
+      for (int n = 0; n < kBNT; ++n) {
+        uint32_t b[D / 8];
+        load_b_rows<D, kBCW>(b, qt, qb, n, lane);
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) s[mt][n][e] = dp[mt][n][e] = 0.0f;
+#pragma unroll
+          for (int d = 0; d < D / 16; ++d) mma16816(s[mt][n], ka[mt][d], b + 2 * d);
+        }
+        load_b_rows<D, kBCW>(b, dt, qb, n, lane);
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+          for (int d = 0; d < D / 16; ++d) mma16816(dp[mt][n], va[mt][d], b + 2 * d);
+      }
+      int mode[NA], one[NA];
+#pragma unroll
+      for (int a = 0; a < NA; ++a)
+        mode[a] = axis_mode<NA, kBCols>(pt + a, k_lo[a], k_hi[a], true, p.maxd, lane, one[a], p.status);
+      float base[MT][2];
+      const bool fold = add_bias<NA, MT, kBNT, -1>(s, base, mode, one, pt, lut, top, kp, p.scale, tq);
+      // s becomes dS^T, dp becomes P^T
+      const float x = p.scale * kLog2e;
+#pragma unroll
+      for (int n = 0; n < kBNT; ++n) {
+        float2 l = *reinterpret_cast<const float2*>(lt + 2 * n);
+        const float2 dl = *reinterpret_cast<const float2*>(lt + kBChunk + 2 * n);
+        const float2 cr = *reinterpret_cast<const float2*>(lt + 2 * kBChunk + 2 * n);
+        const int c = tq * kBCW + 2 * n;
+        if (l.x == -INFINITY || c >= left) l.x = INFINITY;  // no key, or no query: P = 0
+        if (l.y == -INFINITY || c + 1 >= left) l.y = INFINITY;
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            float p0 = s[mt][n][2 * i], p1 = s[mt][n][2 * i + 1];
+            if (fold) {
+              p0 = fmaf(p0, x, fmaf(base[mt][i] - l.x, kLog2e, -cr.x));
+              p1 = fmaf(p1, x, fmaf(base[mt][i] - l.y, kLog2e, -cr.y));
+            } else {
+              p0 = fmaf(p0 - l.x, kLog2e, -cr.x);
+              p1 = fmaf(p1 - l.y, kLog2e, -cr.y);
+            }
+            p0 = ex2(p0);
+            p1 = ex2(p1);
+            s[mt][n][2 * i] = p0 * (dp[mt][n][2 * i] - dl.x);
+            s[mt][n][2 * i + 1] = p1 * (dp[mt][n][2 * i + 1] - dl.y);
+            dp[mt][n][2 * i] = p0;
+            dp[mt][n][2 * i + 1] = p1;
+          }
+      }
+      if (wrow + 16 * MT > khi) {  // rows past the segment's last key have no pairs
+        keep_branch();
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+            if (wrow + mt * 16 + g + 8 * i >= khi)
+#pragma unroll
+              for (int n = 0; n < kBNT; ++n) s[mt][n][2 * i] = s[mt][n][2 * i + 1] = 0.0f;
+      }
+      // the table's gradient
+#pragma unroll
+      for (int a = 0; a < NA; ++a) {
+        float* ca = col + a * p.NB * kBThreads;
+        const int* xs = pt + tq * kBCW * NA + a;
+        if (mode[a] == kOne) {
+          const int b = bk[one[a]];
+          if (b != run_b[a]) {
+            if (run_b[a] != 255) ca[run_b[a] * kBThreads] += run[a];
+            run[a] = 0.0f;
+            run_b[a] = b;
+          }
+          float sum0 = 0.0f, sum1 = 0.0f;
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+            for (int n = 0; n < kBNT; ++n) {
+              fadd2_acc(sum0, sum1, s[mt][n][0], s[mt][n][1]);
+              fadd2_acc(sum0, sum1, s[mt][n][2], s[mt][n][3]);
+            }
+          run[a] += sum0 + sum1;
+        } else if (mode[a] <= kFour) {
+          // runs of eight or four queries on one position
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              const float lo = (s[mt][0][2 * i] + s[mt][0][2 * i + 1]) + (s[mt][1][2 * i] + s[mt][1][2 * i + 1]);
+              const float hi = (s[mt][2][2 * i] + s[mt][2][2 * i + 1]) + (s[mt][3][2 * i] + s[mt][3][2 * i + 1]);
+              const int b0 = bk[clamp_index(-xs[0], kp[mt][i][a], top)];
+              const int b1 = bk[clamp_index(-xs[4 * NA], kp[mt][i][a], top)];
+              if (b0 != 255 && b1 != 255) {
+                add_two(ca, b0, lo, b1, hi);
+              } else {
+                if (b0 != 255) ca[b0 * kBThreads] += lo;
+                if (b1 != 255) ca[b1 * kBThreads] += hi;
+              }
+            }
+        } else {
+#pragma unroll
+          for (int n = 0; n < kBNT; ++n) {
+            const int x0 = -xs[2 * n * NA], x1 = -xs[(2 * n + 1) * NA];
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+              for (int i = 0; i < 2; ++i) {
+                const int b0 = bk[clamp_index(x0, kp[mt][i][a], top)], b1 = bk[clamp_index(x1, kp[mt][i][a], top)];
+                if (b0 != 255 && b1 != 255) {
+                  add_two(ca, b0, s[mt][n][2 * i], b1, s[mt][n][2 * i + 1]);
+                } else {
+                  if (b0 != 255) ca[b0 * kBThreads] += s[mt][n][2 * i];
+                  if (b1 != 255) ca[b1 * kBThreads] += s[mt][n][2 * i + 1];
+                }
+              }
+          }
+        }
+      }
+      uint32_t sa[MT][2][4], pa[MT][2][4];
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+        for (int n = 0; n < kBNT; ++n)
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            sa[mt][n >> 1][(n & 1) * 2 + i] = pack2(s[mt][n][2 * i], s[mt][n][2 * i + 1]);
+            pa[mt][n >> 1][(n & 1) * 2 + i] = pack2(dp[mt][n][2 * i], dp[mt][n][2 * i + 1]);
+          }
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int dc = 0; dc < D / 8; dc += 2) {
+          uint32_t b[4];
+          load_b_cols<D, kBCW>(b, qt, qb, j, dc, lane);
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt) {
+            mma16816(dk[mt][dc], sa[mt][j], b);
+            mma16816(dk[mt][dc + 1], sa[mt][j], b + 2);
+          }
+          load_b_cols<D, kBCW>(b, dt, qb, j, dc, lane);
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt) {
+            mma16816(dv[mt][dc], pa[mt][j], b);
+            mma16816(dv[mt][dc + 1], pa[mt][j], b + 2);
+          }
+        }
+    }
+    if (cc == nc - 1) flush(head);
   }
+  if (steps == 0)  // no query: the table's sums are 0
+    for (int i = h0 * bins + tid; i < h1 * bins; i += kBThreads) tab_part[i] = 0.0f;
+#pragma unroll
+  for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int r = wrow + mt * 16 + g + 8 * i;
+      if (r >= khi) continue;
+      const size_t at = ((size_t)r * p.Hkv + hk) * D + 2 * tq;
+      if (p.splits == 1) {
+#pragma unroll
+        for (int n = 0; n < D / 8; ++n) {
+          *reinterpret_cast<uint32_t*>(p.dk + at + n * 8) =
+              pack2(dk[mt][n][2 * i] * p.scale, dk[mt][n][2 * i + 1] * p.scale);
+          *reinterpret_cast<uint32_t*>(p.dv + at + n * 8) = pack2(dv[mt][n][2 * i], dv[mt][n][2 * i + 1]);
+        }
+      } else {
+        const size_t stride = (size_t)p.Nk * p.Hkv * D;
+        float* to = p.kv_part + (size_t)split * 2 * stride + at;
+#pragma unroll
+        for (int n = 0; n < D / 8; ++n) {
+          *reinterpret_cast<float2*>(to + n * 8) = make_float2(dk[mt][n][2 * i], dk[mt][n][2 * i + 1]);
+          *reinterpret_cast<float2*>(to + stride + n * 8) = make_float2(dv[mt][n][2 * i], dv[mt][n][2 * i + 1]);
+        }
+      }
+    }
 }
 
 // dtable = the tiles' sums in order: 32 bins a CTA, 32 runs of tiles, joined in shared memory
@@ -333,209 +646,6 @@ __global__ void __launch_bounds__(1024) rp_table_kernel(const Params p, int tile
 #pragma unroll
   for (int r = 0; r < 32; ++r) x += part[r][lane];
   p.dtable[(size_t)b * p.Hq + h] = __bfloat16_as_ushort(__float2bfloat16_rn(x));
-}
-
-template <int D, int NA>
-__global__ void __launch_bounds__(kBThreads) rp_dkv_kernel(const Params p) {
-  using C = BwdCfg<D, NA>;
-  extern __shared__ __align__(16) unsigned char smem_raw[];
-  uint4* qs = reinterpret_cast<uint4*>(smem_raw);
-  uint4* ds = qs + kBStages * C::kTile;
-  int* ps = reinterpret_cast<int*>(ds + kBStages * C::kTile);
-  float* ls = reinterpret_cast<float*>(smem_raw + C::kRing);  // [stage][3][chunk]: LSE, Delta, corr
-  float* lut = ls + kBStages * 3 * kBChunk;
-
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, tq = lane & 3;
-  int unit = blockIdx.x;
-  const int split = unit % p.splits;
-  unit /= p.splits;
-  const int hk = unit % p.Hkv, tile = unit / p.Hkv;
-  int first, qlo, qhi, klo, khi;
-  const int seg = seg_of_tile(p.off_k, p.S, p.Nk, kBwdRows, tile, first);
-  seg_bounds(p.off_k, seg, p.Nk, klo, khi, p.status);
-  const int row0 = klo + (tile - first) * kBwdRows;
-  if (tile < first || row0 >= khi) return;
-  seg_bounds(p.off_q, seg, p.Nq, qlo, qhi, p.status);
-  const int nq = qhi - qlo, chunks = (nq + kBChunk - 1) / kBChunk, top = 2 * p.maxd;
-  // the (head, query chunk) steps of this split, head by head
-  const long long total = (long long)p.G * chunks, per = (total + p.splits - 1) / p.splits;
-  const int i0 = (int)min(split * per, total), i1 = (int)min(i0 + per, total);
-
-  auto load = [&](int it) {
-    if (it < i1) {
-      const int h = hk * p.G + it / chunks, q0 = qlo + it % chunks * kBChunk, n = min(kBChunk, qhi - q0);
-      const int st = it % kBStages;
-      load_tile<D, kBChunk, kBThreads>(qs + st * C::kTile, p.q, q0, n, p.Hq, h, tid);
-      load_tile<D, kBChunk, kBThreads>(ds + st * C::kTile, p.dout, q0, n, p.Hq, h, tid);
-      for (int i = tid; i < kBChunk * NA; i += kBThreads)
-        cp_async4(ps + st * kBChunk * NA + i, p.pos_q + (size_t)(q0 + min(i / NA, n - 1)) * NA + i % NA, true);
-      for (int i = tid; i < 3 * kBChunk; i += kBThreads) {
-        const float* src = i < kBChunk ? p.lse_in : i < 2 * kBChunk ? p.delta : p.corr;
-        cp_async4(ls + st * 3 * kBChunk + i, src + (size_t)(q0 + min(i % kBChunk, n - 1)) * p.Hq + h, true);
-      }
-    }
-    cp_async_commit();
-  };
-  load(i0);
-  load(i0 + 1);
-
-  uint32_t ka[D / 16][4], va[D / 16][4];
-  int kp[2][NA], k_lo[NA], k_hi[NA];
-  const int wrow = row0 + warp * 16;
-  {
-    const int r = wrow + g;
-    const size_t a0 = ((size_t)r * p.Hkv + hk) * D, a1 = ((size_t)(r + 8) * p.Hkv + hk) * D;
-    load_a_rows<D>(ka, r < khi ? p.k + a0 : nullptr, r + 8 < khi ? p.k + a1 : nullptr, lane);
-    load_a_rows<D>(va, r < khi ? p.v + a0 : nullptr, r + 8 < khi ? p.v + a1 : nullptr, lane);
-#pragma unroll
-    for (int a = 0; a < NA; ++a) k_lo[a] = INT32_MAX, k_hi[a] = INT32_MIN;
-#pragma unroll
-    for (int i = 0; i < 2; ++i)
-#pragma unroll
-      for (int a = 0; a < NA; ++a) {
-        const int x = p.pos_k[(size_t)min(r + 8 * i, khi - 1) * NA + a];
-        kp[i][a] = p.maxd + x;
-        k_lo[a] = min(k_lo[a], x);
-        k_hi[a] = max(k_hi[a], x);
-      }
-#pragma unroll
-    for (int a = 0; a < NA; ++a) {
-      k_lo[a] = __reduce_min_sync(0xffffffffu, k_lo[a]);
-      k_hi[a] = __reduce_max_sync(0xffffffffu, k_hi[a]);
-    }
-  }
-  float dk[D / 8][4], dv[D / 8][4];
-#pragma unroll
-  for (int n = 0; n < D / 8; ++n)
-#pragma unroll
-    for (int e = 0; e < 4; ++e) dk[n][e] = dv[n][e] = 0.0f;
-
-  int head = -1;
-  for (int it = i0; it < i1; ++it) {
-    cp_async_wait<1>();
-    __syncthreads();
-    load(it + 2);
-    if (it / chunks != head) {  // the same for the whole CTA; the barrier above ended the old table's use
-      head = it / chunks;
-      fill_lut<NA>(p, lut, hk * p.G + head, tid, kBThreads);
-      __syncthreads();
-    }
-    const int st = it % kBStages;
-    const uint4* qt = qs + st * C::kTile;
-    const uint4* dt = ds + st * C::kTile;
-    const int* pt = ps + st * kBChunk * NA;
-    const float* lt = ls + st * 3 * kBChunk;
-#pragma unroll 1
-    for (int half = 0; half < 2; ++half) {
-      const int qb = half * 32, left = nq - it % chunks * kBChunk - qb;
-      if (left <= 0 || wrow >= khi) break;
-      float s[4][4], dp[4][4];
-#pragma unroll
-      for (int n = 0; n < 4; ++n) {
-        uint32_t b[D / 8];
-        load_b_rows<D>(b, qt, qb + n * 8, lane);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) s[n][e] = dp[n][e] = 0.0f;
-#pragma unroll
-        for (int d = 0; d < D / 16; ++d) mma_bf16_16816(s[n], ka[d], b + 2 * d);
-        load_b_rows<D>(b, dt, qb + n * 8, lane);
-#pragma unroll
-        for (int d = 0; d < D / 16; ++d) mma_bf16_16816(dp[n], va[d], b + 2 * d);
-      }
-      int uni[NA];
-      bool all_uni = true;
-      float ub = 0.0f;
-#pragma unroll
-      for (int a = 0; a < NA; ++a) {
-        const int x = pt[(qb + lane) * NA + a];
-        uni[a] = uniform_index(k_lo[a], k_hi[a], __reduce_min_sync(0xffffffffu, x),
-                               __reduce_max_sync(0xffffffffu, x), p.maxd);
-        all_uni = all_uni && uni[a] >= 0;
-        if (uni[a] >= 0) ub += lut[a * (top + 1) + uni[a]];
-      }
-      all_uni = all_uni && fabsf(ub) < kFoldLimit;
-      if (!all_uni) {
-#pragma unroll
-        for (int n = 0; n < 4; ++n)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) s[n][e] = fmaf(s[n][e], p.scale, ub);
-#pragma unroll
-        for (int a = 0; a < NA; ++a) {
-          if (uni[a] >= 0) continue;
-          const float* la = lut + a * (top + 1);
-#pragma unroll
-          for (int n = 0; n < 4; ++n)
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              const int x = -pt[(qb + n * 8 + 2 * tq + e) * NA + a];
-#pragma unroll
-              for (int i = 0; i < 2; ++i) s[n][2 * i + e] += la[clamp_index(x, kp[i][a], top)];
-            }
-        }
-      }
-      // s becomes dS^T, dp becomes P^T
-      const float x = p.scale * kLog2e;
-#pragma unroll
-      for (int n = 0; n < 4; ++n)
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const int col = n * 8 + 2 * tq + e;
-          float lse = lt[qb + col];
-          const float delta = lt[kBChunk + qb + col], corr = lt[2 * kBChunk + qb + col];
-          if (lse == -INFINITY || col >= left) lse = INFINITY;  // no key, or no query: P = 0
-          const float cst = fmaf(ub - lse, kLog2e, -corr);
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const float t = s[n][2 * i + e];
-            const float pr = fast_exp2(all_uni ? fmaf(t, x, cst) : fmaf(t - lse, kLog2e, -corr));
-            s[n][2 * i + e] = pr * (dp[n][2 * i + e] - delta);
-            dp[n][2 * i + e] = pr;
-          }
-        }
-      uint32_t sa[2][4], pa[2][4];
-#pragma unroll
-      for (int n = 0; n < 4; ++n)
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          sa[n >> 1][(n & 1) * 2 + i] = pack_bf16x2(s[n][2 * i], s[n][2 * i + 1]);
-          pa[n >> 1][(n & 1) * 2 + i] = pack_bf16x2(dp[n][2 * i], dp[n][2 * i + 1]);
-        }
-#pragma unroll
-      for (int j = 0; j < 2; ++j)
-#pragma unroll
-        for (int dc = 0; dc < D / 8; dc += 2) {
-          uint32_t b[4];
-          load_b_cols<D>(b, qt, qb + j * 16, dc, lane);
-          mma_bf16_16816(dk[dc], sa[j], b);
-          mma_bf16_16816(dk[dc + 1], sa[j], b + 2);
-          load_b_cols<D>(b, dt, qb + j * 16, dc, lane);
-          mma_bf16_16816(dv[dc], pa[j], b);
-          mma_bf16_16816(dv[dc + 1], pa[j], b + 2);
-        }
-    }
-  }
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const int r = wrow + g + 8 * i;
-    if (r >= khi) continue;
-    const size_t at = ((size_t)r * p.Hkv + hk) * D + 2 * tq;
-    if (p.splits == 1) {
-#pragma unroll
-      for (int n = 0; n < D / 8; ++n) {
-        *reinterpret_cast<uint32_t*>(p.dk + at + n * 8) =
-            pack_bf16x2(dk[n][2 * i] * p.scale, dk[n][2 * i + 1] * p.scale);
-        *reinterpret_cast<uint32_t*>(p.dv + at + n * 8) = pack_bf16x2(dv[n][2 * i], dv[n][2 * i + 1]);
-      }
-    } else {
-      const size_t stride = (size_t)p.Nk * p.Hkv * D;
-      float* to = p.kv_part + (size_t)split * 2 * stride + at;
-#pragma unroll
-      for (int n = 0; n < D / 8; ++n) {
-        *reinterpret_cast<float2*>(to + n * 8) = make_float2(dk[n][2 * i], dk[n][2 * i + 1]);
-        *reinterpret_cast<float2*>(to + stride + n * 8) = make_float2(dv[n][2 * i], dv[n][2 * i + 1]);
-      }
-    }
-  }
 }
 
 constexpr int kSumRows = 8, kSumThreads = 256;
@@ -562,7 +672,7 @@ __global__ void __launch_bounds__(kSumThreads) rp_dkv_join_kernel(const Params p
     }
     const float f = is_v ? 1.0f : p.scale;
     *reinterpret_cast<uint2*>((is_v ? p.dv : p.dk) + at) =
-        make_uint2(pack_bf16x2(x.x * f, x.y * f), pack_bf16x2(x.z * f, x.w * f));
+        make_uint2(pack2(x.x * f, x.y * f), pack2(x.z * f, x.w * f));
   }
 }
 
@@ -574,24 +684,42 @@ static bool allow_smem(K kernel, size_t bytes) {
          cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes) == cudaSuccess;
 }
 
+template <int D, int NA, int MT, bool kExact>
+static lsrm_status run_dq(const Params& p, const BwdPlan& b, cudaStream_t s) {
+  const size_t bytes = BwdCfg<D, NA>::smem_dq(p.maxd);
+  if (!allow_smem(rp_dq_kernel<D, NA, MT, kExact>, bytes)) return LSRM_ERR_CUDA;
+  rp_dq_kernel<D, NA, MT, kExact><<<(unsigned)(b.dq_tiles * p.Hq), kBThreads, bytes, s>>>(p);
+  return launched();
+}
+template <int D, int NA, int MT>
+static lsrm_status run_dkv(const Params& p, const BwdPlan& b, cudaStream_t s) {
+  const size_t bytes = BwdCfg<D, NA>::smem_dkv(p.maxd, p.NB);
+  if (!allow_smem(rp_dkv_kernel<D, NA, MT>, bytes)) return LSRM_ERR_CUDA;
+  rp_dkv_kernel<D, NA, MT><<<(unsigned)(b.kv_tiles * p.Hkv * p.splits), kBThreads, bytes, s>>>(p);
+  return launched();
+}
+
 template <int D, int NA>
 static lsrm_status run_bwd(const Params& p, const BwdPlan& b, cudaStream_t s) {
   lsrm_status st = LSRM_OK;
-  const int bins = NA * p.NB;
   if (p.Nq > 0) {
-    const size_t bytes = BwdCfg<D, NA>::smem_dq(p.maxd, p.NB);
-    if (!allow_smem(rp_dq_kernel<D, NA>, bytes)) return LSRM_ERR_CUDA;
-    rp_dq_kernel<D, NA><<<(unsigned)(b.dq_tiles * p.Hq), kBThreads, bytes, s>>>(p);
-    if ((st = launched()) != LSRM_OK) return st;
+    st = b.exact ? run_dq<D, NA, 1, true>(p, b, s) : run_dq<D, NA, 2, false>(p, b, s);
+    if (st != LSRM_OK) return st;
   }
+  if (p.Nk > 0) {
+    if (D == 32 && b.kv_rows == 128)
+      st = run_dkv<D, NA, D == 32 ? 2 : 1>(p, b, s);
+    else
+      st = run_dkv<D, NA, 1>(p, b, s);
+    if (st != LSRM_OK) return st;
+    if (p.splits > 1) {
+      rp_dkv_join_kernel<D><<<(unsigned)(p.Nk / kSumRows + p.S), kSumThreads, 0, s>>>(p);
+      if ((st = launched()) != LSRM_OK) return st;
+    }
+  }
+  const int bins = NA * p.NB;
   rp_table_kernel<<<dim3((unsigned)((bins + 31) / 32), (unsigned)p.Hq), 1024, 0, s>>>(
-      p, p.Nq > 0 ? (int)b.dq_tiles : 0, bins);
-  if ((st = launched()) != LSRM_OK || p.Nk == 0) return st;
-  const size_t bytes = BwdCfg<D, NA>::smem_dkv(p.maxd);
-  if (!allow_smem(rp_dkv_kernel<D, NA>, bytes)) return LSRM_ERR_CUDA;
-  rp_dkv_kernel<D, NA><<<(unsigned)(b.kv_tiles * p.Hkv * p.splits), kBThreads, bytes, s>>>(p);
-  if ((st = launched()) != LSRM_OK || p.splits == 1) return st;
-  rp_dkv_join_kernel<D><<<(unsigned)(p.Nk / kSumRows + p.S), kSumThreads, 0, s>>>(p);
+      p, p.Nk > 0 ? (int)(b.kv_tiles * b.parts()) : 0, bins);
   return launched();
 }
 
