@@ -31,7 +31,7 @@ constexpr float kSlack = 8.0f;
 #ifndef RP_NT32
 #define RP_NT32 4
 #define RP_NT64 4
-#define RP_MB32 4
+#define RP_MB32 3
 #define RP_MB64 2
 #endif
 template <int D, int NA, int NW>
@@ -53,7 +53,8 @@ struct RowState {
   float m[MT][2], l[MT][2];
 };
 template <int MT, int ND>
-__device__ __forceinline__ void move_reference(RowState<MT>& st, float (&o)[MT][ND][4], const float (&mx)[MT][2]) {
+__device__ __forceinline__ void move_reference(RowState<MT>& st, float (&o)[MT][ND][4], const float (&mx)[MT][2],
+                                               float to_log2) {
   bool need = false;
 #pragma unroll
   for (int mt = 0; mt < MT; ++mt)
@@ -65,7 +66,7 @@ __device__ __forceinline__ void move_reference(RowState<MT>& st, float (&o)[MT][
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const float m = quad_max(fmaxf(mx[mt][i], st.m[mt][i]));
-      const float f = st.m[mt][i] == -INFINITY ? 0.0f : ex2((st.m[mt][i] - m) * kLog2e);
+      const float f = st.m[mt][i] == -INFINITY ? 0.0f : ex2((st.m[mt][i] - m) * to_log2);
       st.m[mt][i] = m;
       st.l[mt][i] *= f;
 #pragma unroll
@@ -114,7 +115,9 @@ __global__ void __launch_bounds__(32 * NW, FwdCfg<D, NA, NW>::kMinCtas) rp_fwd_k
   };
   load(c0);
   load(c0 + 1);
-  fill_lut<NA>(p, lut, h, tid, C::kThreads);
+  // (a row's reference and sums are in the table's units)
+  const bool small = fill_units<NA, C::kThreads>(p, lut, h, tid);
+  const float mul = small ? p.scale * kLog2e : p.scale, to_log2 = small ? 1.0f : kLog2e;
 
   // the warp's 32 rows: operands, positions and their range
   uint32_t qa[2][D / 16][4];
@@ -185,8 +188,9 @@ __global__ void __launch_bounds__(32 * NW, FwdCfg<D, NA, NW>::kMinCtas) rp_fwd_k
       for (int a = 0; a < NA; ++a)
         mode[a] = axis_mode<NA, C::kCols>(pt + kb * NA + a, q_lo[a], q_hi[a], false, p.maxd, lane, one[a], p.status);
       float base[2][2];
-      const bool fold = add_bias<NA, 2, C::NT, 1>(s, base, mode, one, pt + kb * NA, lut, top, qp, p.scale, tq);
+      const bool fold = add_bias<NA, 2, C::NT, 1>(s, base, mode, one, pt + kb * NA, lut, top, qp, mul, small, tq);
       if (left < C::kCols) {
+        keep_branch();
 #pragma unroll
         for (int n = 0; n < C::NT; ++n)
 #pragma unroll
@@ -204,9 +208,9 @@ __global__ void __launch_bounds__(32 * NW, FwdCfg<D, NA, NW>::kMinCtas) rp_fwd_k
           x = fmaxf(x, s[mt][1][2 * i + 1]);
 #pragma unroll
           for (int n = 2; n < C::NT; ++n) x = fmax3(x, s[mt][n][2 * i], s[mt][n][2 * i + 1]);
-          mx[mt][i] = fold ? fmaf(x, p.scale, base[mt][i]) : x;
+          mx[mt][i] = fold ? fmaf(x, mul, base[mt][i]) : x;
         }
-      move_reference<2, D / 8>(st, o, mx);
+      move_reference<2, D / 8>(st, o, mx, to_log2);
       // P = exp(t - m): with the bias in the scores the subtraction comes first (exact for equal scores
       // of any size); with a bias common to a row everything folds into one multiply-add
       uint32_t pa[2][C::NT / 2][4];
@@ -215,16 +219,16 @@ __global__ void __launch_bounds__(32 * NW, FwdCfg<D, NA, NW>::kMinCtas) rp_fwd_k
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           const float m = st.m[mt][i] == -INFINITY ? 0.0f : st.m[mt][i];
-          const float x = fold ? p.scale * kLog2e : kLog2e, cst = (base[mt][i] - m) * kLog2e;
+          const float cst = base[mt][i] - m;
           float sum0 = 0.0f, sum1 = 0.0f;
 #pragma unroll
           for (int n = 0; n < C::NT; ++n) {
             float p0 = s[mt][n][2 * i], p1 = s[mt][n][2 * i + 1];
             if (fold) {
-              ffma2(p0, p1, p0, p1, x, cst);
+              ffma2(p0, p1, p0, p1, mul, cst);
             } else {
               fadd2_acc(p0, p1, -m, -m);
-              fmul2(p0, p1, p0, p1, x, x);
+              if (!small) fmul2(p0, p1, p0, p1, kLog2e, kLog2e);
             }
             p0 = ex2(p0);
             p1 = ex2(p1);
@@ -256,7 +260,8 @@ __global__ void __launch_bounds__(32 * NW, FwdCfg<D, NA, NW>::kMinCtas) rp_fwd_k
       const int r = wrow + mt * 16 + g + 8 * i;
       if (r >= qhi) continue;
       const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-      const float lse = l == 0.0f ? -INFINITY : st.m[mt][i] + logf(l);
+      const float ref = small ? st.m[mt][i] * kLn2 : st.m[mt][i];
+      const float lse = l == 0.0f ? -INFINITY : ref + logf(l);
       const size_t at = (size_t)r * p.Hq + h;
       if (p.splits == 1) {
 #pragma unroll
@@ -270,7 +275,7 @@ __global__ void __launch_bounds__(32 * NW, FwdCfg<D, NA, NW>::kMinCtas) rp_fwd_k
         for (int n = 0; n < D / 8; ++n)
           *reinterpret_cast<float2*>(p.o_part + pat * D + n * 8 + 2 * tq) =
               make_float2(o[mt][n][2 * i] * inv, o[mt][n][2 * i + 1] * inv);
-        if (tq == 0) p.ml_part[pat] = make_float2(st.m[mt][i], l);
+        if (tq == 0) p.ml_part[pat] = make_float2(ref, l);
       }
     }
 }
@@ -435,6 +440,7 @@ __global__ void __launch_bounds__(kFewThreads) rp_few_kernel(const Params p) {
         }
     }
     if (left < kFewKeys) {
+      keep_branch();
 #pragma unroll
       for (int n = 0; n < 4; ++n)
 #pragma unroll
@@ -449,7 +455,7 @@ __global__ void __launch_bounds__(kFewThreads) rp_few_kernel(const Params p) {
       for (int n = 1; n < 4; ++n) x = fmaxf(fmaxf(x, s[n][2 * i]), s[n][2 * i + 1]);
       mx[0][i] = x;
     }
-    move_reference<1, D / 8>(st, o, mx);
+    move_reference<1, D / 8>(st, o, mx, kLog2e);
     uint32_t pa[2][4];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {

@@ -47,8 +47,25 @@ __device__ __forceinline__ void mma16816(float* c, const uint32_t* a, const uint
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]));
 }
 
+// r = (a0, a1) * (b, b) + (c0, c1)
+__device__ __forceinline__ void ffma2v(float& r0, float& r1, float a0, float a1, float b, float c0, float c1) {
+  uint64_t ra, rb, rc, rd;
+  asm("mov.b64 %0, {%1, %2};\n" : "=l"(ra) : "f"(a0), "f"(a1));
+  asm("mov.b64 %0, {%1, %1};\n" : "=l"(rb) : "f"(b));
+  asm("mov.b64 %0, {%1, %2};\n" : "=l"(rc) : "f"(c0), "f"(c1));
+  asm("fma.rn.ftz.f32x2 %0, %1, %2, %3;\n" : "=l"(rd) : "l"(ra), "l"(rb), "l"(rc));
+  asm("mov.b64 {%0, %1}, %2;\n" : "=f"(r0), "=f"(r1) : "l"(rd));
+}
 // In a rarely taken branch: keeps it a branch, where the compiler would rather do both sides and select
 __device__ __forceinline__ void keep_branch() { asm volatile("" ::: "memory"); }
+
+// A bias folds into the exponent's multiply-add only while it is small beside fp32's spacing: past this
+// a score is added to it first, so that scores the addition swallows (a mask of the type's lowest value)
+// count as equal, as they do in the formula's own order.  kFoldLimit is also the size of LSE where its
+// own fp32 spacing (2^-10 at 1e4) begins to lose the logarithm of the row's sum, so the backward
+// normalises such rows anew.
+constexpr float kFoldLimit = 1e4f;
+constexpr float kSmallBias = 64.0f;  // per axis: three axes in log2 units keep a spacing of 2^-15
 
 struct Params {
   const int32_t* off_q;
@@ -73,6 +90,7 @@ struct Params {
   float* tab_part;  // backward: table gradient per (key tile, part of its queries, head)
   float* kv_part;   // backward: dK / dV per split
   float* corr;      // backward: log2 of what exp(t - lse) sums to per (query, head), 0 for all but huge |lse|
+  float* lse2;      // backward: lse in log2 units with corr, +inf for a row without keys
   float* o_part;    // forward: output per key split, and its softmax reference and sum
   float2* ml_part;
   uint32_t* status;
@@ -118,16 +136,6 @@ __device__ __forceinline__ int checked_bucket(const Params& p, int i) {
     return -1;
   }
   return b;
-}
-template <int NA>
-__device__ __forceinline__ void fill_lut(const Params& p, float* lut, int h, int tid, int nthreads) {
-  const int n = 2 * p.maxd + 1;
-  for (int i = tid; i < n; i += nthreads) {
-    const int b = checked_bucket(p, i);
-#pragma unroll
-    for (int a = 0; a < NA; ++a)
-      lut[a * n + i] = b < 0 ? 0.0f : bf16_to_f32(p.table[((size_t)a * p.NB + b) * p.Hq + h]);
-  }
 }
 
 // clamp(x + y, 0, top) in one instruction; any wrap-around stays in the table
@@ -206,12 +214,13 @@ __device__ __forceinline__ float quad_max(float v) {
 }
 
 // ---- what a tile's distances have in common ----
-// Per axis, for a warp's tile of 32 or 64 columns (wide = 64) whose column positions are xs[col * NA]:
+// Per axis, for a warp's tile of 32 or 64 columns whose column positions are xs[col * NA]:
 //   kOne   every (row, column) pair has one clamped distance (all pairs at or past +-maxd, or single
 //          positions): one look-up for the tile;
 //   kLane  each lane's CW columns have one position: one look-up per row;
 //   kFour  aligned runs of four columns have one position: one look-up per row and run;
-//   kEach  a look-up per pair.
+//   kEach  a look-up per pair (following arbitrary runs with a branch per column measured 10-20% slower
+//          on every training case: the branches cost more than the look-ups they save).
 // Lattice orders (bricks, patches, frames) make the slow axes kLane or kFour; distances past
 // max_distance make kOne.  The tests cost about 20 instructions a tile and axis.
 enum : int { kOne = 0, kLane = 1, kFour = 2, kEach = 3 };
@@ -233,21 +242,40 @@ __device__ __forceinline__ int axis_mode(const int* xs, int row_lo, int row_hi, 
   return (same & kLaneMask) == kLaneMask ? kLane : (same & kFourMask) == kFourMask ? kFour : kEach;
 }
 
-// A bias common to a tile folds into the exponent's multiply-add only while it is small beside
-// fp32's spacing: past this a score is added to it first, so that scores the addition swallows (a
-// mask of the type's lowest value) count as equal, as they do in the formula's own order.
-// The same size of LSE is where its own fp32 spacing (2^-10 at 1e4) begins to lose the logarithm of
-// the row's sum, so the backward normalises such rows anew.
-constexpr float kFoldLimit = 1e4f;
+// The bias table of one head in shared memory, and whether it may fold: in log2 units (true) when every
+// entry is small or -inf, so that bias, reference and units become one multiply-add of the exponent; in
+// natural units (false) otherwise.  A CTA-wide call with barriers on both sides of the table.
+template <int NA, int NT>
+__device__ __forceinline__ bool fill_units(const Params& p, float* lut, int h, int tid) {
+  const int n = 2 * p.maxd + 1;
+  bool small = true;
+  for (int i = tid; i < n; i += NT) {
+    const int b = checked_bucket(p, i);
+#pragma unroll
+    for (int a = 0; a < NA; ++a) {
+      const float x = b < 0 ? 0.0f : bf16_to_f32(p.table[((size_t)a * p.NB + b) * p.Hq + h]);
+      small = small && (fabsf(x) <= kSmallBias || x == -INFINITY);
+      lut[a * n + i] = x;
+    }
+  }
+  const bool fold = __syncthreads_and(small);
+  if (fold) {  // every thread scales the entries that it wrote
+    for (int i = tid; i < n; i += NT)
+#pragma unroll
+      for (int a = 0; a < NA; ++a) lut[a * n + i] *= kLog2e;
+  }
+  __syncthreads();
+  return fold;
+}
 
-// The bias of a lane's MT x 2 rows by CW columns: what is constant per row goes to base, the rest is
-// added to the scores s, which become s * scale + bias when there is a rest (or when base is too
-// large to fold).  Returns whether base holds it all.  SIGN: column positions count up (+1, columns are
-// keys: rowc = maxd - pos_q) or down (-1, columns are queries: rowc = maxd + pos_k).
+// The bias of a lane's MT x 2 rows by CW columns, in the table's units.  What is constant per row goes
+// to base; when that is all and the table folds, returns true and leaves the scores raw.  Otherwise the
+// scores become s * mul + bias.  SIGN: column positions count up (+1, columns are keys: rowc = maxd - pos_q)
+// or down (-1, columns are queries: rowc = maxd + pos_k).
 template <int NA, int MT, int NT, int SIGN>
 __device__ __forceinline__ bool add_bias(float (&s)[MT][NT][4], float (&base)[MT][2], const int (&mode)[NA],
                                          const int (&one)[NA], const int* xs, const float* lut, int top,
-                                         const int (&rowc)[MT][2][NA], float scale, int tq) {
+                                         const int (&rowc)[MT][2][NA], float mul, bool fold, int tq) {
   constexpr int CW = 2 * NT;
   const int* mine = xs + tq * CW * NA;
   int worst = kOne;
@@ -257,10 +285,9 @@ __device__ __forceinline__ bool add_bias(float (&s)[MT][NT][4], float (&base)[MT
     worst = max(worst, mode[a]);
     if (mode[a] == kOne) ub += lut[a * (top + 1) + one[a]];
   }
-  bool small = fabsf(ub) < kFoldLimit;
 #pragma unroll
   for (int mt = 0; mt < MT; ++mt) base[mt][0] = base[mt][1] = ub;
-  if (worst == kOne && small) return true;
+  if (worst == kOne && fold) return true;
 #pragma unroll
   for (int a = 0; a < NA; ++a) {
     if (mode[a] != kLane) continue;
@@ -270,18 +297,14 @@ __device__ __forceinline__ bool add_bias(float (&s)[MT][NT][4], float (&base)[MT
 #pragma unroll
       for (int i = 0; i < 2; ++i) base[mt][i] += lut[a * (top + 1) + clamp_index(x, rowc[mt][i][a], top)];
   }
-  if (worst <= kLane) {
-#pragma unroll
-    for (int mt = 0; mt < MT; ++mt) small = small && fabsf(base[mt][0]) < kFoldLimit && fabsf(base[mt][1]) < kFoldLimit;
-    if (__all_sync(0xffffffffu, small)) return true;
-  }
+  if (worst <= kLane && fold) return true;
 #pragma unroll
   for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
     for (int i = 0; i < 2; ++i)
 #pragma unroll
       for (int n = 0; n < NT; ++n)
-        ffma2(s[mt][n][2 * i], s[mt][n][2 * i + 1], s[mt][n][2 * i], s[mt][n][2 * i + 1], scale, base[mt][i]);
+        ffma2(s[mt][n][2 * i], s[mt][n][2 * i + 1], s[mt][n][2 * i], s[mt][n][2 * i + 1], mul, base[mt][i]);
 #pragma unroll
   for (int a = 0; a < NA; ++a) {
     const float* la = lut + a * (top + 1);
@@ -294,8 +317,8 @@ __device__ __forceinline__ bool add_bias(float (&s)[MT][NT][4], float (&base)[MT
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
             const float b = la[clamp_index(x, rowc[mt][i][a], top)];
-            fadd2_acc(s[mt][2 * r][2 * i], s[mt][2 * r][2 * i + 1], b, b);
-            fadd2_acc(s[mt][2 * r + 1][2 * i], s[mt][2 * r + 1][2 * i + 1], b, b);
+            s[mt][2 * r][2 * i] += b, s[mt][2 * r][2 * i + 1] += b;
+            s[mt][2 * r + 1][2 * i] += b, s[mt][2 * r + 1][2 * i + 1] += b;
           }
       }
     } else if (mode[a] == kEach) {
@@ -305,13 +328,28 @@ __device__ __forceinline__ bool add_bias(float (&s)[MT][NT][4], float (&base)[MT
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-          for (int i = 0; i < 2; ++i)
-            fadd2_acc(s[mt][n][2 * i], s[mt][n][2 * i + 1], la[clamp_index(x0, rowc[mt][i][a], top)],
-                      la[clamp_index(x1, rowc[mt][i][a], top)]);
+          for (int i = 0; i < 2; ++i) {
+            // single adds: a pair of look-ups would first have to be moved into a pair of registers
+            s[mt][n][2 * i] += la[clamp_index(x0, rowc[mt][i][a], top)];
+            s[mt][n][2 * i + 1] += la[clamp_index(x1, rowc[mt][i][a], top)];
+          }
       }
     }
   }
   return false;
+}
+
+// the (head, query chunk) range of a split: whole heads, or an even part of one head's chunks
+__device__ __forceinline__ void split_range(const Params& p, int split, int chunks, int& h0, int& h1, int& c0, int& c1,
+                                            int& part) {
+  if (p.splits <= p.G) {
+    const int n = p.G / p.splits;
+    h0 = split * n, h1 = h0 + n, c0 = 0, c1 = chunks, part = 0;
+  } else {
+    const int f = p.splits / p.G, n = (chunks + f - 1) / f;
+    h0 = split / f, h1 = h0 + 1, part = split % f;
+    c0 = min(part * n, chunks), c1 = min(c0 + n, chunks);
+  }
 }
 
 // ---- launch plans and the workspace (host) ----
@@ -323,14 +361,16 @@ struct FwdPlan {
   long long ctas;
 };
 struct BwdPlan {
-  bool exact;   // short segments: 64 queries a CTA and the exact Delta in dq as well
-  int kv_rows;  // keys a CTA: 64 or 128
+  bool tc;      // the tensor-memory kernels: 128 rows a CTA
+  bool exact;   // short segments: the exact Delta in dq as well
   int splits;   // of the key pass over heads and query chunks: a divisor of G, or a multiple of it
   int g;
   long long dq_tiles, kv_tiles;
   int parts() const { return splits > g ? splits / g : 1; }  // table sums per (key tile, head)
 };
 constexpr int kExactKeys = 256;
+
+size_t bwd_tc_smem(int D, int NA, int maxd, int nb);  // of rp_dkv_tc_kernel
 
 inline FwdPlan fwd_plan(const lsrm_relpos_desc& d) {
   FwdPlan f{};
@@ -365,13 +405,15 @@ inline BwdPlan bwd_plan(const lsrm_relpos_desc& d) {
   const long long mean_q = (d.n_q_tokens + S - 1) / S, mean_k = (d.n_k_tokens + S - 1) / S;
   b.g = (int)G;
   b.exact = mean_k <= kExactKeys || mean_q <= 64;
-  b.kv_rows = d.head_dim == 32 && mean_k > 64 ? 128 : 64;
-  const int q_rows = b.exact ? 64 : 128;
-  b.dq_tiles = d.n_q_tokens / q_rows + S;
-  b.kv_tiles = d.n_k_tokens / b.kv_rows + S;
-  const long long busy = ((mean_k + b.kv_rows - 1) / b.kv_rows) * S * d.n_kv_heads;
+  b.tc = !b.exact && mean_q > 128 &&
+         bwd_tc_smem(d.head_dim, d.n_axes, d.max_distance, d.n_buckets) <= 227 * 1024;
+  const int rows = b.tc ? 128 : 64;
+  b.dq_tiles = d.n_q_tokens / rows + S;
+  b.kv_tiles = d.n_k_tokens / rows + S;
+  const long long busy = ((mean_k + rows - 1) / rows) * S * d.n_kv_heads;
   const long long qchunks = (mean_q + 63) / 64;
-  long long sp = busy > 0 ? (3 * kSms + busy - 1) / busy : 1;
+  const long long want = (b.tc ? 2 : 3) * kSms;
+  long long sp = busy > 0 ? (want + busy - 1) / busy : 1;
   if (sp > 64 * G) sp = 64 * G;
   if (sp < G) {
     while (G % sp) ++sp;  // whole heads, evenly
@@ -385,7 +427,7 @@ inline BwdPlan bwd_plan(const lsrm_relpos_desc& d) {
 }
 
 struct Ws {
-  size_t status, o_part, ml_part, delta, corr, tab_part, kv_part, total;
+  size_t status, o_part, ml_part, delta, corr, lse2, tab_part, kv_part, total;
 };
 inline size_t up256(size_t x) { return (x + 255) & ~size_t(255); }
 // the forward's and the backward's scratch share the space behind the status word
@@ -401,7 +443,8 @@ inline Ws ws_layout(const lsrm_relpos_desc& d) {
   const size_t fwd = up256(w.ml_part + parts * 8);
   w.delta = o;
   w.corr = up256(w.delta + rows * 4);
-  w.tab_part = up256(w.corr + rows * 4);
+  w.lse2 = up256(w.corr + rows * 4);
+  w.tab_part = up256(w.lse2 + rows * 4);
   w.kv_part = up256(w.tab_part + (size_t)b.kv_tiles * b.parts() * d.n_q_heads * d.n_axes * d.n_buckets * 4);
   const size_t kv = b.splits > 1 ? (size_t)b.splits * 2 * d.n_k_tokens * d.n_kv_heads * D : 0;
   const size_t bwd = up256(w.kv_part + kv * 4);

@@ -64,6 +64,7 @@ rp::Params params_of(const lsrm_relpos_desc& d, const int32_t* off_q, const int3
   p.ml_part = reinterpret_cast<float2*>(base + w.ml_part);
   p.delta = reinterpret_cast<float*>(base + w.delta);
   p.corr = reinterpret_cast<float*>(base + w.corr);
+  p.lse2 = reinterpret_cast<float*>(base + w.lse2);
   p.tab_part = reinterpret_cast<float*>(base + w.tab_part);
   p.kv_part = reinterpret_cast<float*>(base + w.kv_part);
   p.status = reinterpret_cast<uint32_t*>(base + w.status);

@@ -39,8 +39,8 @@ struct BwdCfg {
   __host__ __device__ static size_t lut(int maxd) { return (((size_t)NA * (2 * maxd + 1) * 4) + 15) & ~(size_t)15; }
   static size_t smem_dq(int maxd) { return kRing + lut(maxd); }
   static size_t smem_dkv(int maxd, int nb) {
-    return kRing + (size_t)kBStages * kBChunk * 12 + lut(maxd) + (size_t)NA * nb * kBThreads * 4 +
-           (((size_t)2 * maxd + 1 + 15) & ~(size_t)15);
+    return kRing + (size_t)kBStages * kBChunk * 8 + lut(maxd) + (size_t)NA * (nb + 1) * kBThreads * 4 +
+           ((size_t)2 * maxd + 1) * 4;
   }
 };
 
@@ -48,8 +48,9 @@ struct BwdCfg {
 // (every key masked by a huge finite bias): corr = log2 sum_j exp(t - lse), a row at a time, lanes over
 // keys.  The tile's rows are wrow .. wrow + 15; lane (g, .) holds the LSE of rows g and g + 8.
 template <int D, int NA>
-__device__ __noinline__ float2 huge_rows(const Params& p, const float* lut, float lse0, float lse1, int wrow, int h,
-                                         int hk, int klo, int khi, int lane) {
+__device__ __noinline__ float2 huge_rows(const Params& p, const float* lut, bool small, float lse0, float lse1,
+                                         int wrow, int h, int hk, int klo, int khi, int lane) {
+  const float units = small ? kLn2 : 1.0f;  // the table's to natural ones
   float2 corr = make_float2(0.0f, 0.0f);
   for (int r = 0; r < 16; ++r) {
     const float l = __shfl_sync(0xffffffffu, r < 8 ? lse0 : lse1, (r & 7) * 4);
@@ -63,8 +64,8 @@ __device__ __noinline__ float2 huge_rows(const Params& p, const float* lut, floa
       for (int d = 0; d < D; ++d) t = fmaf(bf16_to_f32(q[d]), bf16_to_f32(k[d]), t);
       t *= p.scale;
       for (int a = 0; a < NA; ++a)
-        t += lut[a * (2 * p.maxd + 1) + clamp_index(p.pos_k[(size_t)j * NA + a], p.maxd - p.pos_q[row * NA + a],
-                                                    2 * p.maxd)];
+        t += units * lut[a * (2 * p.maxd + 1) + clamp_index(p.pos_k[(size_t)j * NA + a],
+                                                            p.maxd - p.pos_q[row * NA + a], 2 * p.maxd)];
       sum += ex2((t - l) * kLog2e);
     }
     for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
@@ -74,7 +75,7 @@ __device__ __noinline__ float2 huge_rows(const Params& p, const float* lut, floa
 }
 
 template <int D, int NA, int MT, bool kExact>
-__global__ void __launch_bounds__(kBThreads) rp_dq_kernel(const Params p) {
+__global__ void __launch_bounds__(kBThreads, D == 32 ? 3 : 2) rp_dq_kernel(const Params p) {
   using C = BwdCfg<D, NA>;
   constexpr int kRows = 64 * MT;
   extern __shared__ __align__(16) unsigned char smem_raw[];
@@ -105,7 +106,8 @@ __global__ void __launch_bounds__(kBThreads) rp_dq_kernel(const Params p) {
   };
   load(0);
   load(1);
-  fill_lut<NA>(p, lut, h, tid, kBThreads);
+  const bool small = fill_units<NA, kBThreads>(p, lut, h, tid);
+  const float mul = small ? p.scale * kLog2e : p.scale;
 
   uint32_t qa[MT][D / 16][4], da[MT][D / 16][4];
   int qp[MT][2][NA], q_lo[NA], q_hi[NA];
@@ -155,14 +157,27 @@ __global__ void __launch_bounds__(kBThreads) rp_dq_kernel(const Params p) {
     q_hi[a] = __reduce_max_sync(0xffffffffu, q_hi[a]);
     if (q_lo[a] < -kPosLimit || q_hi[a] > kPosLimit) raise_status(p.status, LSRM_ERR_BOUNDS);
   }
-  __syncthreads();  // the bias table
   if (__any_sync(0xffffffffu, huge)) {
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt) {
-      const float2 x = huge_rows<D, NA>(p, lut, lse[mt][0], lse[mt][1], wrow + mt * 16, h, hk, klo, khi, lane);
+      const float2 x = huge_rows<D, NA>(p, lut, small, lse[mt][0], lse[mt][1], wrow + mt * 16, h, hk, klo, khi, lane);
       corr[mt][0] = x.x, corr[mt][1] = x.y;
     }
   }
+  // the exponent's row constant: log2 units with the correction, or natural ones without it
+  float row[MT][2];
+#pragma unroll
+  for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const float l2 = fmaf(lse[mt][i], kLog2e, corr[mt][i]);
+      const int r = wrow + mt * 16 + g + 8 * i;
+      if (r < qhi && tq == 0) {
+        p.lse2[(size_t)r * p.Hq + h] = l2;
+        p.corr[(size_t)r * p.Hq + h] = corr[mt][i];
+      }
+      row[mt][i] = small ? l2 : lse[mt][i];
+    }
   float dq[MT][D / 8][4], pk[kExact ? MT : 1][kExact ? D / 8 : 1][4];
 #pragma unroll
   for (int mt = 0; mt < MT; ++mt)
@@ -208,7 +223,7 @@ __global__ void __launch_bounds__(kBThreads) rp_dq_kernel(const Params p) {
       for (int a = 0; a < NA; ++a)
         mode[a] = axis_mode<NA, kBCols>(pt + a, q_lo[a], q_hi[a], false, p.maxd, lane, one[a], p.status);
       float base[MT][2];
-      const bool fold = add_bias<NA, MT, kBNT, 1>(s, base, mode, one, pt, lut, top, qp, p.scale, tq);
+      const bool fold = add_bias<NA, MT, kBNT, 1>(s, base, mode, one, pt, lut, top, qp, mul, small, tq);
       if (left < kBCols) {
         keep_branch();
 #pragma unroll
@@ -224,17 +239,16 @@ __global__ void __launch_bounds__(kBThreads) rp_dq_kernel(const Params p) {
       for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          const float x = fold ? p.scale * kLog2e : kLog2e, l = lse[mt][i];
-          const float cst = fmaf(fold ? base[mt][i] - l : -l, kLog2e, -corr[mt][i]);
+          const float cst = base[mt][i] - row[mt][i];
           float sum0 = 0.0f, sum1 = 0.0f;
 #pragma unroll
           for (int n = 0; n < kBNT; ++n) {
             float p0 = s[mt][n][2 * i], p1 = s[mt][n][2 * i + 1];
             if (fold) {
-              ffma2(p0, p1, p0, p1, x, cst);
+              ffma2(p0, p1, p0, p1, mul, cst);
             } else {  // the subtraction first: exact for scores of any size
-              fadd2_acc(p0, p1, -l, -l);
-              ffma2(p0, p1, p0, p1, kLog2e, -corr[mt][i]);
+              fadd2_acc(p0, p1, -row[mt][i], -row[mt][i]);
+              if (!small) ffma2(p0, p1, p0, p1, kLog2e, -corr[mt][i]);
             }
             p0 = ex2(p0);
             p1 = ex2(p1);
@@ -273,10 +287,7 @@ __global__ void __launch_bounds__(kBThreads) rp_dq_kernel(const Params p) {
       const int r = wrow + mt * 16 + g + 8 * i;
       if (r >= qhi) continue;
       const size_t at = (size_t)r * p.Hq + h;
-      if (tq == 0) {
-        p.delta[at] = delta[mt][i] + more;
-        p.corr[at] = corr[mt][i];
-      }
+      if (tq == 0) p.delta[at] = delta[mt][i] + more;
       uint16_t* to = p.dq + at * D + 2 * tq;
 #pragma unroll
       for (int n = 0; n < D / 8; ++n) {
@@ -290,39 +301,27 @@ __global__ void __launch_bounds__(kBThreads) rp_dq_kernel(const Params p) {
     }
 }
 
-// hist[b0] += v0, hist[b1] += v1 (entries of the thread's own column) with both reads ahead of both
-// writes: one latency for two, and right when the buckets are the same
-__device__ __forceinline__ void add_two(float* col, int b0, float v0, int b1, float v1) {
-  const float h0 = col[b0 * kBThreads], h1 = col[b1 * kBThreads];
-  col[b1 * kBThreads] = h1 + v1;
-  col[b0 * kBThreads] = h0 + v0 + (b0 == b1 ? v1 : 0.0f);
-}
-
-// the (head, query chunk) range of a split: whole heads, or an even part of one head's chunks
-__device__ __forceinline__ void split_range(const Params& p, int split, int chunks, int& h0, int& h1, int& c0, int& c1,
-                                            int& part) {
-  if (p.splits <= p.G) {
-    const int n = p.G / p.splits;
-    h0 = split * n, h1 = h0 + n, c0 = 0, c1 = chunks, part = 0;
-  } else {
-    const int f = p.splits / p.G, n = (chunks + f - 1) / f;
-    h0 = split / f, h1 = h0 + 1, part = split % f;
-    c0 = min(part * n, chunks), c1 = min(c0 + n, chunks);
-  }
+// two sums into the thread's own column (byte offsets of the buckets' entries) with both reads ahead of
+// both writes: one latency for two, and right when the buckets are the same
+__device__ __forceinline__ void add_two(char* col, int b0, float v0, int b1, float v1) {
+  float *p0 = reinterpret_cast<float*>(col + b0), *p1 = reinterpret_cast<float*>(col + b1);
+  const float x0 = *p0, x1 = *p1;
+  *p1 = x1 + v1;
+  *p0 = x0 + v0 + (b0 == b1 ? v1 : 0.0f);
 }
 
 template <int D, int NA, int MT>
-__global__ void __launch_bounds__(kBThreads) rp_dkv_kernel(const Params p) {
+__global__ void __launch_bounds__(kBThreads, D == 32 ? 4 : 2) rp_dkv_kernel(const Params p) {
   using C = BwdCfg<D, NA>;
   constexpr int kRows = 64 * MT;
   extern __shared__ __align__(16) unsigned char smem_raw[];
   uint4* qs = reinterpret_cast<uint4*>(smem_raw);
   uint4* ds = qs + kBStages * C::kTile;
   int* ps = reinterpret_cast<int*>(ds + kBStages * C::kTile);
-  float* ls = reinterpret_cast<float*>(smem_raw + C::kRing);  // [stage][3][chunk]: LSE, Delta, corr
-  float* lut = ls + kBStages * 3 * kBChunk;
-  float* hist = lut + C::lut(p.maxd) / 4;  // [NA * NB][threads]
-  uint8_t* bk = reinterpret_cast<uint8_t*>(hist + (size_t)NA * p.NB * kBThreads);
+  float* ls = reinterpret_cast<float*>(smem_raw + C::kRing);  // [stage][2][chunk]: LSE (log2 units), Delta
+  float* lut = ls + kBStages * 2 * kBChunk;
+  float* hist = lut + C::lut(p.maxd) / 4;  // [NA][NB and one for ids out of range][threads]
+  int* boff = reinterpret_cast<int*>(hist + (size_t)NA * (p.NB + 1) * kBThreads);  // a bucket's byte offset
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, tq = lane & 3;
   const int bins = NA * p.NB;
@@ -355,10 +354,9 @@ __global__ void __launch_bounds__(kBThreads) rp_dkv_kernel(const Params p) {
       load_tile<D, kBCW, kBChunk, kBThreads>(ds + st * C::kTile, p.dout, q0, n, p.Hq, h, tid);
       for (int i = tid; i < kBChunk * NA; i += kBThreads)
         cp_async4(ps + st * kBChunk * NA + i, p.pos_q + (size_t)(q0 + min(i / NA, n - 1)) * NA + i % NA, true);
-      for (int i = tid; i < 3 * kBChunk; i += kBThreads) {
-        const float* src = i < kBChunk ? p.lse_in : i < 2 * kBChunk ? p.delta : p.corr;
-        cp_async4(ls + st * 3 * kBChunk + i, src + (size_t)(q0 + min(i % kBChunk, n - 1)) * p.Hq + h, true);
-      }
+      static_assert(kBThreads == 2 * kBChunk, "one row constant a thread");
+      cp_async4(ls + st * 2 * kBChunk + tid,
+                (tid < kBChunk ? p.lse2 : p.delta) + (size_t)(q0 + min(tid % kBChunk, n - 1)) * p.Hq + h, true);
     }
     cp_async_commit();
   };
@@ -366,10 +364,11 @@ __global__ void __launch_bounds__(kBThreads) rp_dkv_kernel(const Params p) {
   load(1);
   for (int i = tid; i < top + 1; i += kBThreads) {
     const int b = p.bucket_of[i];
-    bk[i] = (uint8_t)(b < 0 || b >= p.NB ? 255 : b);
+    boff[i] = (b < 0 || b >= p.NB ? p.NB : b) * kBThreads * 4;
   }
-  for (int b = 0; b < bins; ++b) hist[b * kBThreads + tid] = 0.0f;  // the thread's own column
-  float* col = hist + tid;
+  for (int b = 0; b < bins + NA; ++b) hist[b * kBThreads + tid] = 0.0f;  // the thread's own column
+  char* col = reinterpret_cast<char*>(hist + tid);
+  const int axis_bytes = (p.NB + 1) * kBThreads * 4;
 
   uint32_t ka[MT][D / 16][4], va[MT][D / 16][4];
   int kp[MT][2][NA], k_lo[NA], k_hi[NA];
@@ -408,22 +407,22 @@ __global__ void __launch_bounds__(kBThreads) rp_dkv_kernel(const Params p) {
   float run[NA];
   int run_b[NA];
 #pragma unroll
-  for (int a = 0; a < NA; ++a) run[a] = 0.0f, run_b[a] = 255;
+  for (int a = 0; a < NA; ++a) run[a] = 0.0f, run_b[a] = p.NB * kBThreads * 4;
   // the head's sums of the CTA's threads to global memory, and the columns back to 0
   auto flush = [&](int head) {
 #pragma unroll
     for (int a = 0; a < NA; ++a) {
-      if (run_b[a] != 255) col[(a * p.NB + run_b[a]) * kBThreads] += run[a];
+      *reinterpret_cast<float*>(col + a * axis_bytes + run_b[a]) += run[a];
       run[a] = 0.0f;
-      run_b[a] = 255;
     }
     __syncthreads();
     for (int b = warp; b < bins; b += kBThreads / 32) {
+      float* of = hist + (b + b / p.NB) * kBThreads + lane;  // past each axis' entry for ids out of range
       float x = 0.0f;
 #pragma unroll
       for (int t = 0; t < kBThreads; t += 32) {
-        x += hist[b * kBThreads + t + lane];
-        hist[b * kBThreads + t + lane] = 0.0f;
+        x += of[t];
+        of[t] = 0.0f;
       }
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
@@ -432,14 +431,16 @@ __global__ void __launch_bounds__(kBThreads) rp_dkv_kernel(const Params p) {
     __syncthreads();
   };
 
+  bool small = false;
+  float mul = 0.0f;
   for (int it = 0; it < steps; ++it) {
     const int head = h0 + it / nc, cc = it % nc;
     cp_async_wait<1>();
     __syncthreads();
     load(it + 2);
     if (cc == 0) {  // the barriers since the last head's tiles ended the old table's use
-      fill_lut<NA>(p, lut, hk * p.G + head, tid, kBThreads);
-      __syncthreads();
+      small = fill_units<NA, kBThreads>(p, lut, hk * p.G + head, tid);
+      mul = small ? p.scale * kLog2e : p.scale;
     }
     const int st = it % kBStages;
     const uint4* qt = qs + st * C::kTile;
@@ -449,7 +450,7 @@ __global__ void __launch_bounds__(kBThreads) rp_dkv_kernel(const Params p) {
       const int left = nq - (c0 + cc) * kBChunk - qb;
       if (left <= 0 || wrow >= khi) break;
       const int* pt = ps + st * kBChunk * NA + qb * NA;
-      const float* lt = ls + st * 3 * kBChunk + qb + tq * kBCW;
+      const float* lt = ls + st * 2 * kBChunk + qb + tq * kBCW;
       float s[MT][kBNT][4], dp[MT][kBNT][4];
 #pragma unroll
       for (int n = 0; n < kBNT; ++n) {
@@ -473,33 +474,66 @@ __global__ void __launch_bounds__(kBThreads) rp_dkv_kernel(const Params p) {
       for (int a = 0; a < NA; ++a)
         mode[a] = axis_mode<NA, kBCols>(pt + a, k_lo[a], k_hi[a], true, p.maxd, lane, one[a], p.status);
       float base[MT][2];
-      const bool fold = add_bias<NA, MT, kBNT, -1>(s, base, mode, one, pt, lut, top, kp, p.scale, tq);
+      const bool fold = add_bias<NA, MT, kBNT, -1>(s, base, mode, one, pt, lut, top, kp, mul, small, tq);
+      bool flat = true;  // one bias for the tile
+#pragma unroll
+      for (int a = 0; a < NA; ++a) flat = flat && mode[a] == kOne;
       // s becomes dS^T, dp becomes P^T
-      const float x = p.scale * kLog2e;
 #pragma unroll
       for (int n = 0; n < kBNT; ++n) {
         float2 l = *reinterpret_cast<const float2*>(lt + 2 * n);
         const float2 dl = *reinterpret_cast<const float2*>(lt + kBChunk + 2 * n);
-        const float2 cr = *reinterpret_cast<const float2*>(lt + 2 * kBChunk + 2 * n);
-        const int c = tq * kBCW + 2 * n;
-        if (l.x == -INFINITY || c >= left) l.x = INFINITY;  // no key, or no query: P = 0
-        if (l.y == -INFINITY || c + 1 >= left) l.y = INFINITY;
+        if (left < kBCols) {  // no query: P = 0
+          keep_branch();
+          if (tq * kBCW + 2 * n >= left) l.x = INFINITY;
+          if (tq * kBCW + 2 * n + 1 >= left) l.y = INFINITY;
+        }
+        if (small) {
+          if (fold) {
+            const float c0 = flat ? base[0][0] - l.x : -l.x, c1 = flat ? base[0][0] - l.y : -l.y;
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+              for (int i = 0; i < 2; ++i) {
+                float d0 = c0, d1 = c1;
+                if (!flat) fadd2_acc(d0, d1, base[mt][i], base[mt][i]);
+                ffma2v(s[mt][n][2 * i], s[mt][n][2 * i + 1], s[mt][n][2 * i], s[mt][n][2 * i + 1], mul, d0, d1);
+              }
+          } else {
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+              for (int i = 0; i < 2; ++i) fadd2_acc(s[mt][n][2 * i], s[mt][n][2 * i + 1], -l.x, -l.y);
+          }
+        } else {
+          // natural units, the subtraction first: exact for scores of any size
+          keep_branch();
+          float ln[2], cr[2];
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const bool there = tq * kBCW + 2 * n + e < left;
+            const size_t at = (size_t)(qlo + (c0 + cc) * kBChunk + qb + (there ? tq * kBCW + 2 * n + e : 0)) * p.Hq +
+                              hk * p.G + head;
+            ln[e] = there ? p.lse_in[at] : INFINITY;
+            if (ln[e] == -INFINITY) ln[e] = INFINITY;
+            cr[e] = there ? p.corr[at] : 0.0f;
+          }
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+              for (int e = 0; e < 2; ++e)
+                s[mt][n][2 * i + e] = fmaf(s[mt][n][2 * i + e] - ln[e], kLog2e, -cr[e]);
+        }
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
-            float p0 = s[mt][n][2 * i], p1 = s[mt][n][2 * i + 1];
-            if (fold) {
-              p0 = fmaf(p0, x, fmaf(base[mt][i] - l.x, kLog2e, -cr.x));
-              p1 = fmaf(p1, x, fmaf(base[mt][i] - l.y, kLog2e, -cr.y));
-            } else {
-              p0 = fmaf(p0 - l.x, kLog2e, -cr.x);
-              p1 = fmaf(p1 - l.y, kLog2e, -cr.y);
-            }
-            p0 = ex2(p0);
-            p1 = ex2(p1);
-            s[mt][n][2 * i] = p0 * (dp[mt][n][2 * i] - dl.x);
-            s[mt][n][2 * i + 1] = p1 * (dp[mt][n][2 * i + 1] - dl.y);
+            const float p0 = ex2(s[mt][n][2 * i]), p1 = ex2(s[mt][n][2 * i + 1]);
+            float d0 = dp[mt][n][2 * i], d1 = dp[mt][n][2 * i + 1];
+            fadd2_acc(d0, d1, -dl.x, -dl.y);
+            fmul2(s[mt][n][2 * i], s[mt][n][2 * i + 1], d0, d1, p0, p1);
             dp[mt][n][2 * i] = p0;
             dp[mt][n][2 * i + 1] = p1;
           }
@@ -517,12 +551,11 @@ __global__ void __launch_bounds__(kBThreads) rp_dkv_kernel(const Params p) {
       // the table's gradient
 #pragma unroll
       for (int a = 0; a < NA; ++a) {
-        float* ca = col + a * p.NB * kBThreads;
-        const int* xs = pt + tq * kBCW * NA + a;
+        char* ca = col + a * axis_bytes;
         if (mode[a] == kOne) {
-          const int b = bk[one[a]];
+          const int b = boff[one[a]];
           if (b != run_b[a]) {
-            if (run_b[a] != 255) ca[run_b[a] * kBThreads] += run[a];
+            *reinterpret_cast<float*>(ca + run_b[a]) += run[a];
             run[a] = 0.0f;
             run_b[a] = b;
           }
@@ -537,37 +570,25 @@ __global__ void __launch_bounds__(kBThreads) rp_dkv_kernel(const Params p) {
           run[a] += sum0 + sum1;
         } else if (mode[a] <= kFour) {
           // runs of eight or four queries on one position
+          const int x0 = -pt[tq * kBCW * NA + a], x1 = -pt[(tq * kBCW + 4) * NA + a];
 #pragma unroll
           for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              const float lo = (s[mt][0][2 * i] + s[mt][0][2 * i + 1]) + (s[mt][1][2 * i] + s[mt][1][2 * i + 1]);
-              const float hi = (s[mt][2][2 * i] + s[mt][2][2 * i + 1]) + (s[mt][3][2 * i] + s[mt][3][2 * i + 1]);
-              const int b0 = bk[clamp_index(-xs[0], kp[mt][i][a], top)];
-              const int b1 = bk[clamp_index(-xs[4 * NA], kp[mt][i][a], top)];
-              if (b0 != 255 && b1 != 255) {
-                add_two(ca, b0, lo, b1, hi);
-              } else {
-                if (b0 != 255) ca[b0 * kBThreads] += lo;
-                if (b1 != 255) ca[b1 * kBThreads] += hi;
-              }
-            }
+            for (int i = 0; i < 2; ++i)
+              add_two(ca, boff[clamp_index(x0, kp[mt][i][a], top)],
+                      (s[mt][0][2 * i] + s[mt][0][2 * i + 1]) + (s[mt][1][2 * i] + s[mt][1][2 * i + 1]),
+                      boff[clamp_index(x1, kp[mt][i][a], top)],
+                      (s[mt][2][2 * i] + s[mt][2][2 * i + 1]) + (s[mt][3][2 * i] + s[mt][3][2 * i + 1]));
         } else {
 #pragma unroll
           for (int n = 0; n < kBNT; ++n) {
-            const int x0 = -xs[2 * n * NA], x1 = -xs[(2 * n + 1) * NA];
+            const int x0 = -pt[(tq * kBCW + 2 * n) * NA + a], x1 = -pt[(tq * kBCW + 2 * n + 1) * NA + a];
 #pragma unroll
             for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-              for (int i = 0; i < 2; ++i) {
-                const int b0 = bk[clamp_index(x0, kp[mt][i][a], top)], b1 = bk[clamp_index(x1, kp[mt][i][a], top)];
-                if (b0 != 255 && b1 != 255) {
-                  add_two(ca, b0, s[mt][n][2 * i], b1, s[mt][n][2 * i + 1]);
-                } else {
-                  if (b0 != 255) ca[b0 * kBThreads] += s[mt][n][2 * i];
-                  if (b1 != 255) ca[b1 * kBThreads] += s[mt][n][2 * i + 1];
-                }
-              }
+              for (int i = 0; i < 2; ++i)
+                add_two(ca, boff[clamp_index(x0, kp[mt][i][a], top)], s[mt][n][2 * i],
+                        boff[clamp_index(x1, kp[mt][i][a], top)], s[mt][n][2 * i + 1]);
           }
         }
       }
@@ -684,34 +705,35 @@ static bool allow_smem(K kernel, size_t bytes) {
          cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes) == cudaSuccess;
 }
 
-template <int D, int NA, int MT, bool kExact>
+template <int D, int NA, bool kExact>
 static lsrm_status run_dq(const Params& p, const BwdPlan& b, cudaStream_t s) {
   const size_t bytes = BwdCfg<D, NA>::smem_dq(p.maxd);
-  if (!allow_smem(rp_dq_kernel<D, NA, MT, kExact>, bytes)) return LSRM_ERR_CUDA;
-  rp_dq_kernel<D, NA, MT, kExact><<<(unsigned)(b.dq_tiles * p.Hq), kBThreads, bytes, s>>>(p);
+  if (!allow_smem(rp_dq_kernel<D, NA, 1, kExact>, bytes)) return LSRM_ERR_CUDA;
+  rp_dq_kernel<D, NA, 1, kExact><<<(unsigned)(b.dq_tiles * p.Hq), kBThreads, bytes, s>>>(p);
   return launched();
 }
-template <int D, int NA, int MT>
+template <int D, int NA>
 static lsrm_status run_dkv(const Params& p, const BwdPlan& b, cudaStream_t s) {
   const size_t bytes = BwdCfg<D, NA>::smem_dkv(p.maxd, p.NB);
-  if (!allow_smem(rp_dkv_kernel<D, NA, MT>, bytes)) return LSRM_ERR_CUDA;
-  rp_dkv_kernel<D, NA, MT><<<(unsigned)(b.kv_tiles * p.Hkv * p.splits), kBThreads, bytes, s>>>(p);
+  if (!allow_smem(rp_dkv_kernel<D, NA, 1>, bytes)) return LSRM_ERR_CUDA;
+  rp_dkv_kernel<D, NA, 1><<<(unsigned)(b.kv_tiles * p.Hkv * p.splits), kBThreads, bytes, s>>>(p);
   return launched();
 }
+
+lsrm_status launch_bwd_tc(const Params& p, int D, int NA, const BwdPlan& b, cudaStream_t s);
 
 template <int D, int NA>
 static lsrm_status run_bwd(const Params& p, const BwdPlan& b, cudaStream_t s) {
   lsrm_status st = LSRM_OK;
-  if (p.Nq > 0) {
-    st = b.exact ? run_dq<D, NA, 1, true>(p, b, s) : run_dq<D, NA, 2, false>(p, b, s);
+  if (b.tc) {
+    if ((st = launch_bwd_tc(p, D, NA, b, s)) != LSRM_OK) return st;
+  }
+  if (!b.tc && p.Nq > 0) {
+    st = b.exact ? run_dq<D, NA, true>(p, b, s) : run_dq<D, NA, false>(p, b, s);
     if (st != LSRM_OK) return st;
   }
   if (p.Nk > 0) {
-    if (D == 32 && b.kv_rows == 128)
-      st = run_dkv<D, NA, D == 32 ? 2 : 1>(p, b, s);
-    else
-      st = run_dkv<D, NA, 1>(p, b, s);
-    if (st != LSRM_OK) return st;
+    if (!b.tc && (st = run_dkv<D, NA>(p, b, s)) != LSRM_OK) return st;
     if (p.splits > 1) {
       rp_dkv_join_kernel<D><<<(unsigned)(p.Nk / kSumRows + p.S), kSumThreads, 0, s>>>(p);
       if ((st = launched()) != LSRM_OK) return st;

@@ -17,18 +17,10 @@
 // Tensor memory a tile, 128 columns: S [64 fp32] | P [32, bf16 pairs] | O [32] at d = 32; at d = 64 P lies
 // over S (S 64 | O 64), is kept in registers until the chunk's sum has passed, and the next S waits for
 // P V.  Either way four tiles are in flight an SM.
-#include <cuda.h>
-#include <cudaTypedefs.h>
-
-#include "relpos.cuh"
-#include "tma_map.cuh"
+#include "relpos_tc.cuh"
 
 namespace lsrm {
 namespace rp {
-
-using namespace tc;
-
-constexpr int kTcThreads = 320;
 
 template <int D>
 struct TcFwd {
@@ -42,11 +34,6 @@ struct TcFwd {
   static constexpr int kColS = 0, kColP = kAlias ? 0 : 64, kColO = kAlias ? 64 : 96;
   static constexpr uint32_t kIdescQK = idesc_bf16(128, kKeys, false), kIdescPV = idesc_bf16(128, D, true);
   static_assert(kColO + D <= kTileCols, "tensor memory of a tile");
-};
-
-struct ChunkMeta {
-  int lo[kMaxAxes], hi[kMaxAxes];
-  uint32_t same16, same4;  // bit a: runs of 16 / 4 keys have one position on axis a
 };
 
 template <int D, int NA>
@@ -63,31 +50,6 @@ struct TcFwdSmem {
   float lut[1];  // [NA][2 maxd + 1]
   static size_t bytes(int maxd) { return sizeof(TcFwdSmem) + (size_t)NA * (2 * maxd + 1) * 4; }
 };
-
-// r = (a0, a1) * (b, b) + (c0, c1)
-__device__ __forceinline__ void ffma2v(float& r0, float& r1, float a0, float a1, float b, float c0, float c1) {
-  uint64_t ra, rb, rc, rd;
-  asm("mov.b64 %0, {%1, %2};\n" : "=l"(ra) : "f"(a0), "f"(a1));
-  asm("mov.b64 %0, {%1, %1};\n" : "=l"(rb) : "f"(b));
-  asm("mov.b64 %0, {%1, %2};\n" : "=l"(rc) : "f"(c0), "f"(c1));
-  asm("fma.rn.ftz.f32x2 %0, %1, %2, %3;\n" : "=l"(rd) : "l"(ra), "l"(rb), "l"(rc));
-  asm("mov.b64 {%0, %1}, %2;\n" : "=f"(r0), "=f"(r1) : "l"(rd));
-}
-
-// Wait for this thread's tensor-memory loads into r.  The registers are operands of the wait, so nothing
-// that reads them can be moved above it; and every load here is followed by its wait at once, with no
-// branch between the two, so no load is in flight while registers change hands.
-__device__ __forceinline__ void tmem_wait16(uint32_t* r) {
-  asm volatile("tcgen05.wait::ld.sync.aligned;\n"
-               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
-                 "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
-               :
-               : "memory");
-}
-__device__ __forceinline__ void tmem_wait32(uint32_t* r) {
-  tmem_wait16(r);
-  tmem_wait16(r + 16);
-}
 
 template <int D, int NA>
 __global__ void __launch_bounds__(kTcThreads, 2)
@@ -148,7 +110,7 @@ __global__ void __launch_bounds__(kTcThreads, 2)
 #pragma unroll
     for (int a = 0; a < NA; ++a) {
       const float x = b < 0 ? 0.0f : bf16_to_f32(p.table[((size_t)a * p.NB + b) * p.Hq + h]);
-      small = small && (fabsf(x) <= kFoldLimit / kMaxAxes || x == -INFINITY);
+      small = small && (fabsf(x) <= kSmallBias || x == -INFINITY);
       S.lut[a * (top + 1) + i] = x;
     }
   }
@@ -182,33 +144,10 @@ __global__ void __launch_bounds__(kTcThreads, 2)
         for (int i = 0; i < 2; ++i)  // positions past the end repeat the last key's
           x[a][i] = p.pos_k[(size_t)(key + min(lane + 32 * i, n - 1)) * NA + a];
       if (c >= C::kStages && !mbar_wait_w(&S.kv_empty[st], ((c / C::kStages) + 1) & 1, abort, p.status)) break;
-      uint32_t same16 = 0, same4 = 0;
-#pragma unroll
-      for (int a = 0; a < NA; ++a) {
-        const int lo = __reduce_min_sync(0xffffffffu, min(x[a][0], x[a][1]));
-        const int hi = __reduce_max_sync(0xffffffffu, max(x[a][0], x[a][1]));
-        if (lo < -kPosLimit || hi > kPosLimit) raise_status(p.status, LSRM_ERR_BOUNDS);
-        const uint32_t e = __ballot_sync(0xffffffffu, x[a][0] == __shfl_down_sync(0xffffffffu, x[a][0], 1)) &
-                           __ballot_sync(0xffffffffu, x[a][1] == __shfl_down_sync(0xffffffffu, x[a][1], 1));
-        if ((e & 0x7fff7fffu) == 0x7fff7fffu) same16 |= 1u << a;
-        if ((e & 0x77777777u) == 0x77777777u) same4 |= 1u << a;
-        S.pos[st][a][lane] = x[a][0];
-        S.pos[st][a][lane + 32] = x[a][1];
-        if (lane == 0) S.meta[st].lo[a] = lo, S.meta[st].hi[a] = hi;
-      }
-      if (lane == 0) S.meta[st].same16 = same16, S.meta[st].same4 = same4;
+      note_positions<NA>(x, S.pos[st], S.meta[st], lane, p.status);
       if (n < C::kKeys) {
-        // the last chunk of a segment: what lies behind it may be anything, and P = 0 does not hide an
-        // infinity, so V's rows past the end are zeros (in the layout that TMA would have written)
-        constexpr int kPieces = D / 8;
-        for (int i = lane; i < C::kKeys * kPieces; i += 32) {
-          const int r = i / kPieces, cc = i % kPieces;
-          uint4 u = make_uint4(0, 0, 0, 0);
-          if (r < n) u = *reinterpret_cast<const uint4*>(p.v + ((size_t)(key + r) * p.Hkv + hk) * D + cc * 8);
-          const int sw = D == 32 ? cc ^ ((r >> 1) & 3) : cc ^ (r & 7);
-          *reinterpret_cast<uint4*>(S.v[st] + r * C::kRowBytes + sw * 16) = u;
-        }
-        asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
+        copy_tail<D>(S.v[st], p.v, key, n, p.Hkv, hk, lane);
+        fence_async();
       }
       __syncwarp();
       if (lane == 0) {
@@ -308,40 +247,9 @@ __global__ void __launch_bounds__(kTcThreads, 2)
 
     float m = 0.0f, l = 0.0f;  // the row's reference (in the scores' units) and sum
     bool ok = true;
-    // the current chunk: stage, keys from here on, what its distances have in common, common bias
-    int st = 0, left = 0, mode[NA], worst = kOne;
-    float ub = 0.0f;
+    int st = 0, left = 0;  // the current chunk's stage and keys from here on
+    ChunkBias<NA, 1> cb;
 
-    // the bias of columns 16 g .. 16 g + 15 on top of `base`
-    auto bias16 = [&](float (&b)[16], int g, float base) {
-#pragma unroll
-      for (int a = 0; a < NA; ++a)
-        if (mode[a] == kLane) base += S.lut[a * (top + 1) + clamp_index(S.pos[st][a][16 * g], rowc[a], top)];
-#pragma unroll
-      for (int e = 0; e < 16; ++e) b[e] = base;
-#pragma unroll
-      for (int a = 0; a < NA; ++a) {
-        const float* la = S.lut + a * (top + 1);
-        const int4* xs = reinterpret_cast<const int4*>(&S.pos[st][a][16 * g]);
-        if (mode[a] == kFour) {
-#pragma unroll
-          for (int f = 0; f < 4; ++f) {
-            const float y = la[clamp_index(xs[f].x, rowc[a], top)];
-            b[4 * f] += y, b[4 * f + 1] += y, b[4 * f + 2] += y, b[4 * f + 3] += y;
-          }
-        } else if (mode[a] == kEach) {
-#pragma unroll
-          for (int f = 0; f < 4; ++f) {
-            const int4 x = xs[f];
-            // single adds: a pair of look-ups would first have to be moved into a pair of registers
-            b[4 * f] += la[clamp_index(x.x, rowc[a], top)];
-            b[4 * f + 1] += la[clamp_index(x.y, rowc[a], top)];
-            b[4 * f + 2] += la[clamp_index(x.z, rowc[a], top)];
-            b[4 * f + 3] += la[clamp_index(x.w, rowc[a], top)];
-          }
-        }
-      }
-    };
     // The chunk again, or a chunk of a table too large to fold: its maximum, the reference of the rows
     // that are `off` (or, without folding, behind their maximum) moved to it, and P from the scores in
     // the formula's order.  Returns the row's sum.
@@ -351,7 +259,7 @@ __global__ void __launch_bounds__(kTcThreads, 2)
       for (int g = 0; g < 4; ++g) {
         uint32_t r[16];
         float b[16];
-        bias16(b, g, ub);
+        cb.all16(b, cb.ub, S.pos[st], 16 * g, rowc, S.lut, top);
         tmem_ld16(tbase + C::kColS + 16 * g, r);
         tmem_wait16(r);
 #pragma unroll
@@ -378,7 +286,7 @@ __global__ void __launch_bounds__(kTcThreads, 2)
       for (int g = 0; g < 4; ++g) {
         uint32_t r[16], pk[8];
         float b[16];
-        bias16(b, g, ub);
+        cb.all16(b, cb.ub, S.pos[st], 16 * g, rowc, S.lut, top);
         tmem_ld16(tbase + C::kColS + 16 * g, r);
         tmem_wait16(r);
 #pragma unroll
@@ -399,23 +307,14 @@ __global__ void __launch_bounds__(kTcThreads, 2)
       left = khi - k0 - c * C::kKeys;
       if (!wait_all(&S.kv_full[st], (c / C::kStages) & 1) || !wait_all(&S.s_full[t], c & 1)) { ok = false; break; }
       tc_fence_after();
-      worst = kOne;
-      ub = 0.0f;
-#pragma unroll
-      for (int a = 0; a < NA; ++a) {
-        const int lo = clamp_index(S.meta[st].lo[a] - q_hi[a], p.maxd, top);
-        const int hi = clamp_index(S.meta[st].hi[a] - q_lo[a], p.maxd, top);
-        mode[a] = lo == hi ? kOne : (S.meta[st].same16 >> a) & 1 ? kLane : (S.meta[st].same4 >> a) & 1 ? kFour : kEach;
-        worst = max(worst, mode[a]);
-        if (mode[a] == kOne) ub += S.lut[a * (top + 1) + lo];
-      }
+      cb.set(S.meta[st], q_lo, q_hi, p.maxd, S.lut, top);
       if (!C::kAlias && c > 0 && !wait_all(&S.pv_done[t], (c - 1) & 1)) { ok = false; break; }  // P is free
       tc_fence_after();
       float sum;
       if (!fold) {
         sum = slow_chunk(c, false);
       } else {
-        const float base = ub - (m == -INFINITY ? 0.0f : m);
+        const float base = cb.ub - (m == -INFINITY ? 0.0f : m);
         uint32_t pk[C::kAlias ? 32 : 16];
         float s0 = 0.0f, s1 = 0.0f;
 #pragma unroll(C::kAlias ? 2 : 1)
@@ -427,22 +326,15 @@ __global__ void __launch_bounds__(kTcThreads, 2)
 #pragma unroll
           for (int g = 0; g < 2; ++g) {
             float b[16];
-            float row_b = base;
-            if (worst > kLane) {
-              bias16(b, 2 * hf + g, base);
-            } else {
-#pragma unroll
-              for (int a = 0; a < NA; ++a)
-                if (mode[a] == kLane)
-                  row_b += S.lut[a * (top + 1) + clamp_index(S.pos[st][a][32 * hf + 16 * g], rowc[a], top)];
-            }
-            if (worst > kLane) {
+            if (cb.worst > kLane) {
+              cb.all16(b, base, S.pos[st], 32 * hf + 16 * g, rowc, S.lut, top);
 #pragma unroll
               for (int e = 0; e < 16; ++e) b[e] = fmaf(__uint_as_float(r[16 * g + e]), mul, b[e]);
             } else {
+              const float one = cb.row16(base, S.pos[st], 32 * hf + 16 * g, rowc, S.lut, top);
 #pragma unroll
               for (int e = 0; e < 16; e += 2)
-                ffma2(b[e], b[e + 1], __uint_as_float(r[16 * g + e]), __uint_as_float(r[16 * g + e + 1]), mul, row_b);
+                ffma2(b[e], b[e + 1], __uint_as_float(r[16 * g + e]), __uint_as_float(r[16 * g + e + 1]), mul, one);
             }
             if (left < 32 * hf + 16 * g + 16) {
               keep_branch();

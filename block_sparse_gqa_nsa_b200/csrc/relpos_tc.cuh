@@ -1,0 +1,149 @@
+// Shared pieces of the tensor-memory kernels of the relative-position attention (relpos_tc.cu: forward,
+// relpos_bwd_tc.cu: backward).  A thread owns a row of a 128-row tile (a tensor-memory lane); the 64
+// columns of a chunk are the same for all lanes, so a bias that is the same for a run of columns costs
+// one look-up for the run, and branches on the columns' positions are uniform.
+#pragma once
+
+#include <cuda.h>
+#include <cudaTypedefs.h>
+
+#include "relpos.cuh"
+#include "tma_map.cuh"
+
+namespace lsrm {
+namespace rp {
+
+using namespace tc;
+
+constexpr int kTcThreads = 320;  // producer warp, MMA warp, eight warps on the scores
+constexpr int kTcCols = 64;      // columns a chunk
+
+template <int D>
+struct TcTile {
+  static constexpr int kRowBytes = D * 2;
+  static constexpr uint32_t kLayout = D == 32 ? kLayoutSW64 : kLayoutSW128;
+  static constexpr uint32_t kAtomBytes = 8 * kRowBytes;
+  static constexpr int kRowsBytes = 128 * kRowBytes, kColsBytes = kTcCols * kRowBytes;
+  static constexpr uint32_t kIdescScore = idesc_bf16(128, kTcCols, false);  // rows x columns
+  static constexpr uint32_t kIdescSum = idesc_bf16(128, D, true);           // rows x D over the columns
+};
+
+// Wait for this thread's tensor-memory loads into r.  The registers are operands of the wait, so nothing
+// that reads them can be moved above it; and every load here is followed by its wait at once, with no
+// branch between the two.
+__device__ __forceinline__ void tmem_wait16(uint32_t* r) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;\n"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                 "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
+               :
+               : "memory");
+}
+__device__ __forceinline__ void tmem_wait32(uint32_t* r) {
+  tmem_wait16(r);
+  tmem_wait16(r + 16);
+}
+
+// 64 rows of a [tokens][heads][D] tensor into a stage in the layout that TMA writes, zeros past n: what
+// lies behind a segment may be anything, and a weight of 0 does not hide an infinity.  A whole warp;
+// the caller makes it visible to the tensor cores (fence_async) before its arrive.
+template <int D>
+__device__ __forceinline__ void copy_tail(uint8_t* dst, const uint16_t* src, int r0, int n, int heads, int h, int lane) {
+  constexpr int kPieces = D / 8;
+  for (int i = lane; i < kTcCols * kPieces; i += 32) {
+    const int r = i / kPieces, c = i % kPieces;
+    uint4 u = make_uint4(0, 0, 0, 0);
+    if (r < n) u = *reinterpret_cast<const uint4*>(src + ((size_t)(r0 + r) * heads + h) * D + c * 8);
+    const int sw = D == 32 ? c ^ ((r >> 1) & 3) : c ^ (r & 7);
+    *reinterpret_cast<uint4*>(dst + r * (D * 2) + sw * 16) = u;
+  }
+  __syncwarp();
+}
+__device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory"); }
+
+// what a chunk's column positions have in common
+struct ChunkMeta {
+  int lo[kMaxAxes], hi[kMaxAxes];
+  uint32_t same16, same4;  // bit a: aligned runs of 16 / 4 columns have one position on axis a
+};
+// the producer warp's part: lane i holds the positions of columns i and i + 32
+template <int NA>
+__device__ __forceinline__ void note_positions(const int (&x)[NA][2], int (*pos)[kTcCols], ChunkMeta& m, int lane,
+                                               uint32_t* status) {
+  uint32_t same16 = 0, same4 = 0;
+#pragma unroll
+  for (int a = 0; a < NA; ++a) {
+    const int lo = __reduce_min_sync(0xffffffffu, min(x[a][0], x[a][1]));
+    const int hi = __reduce_max_sync(0xffffffffu, max(x[a][0], x[a][1]));
+    if (lo < -kPosLimit || hi > kPosLimit) raise_status(status, LSRM_ERR_BOUNDS);
+    const uint32_t e = __ballot_sync(0xffffffffu, x[a][0] == __shfl_down_sync(0xffffffffu, x[a][0], 1)) &
+                       __ballot_sync(0xffffffffu, x[a][1] == __shfl_down_sync(0xffffffffu, x[a][1], 1));
+    if ((e & 0x7fff7fffu) == 0x7fff7fffu) same16 |= 1u << a;
+    if ((e & 0x77777777u) == 0x77777777u) same4 |= 1u << a;
+    pos[a][lane] = x[a][0];
+    pos[a][lane + 32] = x[a][1];
+    if (lane == 0) m.lo[a] = lo, m.hi[a] = hi;
+  }
+  if (lane == 0) m.same16 = same16, m.same4 = same4;
+}
+
+// A chunk's modes for a warp's rows (kOne, kLane: 16 columns, kFour, kEach) and the bias common to it.
+// SIGN as for add_bias.
+template <int NA, int SIGN>
+struct ChunkBias {
+  int mode[NA], one[NA], worst;
+  float ub;
+  __device__ __forceinline__ void set(const ChunkMeta& m, const int (&row_lo)[NA], const int (&row_hi)[NA], int maxd,
+                                      const float* lut, int top) {
+    worst = kOne;
+    ub = 0.0f;
+#pragma unroll
+    for (int a = 0; a < NA; ++a) {
+      const int lo = clamp_index(SIGN > 0 ? m.lo[a] - row_hi[a] : row_lo[a] - m.hi[a], maxd, top);
+      const int hi = clamp_index(SIGN > 0 ? m.hi[a] - row_lo[a] : row_hi[a] - m.lo[a], maxd, top);
+      one[a] = lo;
+      mode[a] = lo == hi ? kOne : (m.same16 >> a) & 1 ? kLane : (m.same4 >> a) & 1 ? kFour : kEach;
+      worst = max(worst, mode[a]);
+      if (mode[a] == kOne) ub += lut[a * (top + 1) + lo];
+    }
+  }
+  // the row's bias of a run of 16 columns that has only one (worst <= kLane), on top of base
+  __device__ __forceinline__ float row16(float base, int (*pos)[kTcCols], int col, const int (&rowc)[NA],
+                                         const float* lut, int top) const {
+#pragma unroll
+    for (int a = 0; a < NA; ++a)
+      if (mode[a] == kLane) base += lut[a * (top + 1) + clamp_index(SIGN * pos[a][col], rowc[a], top)];
+    return base;
+  }
+  // the biases of columns col .. col + 15 on top of base
+  __device__ __forceinline__ void all16(float (&b)[16], float base, int (*pos)[kTcCols], int col, const int (&rowc)[NA],
+                                        const float* lut, int top) const {
+    base = row16(base, pos, col, rowc, lut, top);
+#pragma unroll
+    for (int e = 0; e < 16; ++e) b[e] = base;
+#pragma unroll
+    for (int a = 0; a < NA; ++a) {
+      const float* la = lut + a * (top + 1);
+      const int4* xs = reinterpret_cast<const int4*>(&pos[a][col]);
+      if (mode[a] == kFour) {
+#pragma unroll
+        for (int f = 0; f < 4; ++f) {
+          const float y = la[clamp_index(SIGN * xs[f].x, rowc[a], top)];
+          b[4 * f] += y, b[4 * f + 1] += y, b[4 * f + 2] += y, b[4 * f + 3] += y;
+        }
+      } else if (mode[a] == kEach) {
+#pragma unroll
+        for (int f = 0; f < 4; ++f) {
+          const int4 x = xs[f];
+          // single adds: a pair of look-ups would first have to be moved into a pair of registers
+          b[4 * f] += la[clamp_index(SIGN * x.x, rowc[a], top)];
+          b[4 * f + 1] += la[clamp_index(SIGN * x.y, rowc[a], top)];
+          b[4 * f + 2] += la[clamp_index(SIGN * x.z, rowc[a], top)];
+          b[4 * f + 3] += la[clamp_index(SIGN * x.w, rowc[a], top)];
+        }
+      }
+    }
+  }
+};
+
+}  // namespace rp
+}  // namespace lsrm

@@ -108,6 +108,17 @@ FORWARD = {
     "no_keys_at_all": dict(lens_q=[40, 40], lens_k=[0, 0]),
     "no_queries_at_all": dict(lens_q=[0, 0], lens_k=[40, 40]),
     "outside": dict(lens_q=[70, 5], lead=9),
+    # long segments: 128-row tiles in the backward
+    "long32": dict(lens_q=[300]),
+    "long64": dict(lens_q=[300, 555], dim=64),
+    "long_gqa16": dict(lens_q=[520, 300], heads=32, kv_heads=2),
+    "long_ragged": dict(lens_q=[600, 0, 1, 700, 65, 640, 129], heads=2, kv_heads=2, places="scattered", axes=2),
+    "long_cross": dict(lens_q=[400, 0, 300], lens_k=[300, 400, 500], dim=64, heads=6, kv_heads=2),
+    "long_outside": dict(lens_q=[300, 400], lead=9, dim=64, axes=2, places="scattered", buckets=64, maxd=200),
+    "long_axes3": dict(lens_q=[450], dim=64, axes=3, places="scattered", maxd=30, buckets=16),
+    "long_frames": dict(lens_q=[640], dim=64, axes=2, places="frames", maxd=7, buckets=8),
+    "long_widest": dict(lens_q=[330], axes=3, maxd=1023, buckets=64, dim=64, places="scattered"),
+    "long_odd_buckets": dict(lens_q=[400, 300], axes=3, buckets=7, maxd=9, places="scattered"),
 }
 
 
@@ -156,7 +167,7 @@ def test_rows_outside_segments_stay():
 
 
 # a neighbour segment's infinities and NaNs do not reach a row, whatever the tile
-@pytest.mark.parametrize("lens", [[40, 23, 61], [1, 1, 1], [130, 5, 200]])
+@pytest.mark.parametrize("lens", [[40, 23, 61], [1, 1, 1], [130, 5, 200], [300, 310, 333]])
 def test_neighbours_do_not_leak(lens):
     c = Case(lens, dim=64)
     clean = {n: x.clone() for n, x in c.check()[0].items()}
@@ -170,7 +181,7 @@ def test_neighbours_do_not_leak(lens):
             assert torch.equal(got[n][part], clean[n][part]), n
 
 
-@pytest.mark.parametrize("lens_q,lens_k", [([130], None), ([3], [200])])
+@pytest.mark.parametrize("lens_q,lens_k", [([130], None), ([3], [200]), ([290, 300], None)])
 @pytest.mark.parametrize("low", [-math.inf, torch.finfo(BF).min, -1e30])
 def test_masks_by_the_table(lens_q, lens_k, low):
     """Entries at -inf or at the type's lowest value mask a bucket; a row whose every key is at -inf
