@@ -9,8 +9,10 @@
 //       the table's gradient.
 //
 // 320 threads: warp 0 brings the streamed operands by TMA and the columns' positions and row constants by
-// plain loads, warp 1 issues the MMAs, warps 2-9 do the scores: two threads a row, 32 columns each, so
-// that eight warps a tile (two tiles an SM) hide each other's tensor-memory and exponential latency.
+// plain loads, warp 1 issues the MMAs, warps 2-9 do the scores: two threads a row, 32 columns each.  Each
+// half of the columns is a pipeline of its own (scores, products, barriers), so that with two tiles an SM
+// four pipelines cover each other's hand-overs between the score warps and the tensor cores (one pipeline
+// a tile: dq 375 us, dk/dv 573 us at 4096 tokens and 32 heads of 32).
 // Against the mma.sync kernels, which they replace on long segments, the operands need no shared-memory
 // reads by the warps that compute, and runs of columns on one position share look-ups and sums.
 //
@@ -33,7 +35,7 @@ struct EwBarrier {
   __device__ __forceinline__ bool sync() {
     __syncwarp();
     mbar_arrive(bar);
-    const bool ok = mbar_wait_w(bar, phase & 1, abort, status);
+    const bool ok = wait_bar_w(bar, phase & 1, abort, status);
     ++phase;
     return ok;
   }
@@ -107,7 +109,7 @@ struct DqTcSmem {
   uint8_t v[C::kStages][C::kColsBytes];
   int pos[C::kStages][NA][kTcCols];
   ChunkMeta meta[C::kStages];
-  uint64_t q_full, kv_full[C::kStages], kv_empty[C::kStages], s_full, p_full, done, drain, ew;
+  uint64_t q_full, kv_full[C::kStages], kv_empty[C::kStages], s_full[2], p_full[2], done[2], drain, ew;
   float rest[2][128];
   uint32_t tmem_base;
   int abort, vote;
@@ -145,9 +147,11 @@ __global__ void __launch_bounds__(kTcThreads, 2)
       mbar_init(&S.kv_full[s], 1);
       mbar_init(&S.kv_empty[s], 1);
     }
-    mbar_init(&S.s_full, 1);
-    mbar_init(&S.p_full, kEwThreads);
-    mbar_init(&S.done, 1);
+    for (int hf = 0; hf < 2; ++hf) {
+      mbar_init(&S.s_full[hf], 1);
+      mbar_init(&S.p_full[hf], kEwThreads / 2);
+      mbar_init(&S.done[hf], 1);
+    }
     mbar_init(&S.drain, 1);
     mbar_init(&S.ew, kEwThreads);
     fence_mbar_init();
@@ -178,7 +182,7 @@ __global__ void __launch_bounds__(kTcThreads, 2)
 #pragma unroll
         for (int i = 0; i < 2; ++i)  // positions past the end repeat the last key's
           x[a][i] = p.pos_k[(size_t)(key + min(lane + 32 * i, n - 1)) * NA + a];
-      if (c >= C::kStages && !mbar_wait_w(&S.kv_empty[st], ((c / C::kStages) + 1) & 1, abort, p.status)) break;
+      if (c >= C::kStages && !wait_bar_w(&S.kv_empty[st], ((c / C::kStages) + 1) & 1, abort, p.status)) break;
       note_positions<NA>(x, S.pos[st], S.meta[st], lane, p.status);
       if (n < kTcCols) {
         copy_tail<D>(S.k[st], p.k, key, n, p.Hkv, hk, lane);
@@ -195,57 +199,58 @@ __global__ void __launch_bounds__(kTcThreads, 2)
     if (lane == 0 && *abort) {
       // let the copies already issued land before the CTA's shared memory goes away
       volatile int no_abort = 0;
-      if (chunks > 0) mbar_wait(&S.q_full, 0, &no_abort, nullptr);
+      if (chunks > 0) wait_bar(&S.q_full, 0, &no_abort, nullptr);
       for (int c = max(0, issued - C::kStages); c < issued; ++c)
-        mbar_wait(&S.kv_full[c % C::kStages], (c / C::kStages) & 1, &no_abort, nullptr);
+        wait_bar(&S.kv_full[c % C::kStages], (c / C::kStages) & 1, &no_abort, nullptr);
     }
   } else if (warp == 1) {
     // ---------------- MMA issuer ----------------
     if (lane == 0 && chunks > 0) {
-      bool ok = mbar_wait(&S.q_full, 0, abort, p.status);
+      bool ok = wait_bar(&S.q_full, 0, abort, p.status);
       tc_fence_after();
       const uint64_t qdesc = smem_desc(smem_u32(S.q), 16, C::kAtomBytes, C::kLayout);
       const uint64_t odesc = smem_desc(smem_u32(S.o), 16, C::kAtomBytes, C::kLayout);
       const uint64_t kdesc = smem_desc(smem_u32(S.k[0]), 16, C::kAtomBytes, C::kLayout);
       const uint64_t vdesc = smem_desc(smem_u32(S.v[0]), 16, C::kAtomBytes, C::kLayout);
       const uint64_t ksum = smem_desc(smem_u32(S.k[0]), C::kColsBytes, C::kAtomBytes, C::kLayout);
-      constexpr uint32_t kStep = C::kColsBytes >> 4;
-      auto issue_scores = [&](int c) {
-        const uint64_t at = (uint64_t)((c % C::kStages) * kStep);
+      constexpr uint32_t kStep = C::kColsBytes >> 4, kHalfStep = kStep / 2;
+      auto issue_scores = [&](int c, int hf) {
+        const uint64_t at = (uint64_t)((c % C::kStages) * kStep + hf * kHalfStep);
 #pragma unroll
         for (int i = 0; i < D / 16; ++i)
-          mma_ss(tmem + C::kColS, qdesc + 2 * i, kdesc + at + 2 * i, C::kIdescScore, i > 0 ? 1u : 0u);
+          mma_ss(tmem + C::kColS + 32 * hf, qdesc + 2 * i, kdesc + at + 2 * i, C::kIdescHalf, i > 0 ? 1u : 0u);
 #pragma unroll
         for (int i = 0; i < D / 16; ++i)
-          mma_ss(tmem + C::kColDp, odesc + 2 * i, vdesc + at + 2 * i, C::kIdescScore, i > 0 ? 1u : 0u);
-        mma_commit(&S.s_full);
+          mma_ss(tmem + C::kColDp + 32 * hf, odesc + 2 * i, vdesc + at + 2 * i, C::kIdescHalf, i > 0 ? 1u : 0u);
+        mma_commit(&S.s_full[hf]);
       };
-      auto issue_dq = [&](int c) {
-        const uint64_t at = (uint64_t)((c % C::kStages) * kStep);
+      auto issue_dq = [&](int c, int hf) {
+        const uint64_t at = (uint64_t)((c % C::kStages) * kStep + hf * kHalfStep);
 #pragma unroll
-        for (int i = 0; i < kTcCols / 16; ++i)
-          mma_ts(tmem + C::kColDq, tmem + C::kColDs + i * 8, ksum + at + i * (16 * C::kRowBytes >> 4), C::kIdescSum,
-                 (c == 0 && i == 0) ? 0u : 1u);
-        mma_commit(&S.done);
+        for (int i = 0; i < 2; ++i)
+          mma_ts(tmem + C::kColDq, tmem + C::kColDs + hf * 16 + i * 8, ksum + at + i * (16 * C::kRowBytes >> 4),
+                 C::kIdescSum, (c == 0 && hf == 0 && i == 0) ? 0u : 1u);
+        mma_commit(&S.done[hf]);
       };
       for (int c = 0; ok && c < chunks; ++c) {
-        if (!mbar_wait(&S.kv_full[c % C::kStages], (c / C::kStages) & 1, abort, p.status)) { ok = false; break; }
-        if (c > 0 && !mbar_wait(&S.p_full, (c - 1) & 1, abort, p.status)) { ok = false; break; }
-        tc_fence_after();
-        issue_scores(c);  // S and dP were released with dS(c - 1)
-        if (c > 0) {
-          issue_dq(c - 1);
-          mma_commit(&S.kv_empty[(c - 1) % C::kStages]);
+        if (!wait_bar(&S.kv_full[c % C::kStages], (c / C::kStages) & 1, abort, p.status)) { ok = false; break; }
+        for (int hf = 0; hf < 2; ++hf) {
+          if (c > 0 && !wait_bar(&S.p_full[hf], (c - 1) & 1, abort, p.status)) { ok = false; break; }
+          tc_fence_after();
+          issue_scores(c, hf);  // S and dP were released with dS(c - 1)
+          if (c > 0) issue_dq(c - 1, hf);
         }
+        if (ok && c > 0) mma_commit(&S.kv_empty[(c - 1) % C::kStages]);
       }
-      if (ok && mbar_wait(&S.p_full, (chunks - 1) & 1, abort, p.status)) {
+      for (int hf = 0; ok && hf < 2; ++hf) {
+        if (!wait_bar(&S.p_full[hf], (chunks - 1) & 1, abort, p.status)) { ok = false; break; }
         tc_fence_after();
-        issue_dq(chunks - 1);
+        issue_dq(chunks - 1, hf);
       }
       // every MMA issued so far must finish before the CTA can release tensor and shared memory
       mma_commit(&S.drain);
       volatile int no_abort = 0;
-      mbar_wait(&S.drain, 0, &no_abort, nullptr);
+      wait_bar(&S.drain, 0, &no_abort, nullptr);
     }
   } else {
     // ---------------- scores: two threads a row ----------------
@@ -296,12 +301,12 @@ __global__ void __launch_bounds__(kTcThreads, 2)
     __syncwarp();
     const float l2 = fmaf(lse, kLog2e, corr), rconst = small ? l2 : lse;
 
-    ChunkBias<NA, 1> cb;
+    ChunkBias<NA, 1, true> cb;
     for (int c = 0; ok && c < chunks; ++c) {
       const int st = c % C::kStages, left = khi - klo - c * kTcCols;
-      if (!mbar_wait_w(&S.kv_full[st], (c / C::kStages) & 1, abort, p.status) ||
-          !mbar_wait_w(&S.s_full, c & 1, abort, p.status) ||
-          (c > 0 && !mbar_wait_w(&S.done, (c - 1) & 1, abort, p.status))) {  // dS is free
+      if (!wait_bar_w(&S.kv_full[st], (c / C::kStages) & 1, abort, p.status) ||
+          !wait_bar_w(&S.s_full[half], c & 1, abort, p.status) ||
+          (c > 0 && !wait_bar_w(&S.done[half], (c - 1) & 1, abort, p.status))) {  // dS is free
         ok = false;
         break;
       }
@@ -316,13 +321,13 @@ __global__ void __launch_bounds__(kTcThreads, 2)
         tmem_wait16(s);
         tmem_wait16(d);
         float x[16];
-        if (small && cb.worst <= kLane) {
-          const float b = cb.row16(cb.ub - rconst, S.pos[st], col, rowc, S.lut, top);
+        if (small && cb.flat(2 * half + g)) {
+          const float b = cb.row16(cb.ub - rconst, S.pos[st], 2 * half + g, rowc, S.lut, top);
 #pragma unroll
           for (int e = 0; e < 16; e += 2)
             ffma2(x[e], x[e + 1], __uint_as_float(s[e]), __uint_as_float(s[e + 1]), mul, b);
         } else {
-          cb.all16(x, cb.ub, S.pos[st], col, rowc, S.lut, top);
+          cb.all16(x, cb.ub, S.pos[st], 2 * half + g, rowc, S.lut, top);
 #pragma unroll
           for (int e = 0; e < 16; ++e) x[e] = fmaf(__uint_as_float(s[e]), mul, x[e]) - rconst;
           if (!small) {
@@ -356,9 +361,11 @@ __global__ void __launch_bounds__(kTcThreads, 2)
       }
       tmem_st_wait();
       tc_fence_before();
-      mbar_arrive(&S.p_full);
+      mbar_arrive(&S.p_full[half]);
     }
-    if (ok && chunks > 0) ok = mbar_wait_w(&S.done, (chunks - 1) & 1, abort, p.status);
+    if (ok && chunks > 0)
+      ok = wait_bar_w(&S.done[0], (chunks - 1) & 1, abort, p.status) &&
+           wait_bar_w(&S.done[1], (chunks - 1) & 1, abort, p.status);
     tc_fence_after();
     S.rest[half][r] = rest;
     ok = eb.sync() && ok;
@@ -417,9 +424,9 @@ struct DkvTcSmem {
   uint8_t q[C::kStages][C::kColsBytes];
   uint8_t o[C::kStages][C::kColsBytes];  // dO
   int pos[C::kStages][NA][kTcCols];
-  float lse[C::kStages][kTcCols], delta[C::kStages][kTcCols];
+  float nlse[C::kStages][kTcCols], ndelta[C::kStages][kTcCols];  // negated: packed adds have no signs
   ChunkMeta meta[C::kStages];
-  uint64_t k_full, q_full[C::kStages], q_empty[C::kStages], s_full, p_full, done, drain, ew;
+  uint64_t k_full, q_full[C::kStages], q_empty[C::kStages], s_full[2], p_full[2], done[2], drain, ew;
   uint32_t tmem_base;
   int abort, vote, pad;
   // behind it: table fp32 [NA][2 maxd + 1], the buckets' byte offsets int32 [2 maxd + 1], and the
@@ -483,9 +490,11 @@ __global__ void __launch_bounds__(kTcThreads, 2)
       mbar_init(&S.q_full[s], 1);
       mbar_init(&S.q_empty[s], 1);
     }
-    mbar_init(&S.s_full, 1);
-    mbar_init(&S.p_full, kEwThreads);
-    mbar_init(&S.done, 1);
+    for (int hf = 0; hf < 2; ++hf) {
+      mbar_init(&S.s_full[hf], 1);
+      mbar_init(&S.p_full[hf], kEwThreads / 2);
+      mbar_init(&S.done[hf], 1);
+    }
     mbar_init(&S.drain, 1);
     mbar_init(&S.ew, kEwThreads);
     fence_mbar_init();
@@ -522,12 +531,12 @@ __global__ void __launch_bounds__(kTcThreads, 2)
         l[i] = lane + 32 * i < n ? p.lse2[q * p.Hq + h] : INFINITY;  // no query: P = 0
         dl[i] = p.delta[q * p.Hq + h];
       }
-      if (it >= C::kStages && !mbar_wait_w(&S.q_empty[st], ((it / C::kStages) + 1) & 1, abort, p.status)) break;
+      if (it >= C::kStages && !wait_bar_w(&S.q_empty[st], ((it / C::kStages) + 1) & 1, abort, p.status)) break;
       note_positions<NA>(x, S.pos[st], S.meta[st], lane, p.status);
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        S.lse[st][lane + 32 * i] = l[i];
-        S.delta[st][lane + 32 * i] = dl[i];
+        S.nlse[st][lane + 32 * i] = -l[i];
+        S.ndelta[st][lane + 32 * i] = -dl[i];
       }
       if (n < kTcCols) {
         copy_tail<D>(S.q[st], p.q, q0, n, p.Hq, h, lane);
@@ -548,14 +557,14 @@ __global__ void __launch_bounds__(kTcThreads, 2)
     }
     if (lane == 0 && *abort) {
       volatile int no_abort = 0;
-      if (steps > 0) mbar_wait(&S.k_full, 0, &no_abort, nullptr);
+      if (steps > 0) wait_bar(&S.k_full, 0, &no_abort, nullptr);
       for (int c = max(0, issued - C::kStages); c < issued; ++c)
-        mbar_wait(&S.q_full[c % C::kStages], (c / C::kStages) & 1, &no_abort, nullptr);
+        wait_bar(&S.q_full[c % C::kStages], (c / C::kStages) & 1, &no_abort, nullptr);
     }
   } else if (warp == 1) {
     // ---------------- MMA issuer ----------------
     if (lane == 0 && steps > 0) {
-      bool ok = mbar_wait(&S.k_full, 0, abort, p.status);
+      bool ok = wait_bar(&S.k_full, 0, abort, p.status);
       tc_fence_after();
       const uint64_t kdesc = smem_desc(smem_u32(S.k), 16, C::kAtomBytes, C::kLayout);
       const uint64_t vdesc = smem_desc(smem_u32(S.v), 16, C::kAtomBytes, C::kLayout);
@@ -563,51 +572,57 @@ __global__ void __launch_bounds__(kTcThreads, 2)
       const uint64_t odesc = smem_desc(smem_u32(S.o[0]), 16, C::kAtomBytes, C::kLayout);
       const uint64_t qsum = smem_desc(smem_u32(S.q[0]), C::kColsBytes, C::kAtomBytes, C::kLayout);
       const uint64_t osum = smem_desc(smem_u32(S.o[0]), C::kColsBytes, C::kAtomBytes, C::kLayout);
-      constexpr uint32_t kStep = C::kColsBytes >> 4;
-      auto issue_scores = [&](int it) {
-        const uint64_t at = (uint64_t)((it % C::kStages) * kStep);
+      constexpr uint32_t kStep = C::kColsBytes >> 4, kHalfStep = kStep / 2;
+      auto issue_scores = [&](int it, int hf) {
+        const uint64_t at = (uint64_t)((it % C::kStages) * kStep + hf * kHalfStep);
 #pragma unroll
         for (int i = 0; i < D / 16; ++i)
-          mma_ss(tmem + C::kColS, kdesc + 2 * i, qdesc + at + 2 * i, C::kIdescScore, i > 0 ? 1u : 0u);
+          mma_ss(tmem + C::kColS + 32 * hf, kdesc + 2 * i, qdesc + at + 2 * i, C::kIdescHalf, i > 0 ? 1u : 0u);
 #pragma unroll
         for (int i = 0; i < D / 16; ++i)
-          mma_ss(tmem + C::kColDp, vdesc + 2 * i, odesc + at + 2 * i, C::kIdescScore, i > 0 ? 1u : 0u);
-        mma_commit(&S.s_full);
+          mma_ss(tmem + C::kColDp + 32 * hf, vdesc + 2 * i, odesc + at + 2 * i, C::kIdescHalf, i > 0 ? 1u : 0u);
+        mma_commit(&S.s_full[hf]);
       };
-      auto issue_sums = [&](int it) {
-        const uint64_t at = (uint64_t)((it % C::kStages) * kStep);
-        const uint32_t first_add = it == 0 ? 0u : 1u;
+      auto issue_sums = [&](int it, int hf) {
+        const uint64_t at = (uint64_t)((it % C::kStages) * kStep + hf * kHalfStep);
+        const uint32_t first_add = it == 0 && hf == 0 ? 0u : 1u;
 #pragma unroll
-        for (int i = 0; i < kTcCols / 16; ++i)
-          mma_ts(tmem + C::kColDv, tmem + C::kColP + (i >> 1) * C::kHalf + (i & 1) * 8,
-                 osum + at + i * (16 * C::kRowBytes >> 4), C::kIdescSum, i == 0 ? first_add : 1u);
+        for (int i = 0; i < 2; ++i)
+          mma_ts(tmem + C::kColDv, tmem + C::kColP + hf * C::kHalf + i * 8, osum + at + i * (16 * C::kRowBytes >> 4),
+                 C::kIdescSum, i == 0 ? first_add : 1u);
 #pragma unroll
-        for (int i = 0; i < kTcCols / 16; ++i)
-          mma_ts(tmem + C::kColDk, tmem + C::kColDs + (i >> 1) * C::kHalf + (i & 1) * 8,
-                 qsum + at + i * (16 * C::kRowBytes >> 4), C::kIdescSum, i == 0 ? first_add : 1u);
-        mma_commit(&S.done);
-        mma_commit(&S.q_empty[it % C::kStages]);
+        for (int i = 0; i < 2; ++i)
+          mma_ts(tmem + C::kColDk, tmem + C::kColDs + hf * C::kHalf + i * 8, qsum + at + i * (16 * C::kRowBytes >> 4),
+                 C::kIdescSum, i == 0 ? first_add : 1u);
+        mma_commit(&S.done[hf]);
       };
       for (int it = 0; ok && it < steps; ++it) {
-        if (!mbar_wait(&S.q_full[it % C::kStages], (it / C::kStages) & 1, abort, p.status)) { ok = false; break; }
-        if (it > 0 && !mbar_wait(&S.p_full, (it - 1) & 1, abort, p.status)) { ok = false; break; }
-        tc_fence_after();
-        if (C::kAlias && it > 0) {
-          // the next scores overwrite the operands of the products, so those have to be done
-          issue_sums(it - 1);
-          if (!mbar_wait(&S.done, (it - 1) & 1, abort, p.status)) { ok = false; break; }
+        if (!wait_bar(&S.q_full[it % C::kStages], (it / C::kStages) & 1, abort, p.status)) { ok = false; break; }
+        for (int hf = 0; hf < 2; ++hf) {
+          if (it > 0 && !wait_bar(&S.p_full[hf], (it - 1) & 1, abort, p.status)) { ok = false; break; }
           tc_fence_after();
+          if (!C::kAlias) issue_scores(it, hf);
+          if (it > 0) issue_sums(it - 1, hf);
         }
-        issue_scores(it);
-        if (!C::kAlias && it > 0) issue_sums(it - 1);
+        if (!ok) break;
+        if (it > 0) mma_commit(&S.q_empty[(it - 1) % C::kStages]);
+        if (C::kAlias) {
+          for (int hf = 0; hf < 2; ++hf) {
+            // the next scores overwrite the operands of the products, so those have to be done
+            if (it > 0 && !wait_bar(&S.done[hf], (it - 1) & 1, abort, p.status)) { ok = false; break; }
+            tc_fence_after();
+            issue_scores(it, hf);
+          }
+        }
       }
-      if (ok && mbar_wait(&S.p_full, (steps - 1) & 1, abort, p.status)) {
+      for (int hf = 0; ok && hf < 2; ++hf) {
+        if (!wait_bar(&S.p_full[hf], (steps - 1) & 1, abort, p.status)) { ok = false; break; }
         tc_fence_after();
-        issue_sums(steps - 1);
+        issue_sums(steps - 1, hf);
       }
       mma_commit(&S.drain);
       volatile int no_abort = 0;
-      mbar_wait(&S.drain, 0, &no_abort, nullptr);
+      wait_bar(&S.drain, 0, &no_abort, nullptr);
     }
   } else {
     // ---------------- scores: two threads a key ----------------
@@ -639,16 +654,16 @@ __global__ void __launch_bounds__(kTcThreads, 2)
     EwBarrier eb{&S.ew, abort, p.status, 0};
     bool ok = true, small = false;
     float mul = 0.0f;
-    ChunkBias<NA, -1> cb;
+    ChunkBias<NA, -1, true> cb;
     for (int it = 0; ok && it < steps; ++it) {
       const int st = it % C::kStages, cc = it % nc, head = h0 + it / nc;
       if (cc == 0) {
         small = ew_fill<NA>(p, lut, hk * p.G + head, ew, &S.vote, eb, ok);
         mul = small ? p.scale * kLog2e : p.scale;
       }
-      if (!mbar_wait_w(&S.q_full[st], (it / C::kStages) & 1, abort, p.status) ||
-          !mbar_wait_w(&S.s_full, it & 1, abort, p.status) ||
-          (!C::kAlias && it > 0 && !mbar_wait_w(&S.done, (it - 1) & 1, abort, p.status))) {  // P and dS are free
+      if (!wait_bar_w(&S.q_full[st], (it / C::kStages) & 1, abort, p.status) ||
+          !wait_bar_w(&S.s_full[half], it & 1, abort, p.status) ||
+          (!C::kAlias && it > 0 && !wait_bar_w(&S.done[half], (it - 1) & 1, abort, p.status))) {  // P and dS are free
         ok = false;
         break;
       }
@@ -662,28 +677,30 @@ __global__ void __launch_bounds__(kTcThreads, 2)
         tmem_ld16(tbase + C::kColDp + col, d);
         tmem_wait16(s);
         tmem_wait16(d);
-        const float4* ls = reinterpret_cast<const float4*>(&S.lse[st][col]);
-        const float4* ds = reinterpret_cast<const float4*>(&S.delta[st][col]);
+        const float4* ls = reinterpret_cast<const float4*>(&S.nlse[st][col]);
+        const float4* ds = reinterpret_cast<const float4*>(&S.ndelta[st][col]);
         float x[16];
-        if (small && cb.worst <= kLane) {
-          const float b = cb.row16(cb.ub, S.pos[st], col, rowc, lut, top);
+        if (small && cb.flat(2 * half + g)) {
+          const float b = cb.row16(cb.ub, S.pos[st], 2 * half + g, rowc, lut, top);
 #pragma unroll
           for (int f = 0; f < 4; ++f) {
-            const float4 l = ls[f];
-            ffma2v(x[4 * f], x[4 * f + 1], __uint_as_float(s[4 * f]), __uint_as_float(s[4 * f + 1]), mul, b - l.x,
-                   b - l.y);
-            ffma2v(x[4 * f + 2], x[4 * f + 3], __uint_as_float(s[4 * f + 2]), __uint_as_float(s[4 * f + 3]), mul,
-                   b - l.z, b - l.w);
+            float4 l = ls[f];
+            fadd2_acc(l.x, l.y, b, b);
+            fadd2_acc(l.z, l.w, b, b);
+            ffma2v(x[4 * f], x[4 * f + 1], __uint_as_float(s[4 * f]), __uint_as_float(s[4 * f + 1]), mul, l.x, l.y);
+            ffma2v(x[4 * f + 2], x[4 * f + 3], __uint_as_float(s[4 * f + 2]), __uint_as_float(s[4 * f + 3]), mul, l.z,
+                   l.w);
           }
         } else {
-          cb.all16(x, cb.ub, S.pos[st], col, rowc, lut, top);
+          cb.all16(x, cb.ub, S.pos[st], 2 * half + g, rowc, lut, top);
 #pragma unroll
           for (int e = 0; e < 16; ++e) x[e] = fmaf(__uint_as_float(s[e]), mul, x[e]);
           if (small) {
 #pragma unroll
             for (int f = 0; f < 4; ++f) {
               const float4 l = ls[f];
-              x[4 * f] -= l.x, x[4 * f + 1] -= l.y, x[4 * f + 2] -= l.z, x[4 * f + 3] -= l.w;
+              fadd2_acc(x[4 * f], x[4 * f + 1], l.x, l.y);
+              fadd2_acc(x[4 * f + 2], x[4 * f + 3], l.z, l.w);
             }
           } else {
             // natural units, the subtraction first: exact for scores of any size
@@ -707,7 +724,7 @@ __global__ void __launch_bounds__(kTcThreads, 2)
             const int i = 4 * f + e;
             const float p0 = ex2(x[i]), p1 = ex2(x[i + 1]);
             float d0 = __uint_as_float(d[i]), d1 = __uint_as_float(d[i + 1]);
-            fadd2_acc(d0, d1, e == 0 ? -dl.x : -dl.z, e == 0 ? -dl.y : -dl.w);
+            fadd2_acc(d0, d1, e == 0 ? dl.x : dl.z, e == 0 ? dl.y : dl.w);
             fmul2(x[i], x[i + 1], d0, d1, p0, p1);
             pp[i / 2] = pack2(p0, p1);
             pd[i / 2] = pack2(x[i], x[i + 1]);
@@ -726,18 +743,19 @@ __global__ void __launch_bounds__(kTcThreads, 2)
         for (int a = 0; a < NA; ++a) {
           char* to = mine + a * axis_bytes;
           const int4* xs = reinterpret_cast<const int4*>(&S.pos[st][a][col]);
-          if (cb.mode[a] <= kLane) {
+          const int md = cb.mode(a, 2 * half + g);
+          if (md <= kLane) {
             float s0 = 0.0f, s1 = 0.0f;
 #pragma unroll
             for (int e = 0; e < 16; e += 2) fadd2_acc(s0, s1, x[e], x[e + 1]);
-            const int b = boff[cb.mode[a] == kOne ? cb.one[a] : clamp_index(-xs[0].x, rowc[a], top)];
+            const int b = boff[md == kOne ? cb.one[a] : clamp_index(-xs[0].x, rowc[a], top)];
             if (b != run_b[a]) {
               *reinterpret_cast<float*>(to + run_b[a]) += run[a];
               run[a] = 0.0f;
               run_b[a] = b;
             }
             run[a] += s0 + s1;
-          } else if (cb.mode[a] == kFour) {
+          } else if (md == kFour) {
 #pragma unroll
             for (int f = 0; f < 4; f += 2)
               add_two_tc(to, boff[clamp_index(-xs[f].x, rowc[a], top)],
@@ -759,7 +777,7 @@ __global__ void __launch_bounds__(kTcThreads, 2)
       }
       tmem_st_wait();
       tc_fence_before();
-      mbar_arrive(&S.p_full);
+      mbar_arrive(&S.p_full[half]);
       if (cc == nc - 1) {
         // the head's sums of the CTA's threads to global memory, and the columns back to 0
 #pragma unroll
@@ -783,7 +801,9 @@ __global__ void __launch_bounds__(kTcThreads, 2)
         ok = eb.sync() && ok;
       }
     }
-    if (ok && steps > 0) ok = mbar_wait_w(&S.done, (steps - 1) & 1, abort, p.status);
+    if (ok && steps > 0)
+      ok = wait_bar_w(&S.done[0], (steps - 1) & 1, abort, p.status) &&
+           wait_bar_w(&S.done[1], (steps - 1) & 1, abort, p.status);
     tc_fence_after();
     // one half writes dV, the other dK
     const size_t at = ((size_t)(valid ? row : row0) * p.Hkv + hk) * D;

@@ -143,7 +143,7 @@ __global__ void __launch_bounds__(kTcThreads, 2)
 #pragma unroll
         for (int i = 0; i < 2; ++i)  // positions past the end repeat the last key's
           x[a][i] = p.pos_k[(size_t)(key + min(lane + 32 * i, n - 1)) * NA + a];
-      if (c >= C::kStages && !mbar_wait_w(&S.kv_empty[st], ((c / C::kStages) + 1) & 1, abort, p.status)) break;
+      if (c >= C::kStages && !wait_bar_w(&S.kv_empty[st], ((c / C::kStages) + 1) & 1, abort, p.status)) break;
       note_positions<NA>(x, S.pos[st], S.meta[st], lane, p.status);
       if (n < C::kKeys) {
         copy_tail<D>(S.v[st], p.v, key, n, p.Hkv, hk, lane);
@@ -160,14 +160,14 @@ __global__ void __launch_bounds__(kTcThreads, 2)
     if (lane == 0 && *abort) {
       // let the copies already issued land before the CTA's shared memory goes away
       volatile int no_abort = 0;
-      if (chunks > 0) mbar_wait(&S.q_full, 0, &no_abort, nullptr);
+      if (chunks > 0) wait_bar(&S.q_full, 0, &no_abort, nullptr);
       for (int c = max(0, issued - C::kStages); c < issued; ++c)
-        mbar_wait(&S.kv_full[c % C::kStages], (c / C::kStages) & 1, &no_abort, nullptr);
+        wait_bar(&S.kv_full[c % C::kStages], (c / C::kStages) & 1, &no_abort, nullptr);
     }
   } else if (warp == 1) {
     // ---------------- MMA issuer: one thread, which mostly waits for the softmax ----------------
     if (lane == 0 && chunks > 0) {
-      bool ok = mbar_wait(&S.q_full, 0, abort, p.status);
+      bool ok = wait_bar(&S.q_full, 0, abort, p.status);
       tc_fence_after();
       const uint64_t qdesc[2] = {smem_desc(smem_u32(S.q[0]), 16, C::kAtomBytes, C::kLayout),
                                  smem_desc(smem_u32(S.q[1]), 16, C::kAtomBytes, C::kLayout)};
@@ -191,11 +191,11 @@ __global__ void __launch_bounds__(kTcThreads, 2)
         mma_commit(&S.pv_done[t]);
       };
       for (int c = 0; ok && c < chunks; ++c) {
-        if (!mbar_wait(&S.kv_full[c % C::kStages], (c / C::kStages) & 1, abort, p.status)) { ok = false; break; }
+        if (!wait_bar(&S.kv_full[c % C::kStages], (c / C::kStages) & 1, abort, p.status)) { ok = false; break; }
         tc_fence_after();
         for (int t = 0; t < tiles; ++t) {
           if (c > 0) {
-            if (!mbar_wait(&S.p_full[t], (c - 1) & 1, abort, p.status)) { ok = false; break; }
+            if (!wait_bar(&S.p_full[t], (c - 1) & 1, abort, p.status)) { ok = false; break; }
             tc_fence_after();
           }
           if (!C::kAlias) {
@@ -210,7 +210,7 @@ __global__ void __launch_bounds__(kTcThreads, 2)
         if (C::kAlias) {
           for (int t = 0; t < tiles; ++t) {
             // S(c) overwrites P(c - 1), so that product has to be done
-            if (c > 0 && !mbar_wait(&S.pv_done[t], (c - 1) & 1, abort, p.status)) { ok = false; break; }
+            if (c > 0 && !wait_bar(&S.pv_done[t], (c - 1) & 1, abort, p.status)) { ok = false; break; }
             tc_fence_after();
             issue_qk(t, c);
           }
@@ -219,14 +219,14 @@ __global__ void __launch_bounds__(kTcThreads, 2)
         if (c > 0) mma_commit(&S.kv_empty[(c - 1) % C::kStages]);
       }
       for (int t = 0; ok && t < tiles; ++t) {
-        if (!mbar_wait(&S.p_full[t], (chunks - 1) & 1, abort, p.status)) { ok = false; break; }
+        if (!wait_bar(&S.p_full[t], (chunks - 1) & 1, abort, p.status)) { ok = false; break; }
         tc_fence_after();
         issue_pv(t, chunks - 1);
       }
       // every MMA issued so far must finish before the CTA can release tensor and shared memory
       mma_commit(&S.drain);
       volatile int no_abort = 0;
-      mbar_wait(&S.drain, 0, &no_abort, nullptr);
+      wait_bar(&S.drain, 0, &no_abort, nullptr);
     }
   } else if (((warp - 2) >> 2) < tiles) {
     // ---------------- softmax: one row a thread ----------------
@@ -243,12 +243,12 @@ __global__ void __launch_bounds__(kTcThreads, 2)
       q_hi[a] = __reduce_max_sync(0xffffffffu, x);
       if (q_lo[a] < -kPosLimit || q_hi[a] > kPosLimit) raise_status(p.status, LSRM_ERR_BOUNDS);
     }
-    auto wait_all = [&](uint64_t* bar, uint32_t parity) -> bool { return mbar_wait_w(bar, parity, abort, p.status); };
+    auto wait_all = [&](uint64_t* bar, uint32_t parity) -> bool { return wait_bar_w(bar, parity, abort, p.status); };
 
     float m = 0.0f, l = 0.0f;  // the row's reference (in the scores' units) and sum
     bool ok = true;
     int st = 0, left = 0;  // the current chunk's stage and keys from here on
-    ChunkBias<NA, 1> cb;
+    ChunkBias<NA, 1, false> cb;
 
     // The chunk again, or a chunk of a table too large to fold: its maximum, the reference of the rows
     // that are `off` (or, without folding, behind their maximum) moved to it, and P from the scores in
@@ -259,7 +259,7 @@ __global__ void __launch_bounds__(kTcThreads, 2)
       for (int g = 0; g < 4; ++g) {
         uint32_t r[16];
         float b[16];
-        cb.all16(b, cb.ub, S.pos[st], 16 * g, rowc, S.lut, top);
+        cb.all16(b, cb.ub, S.pos[st], g, rowc, S.lut, top);
         tmem_ld16(tbase + C::kColS + 16 * g, r);
         tmem_wait16(r);
 #pragma unroll
@@ -286,7 +286,7 @@ __global__ void __launch_bounds__(kTcThreads, 2)
       for (int g = 0; g < 4; ++g) {
         uint32_t r[16], pk[8];
         float b[16];
-        cb.all16(b, cb.ub, S.pos[st], 16 * g, rowc, S.lut, top);
+        cb.all16(b, cb.ub, S.pos[st], g, rowc, S.lut, top);
         tmem_ld16(tbase + C::kColS + 16 * g, r);
         tmem_wait16(r);
 #pragma unroll
@@ -326,12 +326,12 @@ __global__ void __launch_bounds__(kTcThreads, 2)
 #pragma unroll
           for (int g = 0; g < 2; ++g) {
             float b[16];
-            if (cb.worst > kLane) {
-              cb.all16(b, base, S.pos[st], 32 * hf + 16 * g, rowc, S.lut, top);
+            if (!cb.flat(2 * hf + g)) {
+              cb.all16(b, base, S.pos[st], 2 * hf + g, rowc, S.lut, top);
 #pragma unroll
               for (int e = 0; e < 16; ++e) b[e] = fmaf(__uint_as_float(r[16 * g + e]), mul, b[e]);
             } else {
-              const float one = cb.row16(base, S.pos[st], 32 * hf + 16 * g, rowc, S.lut, top);
+              const float one = cb.row16(base, S.pos[st], 2 * hf + g, rowc, S.lut, top);
 #pragma unroll
               for (int e = 0; e < 16; e += 2)
                 ffma2(b[e], b[e + 1], __uint_as_float(r[16 * g + e]), __uint_as_float(r[16 * g + e + 1]), mul, one);

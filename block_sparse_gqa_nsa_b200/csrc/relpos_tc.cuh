@@ -25,6 +25,7 @@ struct TcTile {
   static constexpr uint32_t kAtomBytes = 8 * kRowBytes;
   static constexpr int kRowsBytes = 128 * kRowBytes, kColsBytes = kTcCols * kRowBytes;
   static constexpr uint32_t kIdescScore = idesc_bf16(128, kTcCols, false);  // rows x columns
+  static constexpr uint32_t kIdescHalf = idesc_bf16(128, kTcCols / 2, false);  // half of the columns
   static constexpr uint32_t kIdescSum = idesc_bf16(128, D, true);           // rows x D over the columns
 };
 
@@ -41,6 +42,27 @@ __device__ __forceinline__ void tmem_wait16(uint32_t* r) {
 __device__ __forceinline__ void tmem_wait32(uint32_t* r) {
   tmem_wait16(r);
   tmem_wait16(r + 16);
+}
+
+// Bounded waits as tc::mbar_wait, which look at the abort flag and the clock only every 32 tries: a
+// waiting thread then issues little beside the tries themselves.
+__device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity, volatile int* abort, uint32_t* status) {
+  if (mbar_try_wait(bar, parity)) return true;
+  const uint64_t t0 = globaltimer_ns();
+  while (true) {
+#pragma unroll 1
+    for (int i = 0; i < 32; ++i)
+      if (mbar_try_wait(bar, parity)) return true;
+    if (*abort) return false;
+    if (globaltimer_ns() - t0 > kWaitLimitNs) {
+      *abort = 1;
+      raise_status(status, LSRM_ERR_TIMEOUT);
+      return false;
+    }
+  }
+}
+__device__ __forceinline__ bool wait_bar_w(uint64_t* bar, uint32_t parity, volatile int* abort, uint32_t* status) {
+  return __all_sync(0xffffffffu, wait_bar(bar, parity, abort, status));
 }
 
 // 64 rows of a [tokens][heads][D] tensor into a stage in the layout that TMA writes, zeros past n: what
@@ -60,77 +82,100 @@ __device__ __forceinline__ void copy_tail(uint8_t* dst, const uint16_t* src, int
 }
 __device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory"); }
 
-// what a chunk's column positions have in common
+// what a chunk's column positions have in common on each axis: their range, and bit g of same16 / same4:
+// columns 16 g .. 16 g + 15 have one position / one position per aligned run of four
 struct ChunkMeta {
   int lo[kMaxAxes], hi[kMaxAxes];
-  uint32_t same16, same4;  // bit a: aligned runs of 16 / 4 columns have one position on axis a
+  uint32_t same16[kMaxAxes], same4[kMaxAxes];
 };
 // the producer warp's part: lane i holds the positions of columns i and i + 32
 template <int NA>
 __device__ __forceinline__ void note_positions(const int (&x)[NA][2], int (*pos)[kTcCols], ChunkMeta& m, int lane,
                                                uint32_t* status) {
-  uint32_t same16 = 0, same4 = 0;
 #pragma unroll
   for (int a = 0; a < NA; ++a) {
     const int lo = __reduce_min_sync(0xffffffffu, min(x[a][0], x[a][1]));
     const int hi = __reduce_max_sync(0xffffffffu, max(x[a][0], x[a][1]));
     if (lo < -kPosLimit || hi > kPosLimit) raise_status(status, LSRM_ERR_BOUNDS);
-    const uint32_t e = __ballot_sync(0xffffffffu, x[a][0] == __shfl_down_sync(0xffffffffu, x[a][0], 1)) &
-                       __ballot_sync(0xffffffffu, x[a][1] == __shfl_down_sync(0xffffffffu, x[a][1], 1));
-    if ((e & 0x7fff7fffu) == 0x7fff7fffu) same16 |= 1u << a;
-    if ((e & 0x77777777u) == 0x77777777u) same4 |= 1u << a;
+    const uint32_t e0 = __ballot_sync(0xffffffffu, x[a][0] == __shfl_down_sync(0xffffffffu, x[a][0], 1));
+    const uint32_t e1 = __ballot_sync(0xffffffffu, x[a][1] == __shfl_down_sync(0xffffffffu, x[a][1], 1));
     pos[a][lane] = x[a][0];
     pos[a][lane + 32] = x[a][1];
-    if (lane == 0) m.lo[a] = lo, m.hi[a] = hi;
+    if (lane == 0) {
+      uint32_t same16 = 0, same4 = 0;
+#pragma unroll
+      for (int g = 0; g < 4; ++g) {
+        const uint32_t e = (g < 2 ? e0 : e1) >> (16 * (g & 1));
+        if ((e & 0x7fffu) == 0x7fffu) same16 |= 1u << g;
+        if ((e & 0x7777u) == 0x7777u) same4 |= 1u << g;
+      }
+      m.lo[a] = lo, m.hi[a] = hi;
+      m.same16[a] = same16, m.same4[a] = same4;
+    }
   }
-  if (lane == 0) m.same16 = same16, m.same4 = same4;
 }
 
-// A chunk's modes for a warp's rows (kOne, kLane: 16 columns, kFour, kEach) and the bias common to it.
-// SIGN as for add_bias.
-template <int NA, int SIGN>
+// A chunk's biases for a warp's rows.  Per axis and run of 16 columns: kOne (the chunk has one clamped
+// distance), kLane (one position in the run), kFour (one per four columns), kEach.  SIGN as for add_bias.
+// RUNS: told run by run, which suits rows of patches whose ends fall anywhere (six frames' training step
+// 1401 -> 1329 us); else for the chunk as a whole, which costs less per run (forward over bricks of
+// three axes 612 -> 531 us).
+template <int NA, int SIGN, bool RUNS>
 struct ChunkBias {
-  int mode[NA], one[NA], worst;
-  float ub;
+  int one[NA];  // the chunk's only index into the table, or -1
+  int whole[NA];
+  uint32_t same16[NA], same4[NA];
+  float ub;  // the bias common to the chunk
   __device__ __forceinline__ void set(const ChunkMeta& m, const int (&row_lo)[NA], const int (&row_hi)[NA], int maxd,
                                       const float* lut, int top) {
-    worst = kOne;
     ub = 0.0f;
 #pragma unroll
     for (int a = 0; a < NA; ++a) {
       const int lo = clamp_index(SIGN > 0 ? m.lo[a] - row_hi[a] : row_lo[a] - m.hi[a], maxd, top);
       const int hi = clamp_index(SIGN > 0 ? m.hi[a] - row_lo[a] : row_hi[a] - m.lo[a], maxd, top);
-      one[a] = lo;
-      mode[a] = lo == hi ? kOne : (m.same16 >> a) & 1 ? kLane : (m.same4 >> a) & 1 ? kFour : kEach;
-      worst = max(worst, mode[a]);
-      if (mode[a] == kOne) ub += lut[a * (top + 1) + lo];
+      one[a] = lo == hi ? lo : -1;
+      same16[a] = m.same16[a], same4[a] = m.same4[a];
+      whole[a] = lo == hi ? kOne : same16[a] == 15u ? kLane : same4[a] == 15u ? kFour : kEach;
+      if (lo == hi) ub += lut[a * (top + 1) + lo];
     }
   }
-  // the row's bias of a run of 16 columns that has only one (worst <= kLane), on top of base
-  __device__ __forceinline__ float row16(float base, int (*pos)[kTcCols], int col, const int (&rowc)[NA],
+  __device__ __forceinline__ int mode(int a, int g) const {
+    if (!RUNS) return whole[a];
+    return one[a] >= 0 ? kOne : (same16[a] >> g & 1) ? kLane : (same4[a] >> g & 1) ? kFour : kEach;
+  }
+  // whether run g has one bias per row
+  __device__ __forceinline__ bool flat(int g) const {
+    bool f = true;
+#pragma unroll
+    for (int a = 0; a < NA; ++a) f = f && mode(a, g) <= kLane;
+    return f;
+  }
+  // the row's part of run g that is the same for its columns, on top of base
+  __device__ __forceinline__ float row16(float base, int (*pos)[kTcCols], int g, const int (&rowc)[NA],
                                          const float* lut, int top) const {
 #pragma unroll
     for (int a = 0; a < NA; ++a)
-      if (mode[a] == kLane) base += lut[a * (top + 1) + clamp_index(SIGN * pos[a][col], rowc[a], top)];
+      if (mode(a, g) == kLane) base += lut[a * (top + 1) + clamp_index(SIGN * pos[a][16 * g], rowc[a], top)];
     return base;
   }
-  // the biases of columns col .. col + 15 on top of base
-  __device__ __forceinline__ void all16(float (&b)[16], float base, int (*pos)[kTcCols], int col, const int (&rowc)[NA],
+  // the biases of run g on top of base
+  __device__ __forceinline__ void all16(float (&b)[16], float base, int (*pos)[kTcCols], int g, const int (&rowc)[NA],
                                         const float* lut, int top) const {
-    base = row16(base, pos, col, rowc, lut, top);
+    base = row16(base, pos, g, rowc, lut, top);
 #pragma unroll
     for (int e = 0; e < 16; ++e) b[e] = base;
 #pragma unroll
     for (int a = 0; a < NA; ++a) {
       const float* la = lut + a * (top + 1);
-      const int4* xs = reinterpret_cast<const int4*>(&pos[a][col]);
-      if (mode[a] == kFour) {
+      const int4* xs = reinterpret_cast<const int4*>(&pos[a][16 * g]);
+      const int m = mode(a, g);
+      if (m == kFour) {
 #pragma unroll
         for (int f = 0; f < 4; ++f) {
           const float y = la[clamp_index(SIGN * xs[f].x, rowc[a], top)];
           b[4 * f] += y, b[4 * f + 1] += y, b[4 * f + 2] += y, b[4 * f + 3] += y;
         }
-      } else if (mode[a] == kEach) {
+      } else if (m == kEach) {
 #pragma unroll
         for (int f = 0; f < 4; ++f) {
           const int4 x = xs[f];
