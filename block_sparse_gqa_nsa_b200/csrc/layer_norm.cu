@@ -103,44 +103,53 @@ struct LnFwd {
   float eps;
 };
 
-// Rows in registers: TPR threads a row, NV vectors of VEC elements a thread (C <= TPR * VEC * NV)
-template <typename T, int VEC, int TPR, int NV>
+// Rows in registers: TPR threads a row, NV vectors of VEC elements a thread (C <= TPR * VEC * NV), R rows
+// a thread group at once, all loaded before the first is used
+template <typename T, int VEC, int TPR, int NV, int R>
 __global__ void __launch_bounds__(kLnThreads) ln_fwd_kernel(const LnFwd p) {
   __shared__ float red[kLnWarps];
-  constexpr int kRowsPerCta = kLnThreads / TPR;
+  constexpr int kGroups = kLnThreads / TPR;
   const int sub = threadIdx.x % TPR;
-  const long long row = (long long)blockIdx.x * kRowsPerCta + threadIdx.x / TPR;
-  const bool live = row < p.rows;
-  const T* x = static_cast<const T*>(p.x) + (live ? row : 0) * p.C;
-  LnVec<T, VEC> xv[NV];
-  float s = 0.0f;
+  const long long row0 = (long long)blockIdx.x * (kGroups * R) + threadIdx.x / TPR;
+  LnVec<T, VEC> xv[R][NV];
 #pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const int c = (i * TPR + sub) * VEC;
-    if (live && c < p.C)
-      xv[i].load(x + c);
-    else
-      xv[i].zero();
-  }
+  for (int k = 0; k < R; ++k) {
+    const long long row = row0 + k * kGroups;
+    const T* x = static_cast<const T*>(p.x) + (row < p.rows ? row : 0) * p.C;
 #pragma unroll
-  for (int i = 0; i < NV; ++i)
-#pragma unroll
-    for (int e = 0; e < VEC; ++e) s += xv[i].get(e);
-  const float mean = ln_row_sum<TPR>(s, red) / (float)p.C;
-  s = 0.0f;
-#pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    if ((i * TPR + sub) * VEC < p.C) {
-#pragma unroll
-      for (int e = 0; e < VEC; ++e) {
-        const float d = xv[i].get(e) - mean;
-        s = fmaf(d, d, s);
-      }
+    for (int i = 0; i < NV; ++i) {
+      const int c = (i * TPR + sub) * VEC;
+      if (row < p.rows && c < p.C)
+        xv[k][i].load(x + c);
+      else
+        xv[k][i].zero();
     }
   }
-  const float rstd = rsqrtf(ln_row_sum<TPR>(s, red) / (float)p.C + p.eps);
-  if (!live) return;
-  T* y = static_cast<T*>(p.y) + row * p.C;
+  float mean[R], rstd[R];
+#pragma unroll
+  for (int k = 0; k < R; ++k) {
+    float s = 0.0f;
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) s += xv[k][i].get(e);
+    mean[k] = ln_row_sum<TPR>(s, red) / (float)p.C;
+  }
+#pragma unroll
+  for (int k = 0; k < R; ++k) {
+    float s = 0.0f;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      if ((i * TPR + sub) * VEC < p.C) {
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) {
+          const float d = xv[k][i].get(e) - mean[k];
+          s = fmaf(d, d, s);
+        }
+      }
+    }
+    rstd[k] = rsqrtf(ln_row_sum<TPR>(s, red) / (float)p.C + p.eps);
+  }
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
     const int c = (i * TPR + sub) * VEC;
@@ -149,17 +158,27 @@ __global__ void __launch_bounds__(kLnThreads) ln_fwd_kernel(const LnFwd p) {
     if (p.gamma != nullptr) gv.load(static_cast<const T*>(p.gamma) + c);
     if (p.beta != nullptr) bv.load(static_cast<const T*>(p.beta) + c);
 #pragma unroll
-    for (int e = 0; e < VEC; ++e) {
-      float o = (xv[i].get(e) - mean) * rstd;
-      if (p.gamma != nullptr) o *= gv.get(e);
-      if (p.beta != nullptr) o += bv.get(e);
-      xv[i].set(e, o);
+    for (int k = 0; k < R; ++k) {
+      const long long row = row0 + k * kGroups;
+      if (row >= p.rows) continue;
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) {
+        float o = (xv[k][i].get(e) - mean[k]) * rstd[k];
+        if (p.gamma != nullptr) o *= gv.get(e);
+        if (p.beta != nullptr) o += bv.get(e);
+        xv[k][i].set(e, o);
+      }
+      xv[k][i].store(static_cast<T*>(p.y) + row * p.C + c);
     }
-    xv[i].store(y + c);
   }
   if (sub == 0) {
-    if (p.mean != nullptr) p.mean[row] = mean;
-    if (p.rstd != nullptr) p.rstd[row] = rstd;
+#pragma unroll
+    for (int k = 0; k < R; ++k) {
+      const long long row = row0 + k * kGroups;
+      if (row >= p.rows) continue;
+      if (p.mean != nullptr) p.mean[row] = mean[k];
+      if (p.rstd != nullptr) p.rstd[row] = rstd[k];
+    }
   }
 }
 
@@ -205,11 +224,12 @@ struct LnBwd {
   int C;
 };
 
-template <typename T, int VEC, int TPR, int NV>
+// Rows shared by a lane group of a warp: TPR threads a row, R rows a group at once
+template <typename T, int VEC, int TPR, int NV, int R>
 __global__ void __launch_bounds__(kLnThreads) ln_bwd_kernel(const LnBwd p) {
-  __shared__ float red[kLnWarps];
-  __shared__ float cols[TPR < kLnThreads ? kLnWarps : 1][2][TPR < kLnThreads ? 32 * VEC : 1];
-  constexpr int kRowsPerCta = kLnThreads / TPR;
+  static_assert(TPR <= 32, "a lane group");
+  __shared__ float cols[kLnWarps][2][32 * VEC];
+  constexpr int kGroups = kLnThreads / TPR;
   const int sub = threadIdx.x % TPR;
   LnVec<T, VEC> gv[NV];
 #pragma unroll
@@ -231,93 +251,197 @@ __global__ void __launch_bounds__(kLnThreads) ln_bwd_kernel(const LnBwd p) {
     for (int e = 0; e < VEC; ++e) dg[i][e] = db[i][e] = 0.0f;
 
   const float inv_c = 1.0f / (float)p.C;
-  const long long steps = (p.rows + kRowsPerCta - 1) / kRowsPerCta;
+  const long long steps = (p.rows + kGroups * R - 1) / (kGroups * R);
   for (long long it = blockIdx.x; it < steps; it += gridDim.x) {
-    const long long row = it * kRowsPerCta + threadIdx.x / TPR;
-    const bool live = row < p.rows;
-    const long long at = (live ? row : 0) * p.C;
-    const float mean = live ? p.mean[row] : 0.0f, rstd = live ? p.rstd[row] : 0.0f;
-    LnVec<T, VEC> xv[NV], dv[NV];
+    const long long row0 = it * (kGroups * R) + threadIdx.x / TPR;
+    LnVec<T, VEC> xv[R][NV], dv[R][NV];
+    float mean[R], rstd[R];
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int c = (i * TPR + sub) * VEC;
-      if (live && c < p.C) {
-        xv[i].load(static_cast<const T*>(p.x) + at + c);
-        dv[i].load(static_cast<const T*>(p.dy) + at + c);
-      } else {
-        xv[i].zero();
-        dv[i].zero();
+    for (int k = 0; k < R; ++k) {
+      const long long row = row0 + k * kGroups;
+      const bool live = row < p.rows;
+      const long long at = (live ? row : 0) * p.C;
+      mean[k] = live ? p.mean[row] : 0.0f;
+      rstd[k] = live ? p.rstd[row] : 0.0f;
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        const int c = (i * TPR + sub) * VEC;
+        if (live && c < p.C) {
+          xv[k][i].load(static_cast<const T*>(p.x) + at + c);
+          dv[k][i].load(static_cast<const T*>(p.dy) + at + c);
+        } else {
+          xv[k][i].zero();
+          dv[k][i].zero();
+        }
       }
     }
-    float sg = 0.0f, sgx = 0.0f;
 #pragma unroll
-    for (int i = 0; i < NV; ++i)
+    for (int k = 0; k < R; ++k) {
+      const long long row = row0 + k * kGroups;
+      float sg = 0.0f, sgx = 0.0f;
 #pragma unroll
-      for (int e = 0; e < VEC; ++e) {
-        const float xh = (xv[i].get(e) - mean) * rstd, d = dv[i].get(e), g = d * gv[i].get(e);
-        sg += g;
-        sgx = fmaf(g, xh, sgx);
-        dg[i][e] = fmaf(d, xh, dg[i][e]);
-        db[i][e] += d;
-      }
-    sg = ln_row_sum<TPR>(sg, red) * inv_c;
-    sgx = ln_row_sum<TPR>(sgx, red) * inv_c;
-    if (live) {
+      for (int i = 0; i < NV; ++i)
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) {
+          const float xh = (xv[k][i].get(e) - mean[k]) * rstd[k], d = dv[k][i].get(e), g = d * gv[i].get(e);
+          sg += g;
+          sgx = fmaf(g, xh, sgx);
+          dg[i][e] = fmaf(d, xh, dg[i][e]);
+          db[i][e] += d;
+        }
+      sg = ln_row_sum<TPR>(sg, nullptr) * inv_c;
+      sgx = ln_row_sum<TPR>(sgx, nullptr) * inv_c;
+      if (row >= p.rows) continue;
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
         const int c = (i * TPR + sub) * VEC;
         if (c >= p.C) continue;
 #pragma unroll
         for (int e = 0; e < VEC; ++e) {
-          const float xh = (xv[i].get(e) - mean) * rstd, g = dv[i].get(e) * gv[i].get(e);
-          xv[i].set(e, rstd * (g - sg - xh * sgx));
+          const float xh = (xv[k][i].get(e) - mean[k]) * rstd[k], g = dv[k][i].get(e) * gv[i].get(e);
+          xv[k][i].set(e, rstd[k] * (g - sg - xh * sgx));
         }
-        xv[i].store(static_cast<T*>(p.dx) + at + c);
+        xv[k][i].store(static_cast<T*>(p.dx) + row * p.C + c);
       }
     }
   }
 
   // the CTA's column sums, in a fixed order
   float* part = p.part + (long long)blockIdx.x * 2 * p.C;
-  if constexpr (TPR == kLnThreads) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int c = (i * TPR + sub) * VEC;
-      if (c >= p.C) continue;
+  for (int i = 0; i < NV; ++i) {
+    __syncthreads();
 #pragma unroll
-      for (int e = 0; e < VEC; ++e) {
-        part[c + e] = dg[i][e];
-        part[p.C + c + e] = db[i][e];
+    for (int e = 0; e < VEC; ++e) {
+      float a = dg[i][e], b = db[i][e];
+#pragma unroll
+      for (int o = TPR; o < 32; o <<= 1) {
+        a += __shfl_xor_sync(0xffffffffu, a, o);
+        b += __shfl_xor_sync(0xffffffffu, b, o);
+      }
+      if (lane < TPR) {
+        cols[warp][0][lane * VEC + e] = a;
+        cols[warp][1][lane * VEC + e] = b;
       }
     }
-  } else {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    __syncthreads();
+    for (int t = threadIdx.x; t < 2 * TPR * VEC; t += kLnThreads) {
+      const int which = t / (TPR * VEC), c = t % (TPR * VEC), col = i * TPR * VEC + c;
+      if (col >= p.C) continue;
+      float s = 0.0f;
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      __syncthreads();
+      for (int w = 0; w < kLnWarps; ++w) s += cols[w][which][c];
+      part[which * p.C + col] = s;
+    }
+  }
+}
+
+// Rows by whole CTAs of NT threads, one vector a thread (C <= NT * VEC), R rows at once.  A thread keeps
+// the sums of only VEC columns, so several CTAs fit an SM (a warp a row would need 4 x the registers
+// at 1024 columns and leave 8 warps an SM: 177 us against the floor of 115 at 121344 rows); the R rows'
+// statistics cross the warps behind one barrier.
+template <typename T, int VEC, int NT, int R>
+__global__ void __launch_bounds__(NT) ln_bwd_cta_kernel(const LnBwd p) {
+  constexpr int kWarps = NT / 32;
+  static_assert(2 * R <= 32 && (2 * R & (2 * R - 1)) == 0, "the statistics are folded over the lanes");
+  __shared__ float red[2][kWarps][2 * R];
+  const int c = threadIdx.x * VEC, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const bool have = c < p.C;
+  LnVec<T, VEC> gv;
+  gv.zero();
+  if (have) {
+    if (p.gamma != nullptr)
+      gv.load(static_cast<const T*>(p.gamma) + c);
+    else
 #pragma unroll
-      for (int e = 0; e < VEC; ++e) {
-        float a = dg[i][e], b = db[i][e];
+      for (int e = 0; e < VEC; ++e) gv.set(e, 1.0f);
+  }
+  float dg[VEC], db[VEC];
 #pragma unroll
-        for (int o = TPR; o < 32; o <<= 1) {
-          a += __shfl_xor_sync(0xffffffffu, a, o);
-          b += __shfl_xor_sync(0xffffffffu, b, o);
-        }
-        if (lane < TPR) {
-          cols[warp][0][lane * VEC + e] = a;
-          cols[warp][1][lane * VEC + e] = b;
-        }
-      }
-      __syncthreads();
-      for (int t = threadIdx.x; t < 2 * TPR * VEC; t += kLnThreads) {
-        const int which = t / (TPR * VEC), c = t % (TPR * VEC), col = i * TPR * VEC + c;
-        if (col >= p.C) continue;
-        float s = 0.0f;
+  for (int e = 0; e < VEC; ++e) dg[e] = db[e] = 0.0f;
+  const float inv_c = 1.0f / (float)p.C;
+  const long long steps = (p.rows + R - 1) / R;
+  int buf = 0;
+  for (long long it = blockIdx.x; it < steps; it += gridDim.x, buf ^= 1) {
+    LnVec<T, VEC> xv[R], dv[R];
+    float mean[R], rstd[R], s[2 * R];
 #pragma unroll
-        for (int w = 0; w < kLnWarps; ++w) s += cols[w][which][c];
-        part[which * p.C + col] = s;
+    for (int k = 0; k < R; ++k) {
+      const long long row = it * R + k;
+      const bool live = row < p.rows;
+      mean[k] = live ? p.mean[row] : 0.0f;
+      rstd[k] = live ? p.rstd[row] : 0.0f;
+      if (live && have) {
+        xv[k].load(static_cast<const T*>(p.x) + row * p.C + c);
+        dv[k].load(static_cast<const T*>(p.dy) + row * p.C + c);
+      } else {
+        xv[k].zero();
+        dv[k].zero();
       }
     }
+#pragma unroll
+    for (int k = 0; k < R; ++k) {
+      float sg = 0.0f, sgx = 0.0f;
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) {
+        const float xh = (xv[k].get(e) - mean[k]) * rstd[k], d = dv[k].get(e), g = d * gv.get(e);
+        sg += g;
+        sgx = fmaf(g, xh, sgx);
+        dg[e] = fmaf(d, xh, dg[e]);
+        db[e] += d;
+      }
+      s[2 * k] = sg;
+      s[2 * k + 1] = sgx;
+    }
+    // 2 R sums over the warp: while there are several, the halves of the lanes swap the sums they give
+    // up, so 2 R values cost 2 R - 1 + (5 - log2 2R) shuffles instead of 5 each
+    int n = 2 * R, o = 16;
+#pragma unroll
+    for (int step = 0; step < 5; ++step, o >>= 1) {
+      if (n > 1) {
+        n >>= 1;
+        const bool up = (lane & o) != 0;
+#pragma unroll
+        for (int i = 0; i < R; ++i) {
+          if (i >= n) break;
+          const float give = up ? s[i] : s[i + n], keep = up ? s[i + n] : s[i];
+          s[i] = keep + __shfl_xor_sync(0xffffffffu, give, o);
+        }
+      } else {
+        s[0] += __shfl_xor_sync(0xffffffffu, s[0], o);
+      }
+    }
+    // lane bits from the top select the sum that the lane holds
+    constexpr int kFold = 2 * R == 2 ? 1 : 2 * R == 4 ? 2 : 2 * R == 8 ? 3 : 4;
+    if ((lane & ((1 << (5 - kFold)) - 1)) == 0) red[buf][warp][lane >> (5 - kFold)] = s[0];
+    __syncthreads();  // the buffer's last readers are two barriers back
+#pragma unroll
+    for (int k = 0; k < R; ++k) {
+      const long long row = it * R + k;
+      float sg = 0.0f, sgx = 0.0f;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {
+        sg += red[buf][w][2 * k];
+        sgx += red[buf][w][2 * k + 1];
+      }
+      sg *= inv_c;
+      sgx *= inv_c;
+      if (row >= p.rows || !have) continue;
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) {
+        const float xh = (xv[k].get(e) - mean[k]) * rstd[k], g = dv[k].get(e) * gv.get(e);
+        xv[k].set(e, rstd[k] * (g - sg - xh * sgx));
+      }
+      xv[k].store(static_cast<T*>(p.dx) + row * p.C + c);
+    }
+  }
+  if (!have) return;
+  float* part = p.part + (long long)blockIdx.x * 2 * p.C;
+#pragma unroll
+  for (int e = 0; e < VEC; ++e) {
+    part[c + e] = dg[e];
+    part[p.C + c + e] = db[e];
   }
 }
 
@@ -364,17 +488,18 @@ __global__ void __launch_bounds__(kLnThreads) ln_bwd_cols_kernel(const LnBwd p) 
   part[p.C + c] = b;
 }
 
-// dgamma / dbeta = the sum of the CTAs' partials: 32 columns a CTA, its warps take every
-// kLnWarps-th partial, and the warps' sums are added in order
+// dgamma / dbeta = the sum of the CTAs' partials: 32 columns a CTA, its warps take every 32nd partial,
+// and the warps' sums are added in order
 template <typename T>
-__global__ void __launch_bounds__(kLnThreads) ln_bwd_finish_kernel(const float* part, int n, int C, void* dgamma,
-                                                                   void* dbeta) {
-  __shared__ float s[2][kLnWarps][32];
+__global__ void __launch_bounds__(1024) ln_bwd_finish_kernel(const float* part, int n, int C, void* dgamma,
+                                                             void* dbeta) {
+  __shared__ float s[2][32][33];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int c = blockIdx.x * 32 + lane;
   float a = 0.0f, b = 0.0f;
   if (c < C) {
-    for (int i = warp; i < n; i += kLnWarps) {
+#pragma unroll 4
+    for (int i = warp; i < n; i += 32) {
       a += part[(long long)i * 2 * C + c];
       b += part[(long long)i * 2 * C + C + c];
     }
@@ -387,29 +512,35 @@ __global__ void __launch_bounds__(kLnThreads) ln_bwd_finish_kernel(const float* 
   if (out == nullptr) return;
   float t = 0.0f;
 #pragma unroll
-  for (int w = 0; w < kLnWarps; ++w) t += s[warp][w][lane];
+  for (int w = 0; w < 32; ++w) t += s[warp][w][lane];
   static_cast<T*>(out)[c] = ln_from_f32<T>(t);
 }
 
 // ---- variants: by the row's width, the element type and alignment alone ----
 //
-// Aligned rows (C a multiple of the vector, pointers on 16 bytes): the fewest lanes that hold the
-// row with one vector each up to a warp, then up to kNvMax vectors a lane, then a CTA a row.
-// Others: single elements, coalesced across the lanes.
+// Aligned rows (C a multiple of the vector, pointers on 16 bytes): the fewest lanes that hold the row
+// with one vector each up to a warp; then the forward takes up to 8 (bf16) or 16 (fp32) vectors a lane
+// and a CTA a row past that, the backward whole CTAs of 64 to 1024 threads with one vector each.
+// Others: single elements, coalesced across the lanes, up to 32 (backward 16) a lane.
 struct LnShape {
-  int vec, tpr, nv;  // nv = 0: the wide kernels
+  int vec, tpr, nv;  // nv = 0: the wide kernels; the backward's tpr > 32: CTAs of tpr threads
 };
 
 LnShape ln_shape(int C, int elem, bool vec_ok, bool backward) {
   const int vec = vec_ok ? 16 / elem : 1;
   const int n = (C + vec - 1) / vec;  // vectors a row
-  // elements a lane may hold: the backward keeps two fp32 sums per element beside the row itself
-  const int most = vec_ok ? (backward ? 32 / vec : 64 / vec) : (backward ? 16 : 32);
+  const int most = vec_ok ? (backward ? 1 : 64 / vec) : (backward ? 16 : 32);
   int tpr = 1;
   while (tpr < 32 && tpr < n) tpr *= 2;
   int nv = 1;
   while (nv * tpr < n) nv *= 2;
   if (nv <= most) return {vec, tpr, nv};
+  if (backward) {
+    if (!vec_ok) return {1, kLnThreads, 0};
+    while (tpr < n && tpr <= 1024) tpr *= 2;
+    if (tpr <= 1024) return {vec, tpr, 1};
+    return {1, kLnThreads, 0};
+  }
   tpr = kLnThreads;
   nv = 1;
   while (nv * tpr < n) nv *= 2;
@@ -417,69 +548,108 @@ LnShape ln_shape(int C, int elem, bool vec_ok, bool backward) {
   return {1, kLnThreads, 0};
 }
 
+lsrm_status ln_launched() { return cudaGetLastError() == cudaSuccess ? LSRM_OK : LSRM_ERR_CUDA; }
+
+// rows a group takes at once: four where a thread holds 16 bytes of a row, as long as that still leaves
+// every SM a few CTAs
+#ifndef LN_RF
+#define LN_RF 4
+#define LN_RB 4
+#define LN_RC 4
+#define LN_RW 1
+#endif
 template <typename T, int VEC, int TPR, int NV>
 lsrm_status ln_run_fwd(const LnFwd& p, cudaStream_t s) {
-  constexpr int kRows = kLnThreads / TPR;
-  const long long ctas = (p.rows + kRows - 1) / kRows;
+  constexpr int kGroups = kLnThreads / TPR, R = NV * VEC * (int)sizeof(T) <= 16 ? LN_RF : LN_RW;
+  if (R > 1 && p.rows >= (long long)kGroups * R * 4 * kLnSms) {
+    const long long ctas = (p.rows + kGroups * R - 1) / (kGroups * R);
+    if (ctas > (long long)INT32_MAX) return LSRM_ERR_UNSUPPORTED;
+    ln_fwd_kernel<T, VEC, TPR, NV, R><<<(unsigned)ctas, kLnThreads, 0, s>>>(p);
+    return ln_launched();
+  }
+  const long long ctas = (p.rows + kGroups - 1) / kGroups;
   if (ctas > (long long)INT32_MAX) return LSRM_ERR_UNSUPPORTED;
-  ln_fwd_kernel<T, VEC, TPR, NV><<<(unsigned)ctas, kLnThreads, 0, s>>>(p);
-  return cudaGetLastError() == cudaSuccess ? LSRM_OK : LSRM_ERR_CUDA;
+  ln_fwd_kernel<T, VEC, TPR, NV, 1><<<(unsigned)ctas, kLnThreads, 0, s>>>(p);
+  return ln_launched();
+}
+
+// CTAs of a persistent backward kernel: as many as are resident, or as there are steps
+template <typename K>
+lsrm_status ln_ctas(K kernel, int threads, long long steps, int max_ctas, int* ctas) {
+  int per_sm = 0;
+  if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, threads, 0) != cudaSuccess) return LSRM_ERR_CUDA;
+  const long long fit = (long long)kLnSms * (per_sm > 0 ? per_sm : 1);
+  long long n = steps < fit ? steps : fit;
+  if (n > max_ctas) n = max_ctas;
+  *ctas = (int)n;
+  return n < 1 ? LSRM_ERR_CUDA : LSRM_OK;
 }
 
 template <typename T, int VEC, int TPR, int NV>
 lsrm_status ln_run_bwd(const LnBwd& p, int max_ctas, int* ctas, cudaStream_t s) {
-  constexpr int kRows = kLnThreads / TPR;
-  int per_sm = 0;
-  if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, ln_bwd_kernel<T, VEC, TPR, NV>, kLnThreads, 0) !=
-      cudaSuccess)
-    return LSRM_ERR_CUDA;
-  const long long want = (p.rows + kRows - 1) / kRows, fit = (long long)kLnSms * (per_sm > 0 ? per_sm : 1);
-  long long n = want < fit ? want : fit;
-  if (n > max_ctas) n = max_ctas;
-  if (n < 1) return LSRM_ERR_CUDA;
-  *ctas = (int)n;
-  ln_bwd_kernel<T, VEC, TPR, NV><<<(unsigned)n, kLnThreads, 0, s>>>(p);
-  return cudaGetLastError() == cudaSuccess ? LSRM_OK : LSRM_ERR_CUDA;
+  lsrm_status st;
+  if constexpr (TPR > 32) {
+    constexpr int R = LN_RC;
+    auto kernel = ln_bwd_cta_kernel<T, VEC, TPR, R>;
+    if ((st = ln_ctas(kernel, TPR, (p.rows + R - 1) / R, max_ctas, ctas)) != LSRM_OK) return st;
+    kernel<<<(unsigned)*ctas, TPR, 0, s>>>(p);
+  } else {
+    constexpr int kGroups = kLnThreads / TPR, R = VEC > 1 ? LN_RB : 1;
+    auto kernel = ln_bwd_kernel<T, VEC, TPR, NV, R>;
+    if ((st = ln_ctas(kernel, kLnThreads, (p.rows + kGroups * R - 1) / (kGroups * R), max_ctas, ctas)) != LSRM_OK)
+      return st;
+    kernel<<<(unsigned)*ctas, kLnThreads, 0, s>>>(p);
+  }
+  return ln_launched();
 }
 
-// f(vector width, threads a row, vectors a thread) with the shape as template arguments
+// f(vector width, vectors a thread, threads a row) with the shape as template arguments
 template <int V, int N>
 struct LnTag {
   static constexpr int vec = V, nv = N;
 };
-template <int TPR, typename T, typename F>
+template <bool BWD, int TPR, typename T, typename F>
 lsrm_status ln_nv(const LnShape& h, F f) {
   constexpr int V = 16 / sizeof(T);
+  constexpr std::integral_constant<int, TPR> tpr{};
   if (h.vec == V) {
-    switch (h.nv) {
-      case 1: return f(LnTag<V, 1>{}, std::integral_constant<int, TPR>{});
-      case 2: if constexpr (TPR >= 32) return f(LnTag<V, 2>{}, std::integral_constant<int, TPR>{}); break;
-      case 4: if constexpr (TPR >= 32) return f(LnTag<V, 4>{}, std::integral_constant<int, TPR>{}); break;
-      case 8: if constexpr (TPR >= 32) return f(LnTag<V, 8>{}, std::integral_constant<int, TPR>{}); break;
-      case 16: if constexpr (TPR >= 32 && V == 4) return f(LnTag<V, 16>{}, std::integral_constant<int, TPR>{}); break;
+    if (h.nv == 1) return f(LnTag<V, 1>{}, tpr);
+    if constexpr (!BWD && TPR >= 32) {
+      switch (h.nv) {
+        case 2: return f(LnTag<V, 2>{}, tpr);
+        case 4: return f(LnTag<V, 4>{}, tpr);
+        case 8: return f(LnTag<V, 8>{}, tpr);
+        case 16: if constexpr (V == 4) return f(LnTag<V, 16>{}, tpr); break;
+      }
     }
-  } else {
-    switch (h.nv) {
-      case 1: return f(LnTag<1, 1>{}, std::integral_constant<int, TPR>{});
-      case 2: if constexpr (TPR >= 32) return f(LnTag<1, 2>{}, std::integral_constant<int, TPR>{}); break;
-      case 4: if constexpr (TPR >= 32) return f(LnTag<1, 4>{}, std::integral_constant<int, TPR>{}); break;
-      case 8: if constexpr (TPR >= 32) return f(LnTag<1, 8>{}, std::integral_constant<int, TPR>{}); break;
-      case 16: if constexpr (TPR >= 32) return f(LnTag<1, 16>{}, std::integral_constant<int, TPR>{}); break;
-      case 32: if constexpr (TPR >= 32) return f(LnTag<1, 32>{}, std::integral_constant<int, TPR>{}); break;
+  } else if constexpr (!BWD || TPR <= 32) {
+    if (h.nv == 1) return f(LnTag<1, 1>{}, tpr);
+    if constexpr (TPR >= 32) {
+      switch (h.nv) {
+        case 2: return f(LnTag<1, 2>{}, tpr);
+        case 4: return f(LnTag<1, 4>{}, tpr);
+        case 8: return f(LnTag<1, 8>{}, tpr);
+        case 16: return f(LnTag<1, 16>{}, tpr);
+        case 32: if constexpr (!BWD) return f(LnTag<1, 32>{}, tpr); break;
+      }
     }
   }
   return LSRM_ERR_UNSUPPORTED;
 }
-template <typename T, typename F>
+template <bool BWD, typename T, typename F>
 lsrm_status ln_dispatch(const LnShape& h, F f) {
   switch (h.tpr) {
-    case 1: return ln_nv<1, T>(h, f);
-    case 2: return ln_nv<2, T>(h, f);
-    case 4: return ln_nv<4, T>(h, f);
-    case 8: return ln_nv<8, T>(h, f);
-    case 16: return ln_nv<16, T>(h, f);
-    case 32: return ln_nv<32, T>(h, f);
-    case kLnThreads: return ln_nv<kLnThreads, T>(h, f);
+    case 1: return ln_nv<BWD, 1, T>(h, f);
+    case 2: return ln_nv<BWD, 2, T>(h, f);
+    case 4: return ln_nv<BWD, 4, T>(h, f);
+    case 8: return ln_nv<BWD, 8, T>(h, f);
+    case 16: return ln_nv<BWD, 16, T>(h, f);
+    case 32: return ln_nv<BWD, 32, T>(h, f);
+    case 64: if constexpr (BWD) return ln_nv<BWD, 64, T>(h, f); break;
+    case 128: if constexpr (BWD) return ln_nv<BWD, 128, T>(h, f); break;
+    case 256: return ln_nv<BWD, 256, T>(h, f);
+    case 512: if constexpr (BWD) return ln_nv<BWD, 512, T>(h, f); break;
+    case 1024: if constexpr (BWD) return ln_nv<BWD, 1024, T>(h, f); break;
   }
   return LSRM_ERR_UNSUPPORTED;
 }
@@ -495,7 +665,7 @@ lsrm_status ln_forward(const LnFwd& p, cudaStream_t s) {
     ln_fwd_wide_kernel<T><<<(unsigned)p.rows, kLnThreads, 0, s>>>(p);
     return cudaGetLastError() == cudaSuccess ? LSRM_OK : LSRM_ERR_CUDA;
   }
-  return ln_dispatch<T>(h, [&](auto tag, auto tpr) {
+  return ln_dispatch<false, T>(h, [&](auto tag, auto tpr) {
     return ln_run_fwd<T, decltype(tag)::vec, decltype(tpr)::value, decltype(tag)::nv>(p, s);
   });
 }
@@ -516,24 +686,24 @@ lsrm_status ln_backward(const LnBwd& p, void* dgamma, void* dbeta, int max_ctas,
       ln_bwd_wide_kernel<T><<<(unsigned)p.rows, kLnThreads, 0, s>>>(p);
       if (cudaGetLastError() != cudaSuccess) return LSRM_ERR_CUDA;
     } else {
-      const lsrm_status st = ln_dispatch<T>(h, [&](auto tag, auto tpr) {
+      const lsrm_status st = ln_dispatch<true, T>(h, [&](auto tag, auto tpr) {
         return ln_run_bwd<T, decltype(tag)::vec, decltype(tpr)::value, decltype(tag)::nv>(p, max_ctas, &n, s);
       });
       if (st != LSRM_OK) return st;
     }
   }
   if (dgamma == nullptr && dbeta == nullptr) return LSRM_OK;
-  ln_bwd_finish_kernel<T><<<(unsigned)((p.C + 31) / 32), kLnThreads, 0, s>>>(p.part, n, p.C, dgamma, dbeta);
+  ln_bwd_finish_kernel<T><<<(unsigned)((p.C + 31) / 32), 1024, 0, s>>>(p.part, n, p.C, dgamma, dbeta);
   return cudaGetLastError() == cudaSuccess ? LSRM_OK : LSRM_ERR_CUDA;
 }
 
 }  // namespace
 
-// CTAs whose partial sums the workspace holds: as many as can be resident (8 of 256 threads an SM),
+// CTAs whose partial sums the workspace holds: as many as can be resident,
 // or one a row where there are fewer rows.  Rows above kLnWidest never fit registers; their column
 // sums are split kLnWideSplits ways.
 int ln_max_ctas(long long rows, int C) {
-  const long long most = C > kLnWidest ? kLnWideSplits : 8 * kLnSms;
+  const long long most = C > kLnWidest ? kLnWideSplits : 16 * kLnSms;
   return (int)(rows < most ? (rows > 0 ? rows : 1) : most);
 }
 

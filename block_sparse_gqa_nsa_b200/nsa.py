@@ -336,27 +336,40 @@ def lsrm_diag_exp2_poly(x, y, stream=None):
 # These calls check shapes as well, and run on the tensors' own device (its current stream unless
 # one is given), whichever device is current.
 
-def _check_all(device, *items):
-    """(tensor, name, dtype, shape) of each: the type, shape, contiguity and device the call needs."""
+def _check_all(items) -> int:
+    """The type, shape, contiguity and device that the call needs of each (tensor, name, dtype, shape);
+    returns the device index.  Kept lean: small calls are bound by the host."""
+    index = items[0][0].get_device()
     for t, name, dtype, shape in items:
-        if t.dtype != dtype:
+        if t.dtype is not dtype:
             raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
         if t.shape != shape:
             raise ValueError(f"{name}: expected {list(shape)}, got {list(t.shape)}")
         if not t.is_contiguous():
             raise ValueError(f"{name}: must be contiguous")
-        if t.device != device:
-            raise ValueError(f"{name}: on {t.device}, expected {device}")
+        if t.get_device() != index:
+            raise ValueError(f"{name}: on {t.device}, expected {items[0][0].device}")
+    return index
 
 
-def _call_on(device: torch.device, name: str, stream, *args):
-    if device.type != "cuda":
+# the raw handle of a device's current stream, without making a stream object
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _call_on(index: int, name: str, stream, *args):
+    if index < 0:
         raise ValueError(f"{name}: needs CUDA tensors")
-    if device.index == torch.cuda.current_device():
-        _call(name, *args, _stream(stream))
+    if stream is not None:
+        handle = stream.cuda_stream
+    elif _raw_stream is not None:
+        handle = _raw_stream(index)
     else:
-        with torch.cuda.device(device):
-            _call(name, *args, _stream(stream))
+        handle = torch.cuda.current_stream(index).cuda_stream
+    if index == torch.cuda.current_device():
+        _call(name, *args, handle)
+    else:
+        with torch.cuda.device(index):
+            _call(name, *args, handle)
 
 
 def lsrm_relpos_workspace_size(desc: RelposDesc) -> int:
@@ -365,7 +378,7 @@ def lsrm_relpos_workspace_size(desc: RelposDesc) -> int:
 
 def lsrm_relpos_workspace_init(desc: RelposDesc, ws: torch.Tensor, stream=None):
     _check(ws, torch.uint8, "ws")
-    _call_on(ws.device, "lsrm_relpos_workspace_init", stream, ctypes.byref(desc), ws.data_ptr(), ws.numel())
+    _call_on(ws.get_device(), "lsrm_relpos_workspace_init", stream, ctypes.byref(desc), ws.data_ptr(), ws.numel())
 
 
 def relpos_workspace(desc: RelposDesc, device=None, stream=None) -> torch.Tensor:
@@ -408,9 +421,8 @@ def lsrm_relpos_forward(desc: RelposDesc, off_q, off_k, pos_q, pos_k, bucket_of,
         items.append((lse, "lse", torch.float32, qs[:2]))
     if ws is not None:
         items.append((ws, "ws", torch.uint8, ws.shape))
-    _check_all(q.device, *items)
-    _call_on(q.device, "lsrm_relpos_forward", stream, ctypes.byref(desc), *map(_ptr, (off_q, off_k, pos_q, pos_k,
-             bucket_of, table, q, k, v, out, lse, ws)), 0 if ws is None else ws.numel())
+    _call_on(_check_all(items), "lsrm_relpos_forward", stream, ctypes.byref(desc), *map(_ptr, (off_q, off_k, pos_q,
+             pos_k, bucket_of, table, q, k, v, out, lse, ws)), 0 if ws is None else ws.numel())
 
 
 def lsrm_relpos_backward(desc: RelposDesc, off_q, off_k, pos_q, pos_k, bucket_of, table, q, k, v, out, lse, dout,
@@ -418,11 +430,11 @@ def lsrm_relpos_backward(desc: RelposDesc, off_q, off_k, pos_q, pos_k, bucket_of
     """Gradients of lsrm_relpos_forward with respect to q, k, v and the bias table."""
     bf = torch.bfloat16
     qs, ks, items = _relpos_checks(desc, off_q, off_k, pos_q, pos_k, bucket_of, table, q, k, v)
-    _check_all(q.device, *items, (out, "out", bf, qs), (lse, "lse", torch.float32, qs[:2]), (dout, "dout", bf, qs),
-               (dq, "dq", bf, qs), (dk, "dk", bf, ks), (dv, "dv", bf, ks), (dtable, "dtable", bf, table.shape),
-               (ws, "ws", torch.uint8, ws.shape))
-    _call_on(q.device, "lsrm_relpos_backward", stream, ctypes.byref(desc), *map(_ptr, (off_q, off_k, pos_q, pos_k,
-             bucket_of, table, q, k, v, out, lse, dout, dq, dk, dv, dtable, ws)), ws.numel())
+    items += ((out, "out", bf, qs), (lse, "lse", torch.float32, qs[:2]), (dout, "dout", bf, qs), (dq, "dq", bf, qs),
+              (dk, "dk", bf, ks), (dv, "dv", bf, ks), (dtable, "dtable", bf, table.shape),
+              (ws, "ws", torch.uint8, ws.shape))
+    _call_on(_check_all(items), "lsrm_relpos_backward", stream, ctypes.byref(desc), *map(_ptr, (off_q, off_k, pos_q,
+             pos_k, bucket_of, table, q, k, v, out, lse, dout, dq, dk, dv, dtable, ws)), ws.numel())
 
 
 _LN_DTYPES = {torch.bfloat16: 0, torch.float32: 1}
@@ -431,21 +443,28 @@ _LN_DTYPES = {torch.bfloat16: 0, torch.float32: 1}
 def _ln_rows(x):
     if x.dtype not in _LN_DTYPES:
         raise TypeError(f"x: expected torch.bfloat16 or torch.float32, got {x.dtype}")
-    if x.dim() < 1 or x.shape[-1] < 1:
+    shape = x.shape
+    if len(shape) < 1 or shape[-1] < 1:
         raise ValueError("x: needs rows of at least one element")
-    return x.numel() // x.shape[-1], x.shape[-1]
+    return x.numel() // shape[-1], shape[-1]
 
 
 def lsrm_layer_norm_forward(x, gamma, beta, eps, y, mean=None, rstd=None, stream=None):
     """Layer norm over the last axis of x; gamma / beta (or None) of x's type; mean / rstd (optional)
     fp32, one per row, are what the backward needs.  y may be x."""
     rows, width = _ln_rows(x)
-    items = [(x, "x", x.dtype, x.shape), (y, "y", x.dtype, x.shape)]
-    items += [(t, n, x.dtype, (width,)) for t, n in ((gamma, "gamma"), (beta, "beta")) if t is not None]
-    items += [(t, n, torch.float32, (rows,)) for t, n in ((mean, "mean"), (rstd, "rstd")) if t is not None]
-    _check_all(x.device, *items)
-    _call_on(x.device, "lsrm_layer_norm_forward", stream, rows, width, _LN_DTYPES[x.dtype], _ptr(x), _ptr(gamma),
-             _ptr(beta), float(eps), _ptr(y), _ptr(mean), _ptr(rstd))
+    dtype, per_row = x.dtype, (rows,)
+    items = [(x, "x", dtype, x.shape), (y, "y", dtype, x.shape)]
+    if gamma is not None:
+        items.append((gamma, "gamma", dtype, (width,)))
+    if beta is not None:
+        items.append((beta, "beta", dtype, (width,)))
+    if mean is not None:
+        items.append((mean, "mean", torch.float32, per_row))
+    if rstd is not None:
+        items.append((rstd, "rstd", torch.float32, per_row))
+    _call_on(_check_all(items), "lsrm_layer_norm_forward", stream, rows, width, _LN_DTYPES[dtype], _ptr(x),
+             _ptr(gamma), _ptr(beta), eps, _ptr(y), _ptr(mean), _ptr(rstd))
 
 
 def lsrm_layer_norm_workspace_size(rows: int, width: int) -> int:
@@ -463,11 +482,15 @@ def layer_norm_workspace(rows: int, width: int, device=None) -> torch.Tensor:
 def lsrm_layer_norm_backward(dy, x, gamma, mean, rstd, dx, dgamma, dbeta, ws, stream=None):
     """Gradients of lsrm_layer_norm_forward; dgamma / dbeta may be None.  dx may be dy or x."""
     rows, width = _ln_rows(x)
-    items = [(x, "x", x.dtype, x.shape), (dy, "dy", x.dtype, x.shape), (dx, "dx", x.dtype, x.shape),
+    dtype, columns = x.dtype, (width,)
+    items = [(x, "x", dtype, x.shape), (dy, "dy", dtype, x.shape), (dx, "dx", dtype, x.shape),
              (mean, "mean", torch.float32, (rows,)), (rstd, "rstd", torch.float32, (rows,)),
              (ws, "ws", torch.uint8, ws.shape)]
-    items += [(t, n, x.dtype, (width,)) for t, n in ((gamma, "gamma"), (dgamma, "dgamma"), (dbeta, "dbeta"))
-              if t is not None]
-    _check_all(x.device, *items)
-    _call_on(x.device, "lsrm_layer_norm_backward", stream, rows, width, _LN_DTYPES[x.dtype], _ptr(dy), _ptr(x),
+    if gamma is not None:
+        items.append((gamma, "gamma", dtype, columns))
+    if dgamma is not None:
+        items.append((dgamma, "dgamma", dtype, columns))
+    if dbeta is not None:
+        items.append((dbeta, "dbeta", dtype, columns))
+    _call_on(_check_all(items), "lsrm_layer_norm_backward", stream, rows, width, _LN_DTYPES[dtype], _ptr(dy), _ptr(x),
              _ptr(gamma), _ptr(mean), _ptr(rstd), _ptr(dx), _ptr(dgamma), _ptr(dbeta), _ptr(ws), ws.numel())
