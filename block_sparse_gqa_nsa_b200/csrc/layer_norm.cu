@@ -342,7 +342,7 @@ __global__ void __launch_bounds__(kLnThreads) ln_bwd_kernel(const LnBwd p) {
 // at 1024 columns and leave 8 warps an SM: 177 us against the floor of 115 at 121344 rows); the R rows'
 // statistics cross the warps behind one barrier.
 template <typename T, int VEC, int NT, int R>
-__global__ void __launch_bounds__(NT) ln_bwd_cta_kernel(const LnBwd p) {
+__global__ void __launch_bounds__(NT, NT < 512 ? 512 / NT : 1) ln_bwd_cta_kernel(const LnBwd p) {
   constexpr int kWarps = NT / 32;
   static_assert(2 * R <= 32 && (2 * R & (2 * R - 1)) == 0, "the statistics are folded over the lanes");
   __shared__ float red[2][kWarps][2 * R];
@@ -550,17 +550,16 @@ LnShape ln_shape(int C, int elem, bool vec_ok, bool backward) {
 
 lsrm_status ln_launched() { return cudaGetLastError() == cudaSuccess ? LSRM_OK : LSRM_ERR_CUDA; }
 
-// rows a group takes at once: four where a thread holds 16 bytes of a row, as long as that still leaves
-// every SM a few CTAs
-#ifndef LN_RF
-#define LN_RF 4
-#define LN_RB 4
-#define LN_RC 4
-#define LN_RW 1
-#endif
+// Rows a thread group takes at once: two where a thread holds 16 bytes of a row, as long as that still
+// leaves every SM a few CTAs (head rows of 32: one row 24.5 us, two or four 20.6, eight 25.7; four rows of
+// 64 bytes a thread 159 us against 92 with one).
+constexpr int kLnRows = 2;
+// of the backward's CTAs (hidden rows of 1024: two rows 142 us, four 140, eight 183; at least 512 threads
+// an SM: 640 cost spills, 148 -> 164 us)
+constexpr int kLnCtaRows = 4;
 template <typename T, int VEC, int TPR, int NV>
 lsrm_status ln_run_fwd(const LnFwd& p, cudaStream_t s) {
-  constexpr int kGroups = kLnThreads / TPR, R = NV * VEC * (int)sizeof(T) <= 16 ? LN_RF : LN_RW;
+  constexpr int kGroups = kLnThreads / TPR, R = NV * VEC * (int)sizeof(T) <= 16 ? kLnRows : 1;
   if (R > 1 && p.rows >= (long long)kGroups * R * 4 * kLnSms) {
     const long long ctas = (p.rows + kGroups * R - 1) / (kGroups * R);
     if (ctas > (long long)INT32_MAX) return LSRM_ERR_UNSUPPORTED;
@@ -589,12 +588,12 @@ template <typename T, int VEC, int TPR, int NV>
 lsrm_status ln_run_bwd(const LnBwd& p, int max_ctas, int* ctas, cudaStream_t s) {
   lsrm_status st;
   if constexpr (TPR > 32) {
-    constexpr int R = LN_RC;
+    constexpr int R = TPR == 1024 ? 2 : kLnCtaRows;
     auto kernel = ln_bwd_cta_kernel<T, VEC, TPR, R>;
     if ((st = ln_ctas(kernel, TPR, (p.rows + R - 1) / R, max_ctas, ctas)) != LSRM_OK) return st;
     kernel<<<(unsigned)*ctas, TPR, 0, s>>>(p);
   } else {
-    constexpr int kGroups = kLnThreads / TPR, R = VEC > 1 ? LN_RB : 1;
+    constexpr int kGroups = kLnThreads / TPR, R = VEC > 1 ? kLnRows : 1;
     auto kernel = ln_bwd_kernel<T, VEC, TPR, NV, R>;
     if ((st = ln_ctas(kernel, kLnThreads, (p.rows + kGroups * R - 1) / (kGroups * R), max_ctas, ctas)) != LSRM_OK)
       return st;

@@ -530,7 +530,7 @@ __global__ void __launch_bounds__(kFewThreads) rp_few_kernel(const Params p) {
 
 // ---- parts of a split -----------------------------------------------------------------------------
 
-constexpr int kJoinRows = 8, kJoinThreads = 256;
+constexpr int kJoinRows = 1, kJoinThreads = 256;
 
 // out = sum_s l_s exp(m_s - m) o_s / sum_s l_s exp(m_s - m) in the order of the splits (reference and
 // sum apart: their LSE would lose the sum beside a huge reference); D / 4 lanes a (query, head)
@@ -587,11 +587,14 @@ static lsrm_status run_fwd(const Params& p, long long ctas, cudaStream_t s) {
 }
 
 lsrm_status launch_fwd_tc(const Params& p, int D, int NA, long long ctas, cudaStream_t s);
+lsrm_status launch_short(const Params& p, int D, int NA, long long ctas, bool dq, cudaStream_t s);
 
 template <int D, int NA>
 static lsrm_status run_shape(const Params& p, const FwdPlan& f, cudaStream_t s) {
   lsrm_status st;
-  if (f.rows == 0) {
+  if (f.rows < 0) {
+    st = launch_short(p, D, NA, f.ctas, false, s);
+  } else if (f.rows == 0) {
     const size_t bytes = FewCfg<D, NA>::smem(p.maxd, p.NB, p.G < 16 ? p.G : 16);
     if (!allow_smem(rp_few_kernel<D, NA>, bytes)) return LSRM_ERR_CUDA;
     rp_few_kernel<D, NA><<<(unsigned)f.ctas, kFewThreads, bytes, s>>>(p);

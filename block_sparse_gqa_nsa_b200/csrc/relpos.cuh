@@ -354,23 +354,41 @@ __device__ __forceinline__ void split_range(const Params& p, int split, int chun
 
 // ---- launch plans and the workspace (host) ----
 constexpr int kSms = 148;
+constexpr int kShHeads = 16;                 // heads a CTA of the short segments' kernels takes, at most
+constexpr size_t kShTables = 64 * 1024;      // bytes of their bias tables, at most
+inline size_t short_tables(const lsrm_relpos_desc& d) {
+  const size_t g = (size_t)(d.n_q_heads / d.n_kv_heads);
+  return (g < kShHeads ? g : kShHeads) * d.n_axes * (2 * (size_t)d.max_distance + 1) * 4;
+}
+inline long long short_ctas(const lsrm_relpos_desc& d) {
+  const long long g = d.n_q_heads / d.n_kv_heads, gh = g < kShHeads ? g : kShHeads;
+  return (d.n_q_tokens / 64 + d.n_segs) * d.n_kv_heads * ((g + gh - 1) / gh);
+}
 
 struct FwdPlan {
-  int rows;  // queries a CTA: 256 (tensor-memory kernel), 128, 64, or 0 for the kernel of few rows
+  int rows;  // queries a CTA: 256 (tensor-memory kernel), 128, 64, 0 for the kernel of few rows, -1 for short segments
   int splits;
   long long ctas;
 };
 struct BwdPlan {
   bool tc;      // the tensor-memory kernels: 128 rows a CTA
   bool exact;   // short segments: the exact Delta in dq as well
+  bool shrt;    // short segments' dq kernel
   int splits;   // of the key pass over heads and query chunks: a divisor of G, or a multiple of it
   int g;
-  long long dq_tiles, kv_tiles;
+  long long dq_tiles, kv_tiles, short_ctas;
   int parts() const { return splits > g ? splits / g : 1; }  // table sums per (key tile, head)
 };
 constexpr int kExactKeys = 256;
 
 size_t bwd_tc_smem(int D, int NA, int maxd, int nb);  // of rp_dkv_tc_kernel
+
+// Short segments' kernels: while a segment is a tile of queries or so, enough of them fill the GPU, and
+// the tables of a group's heads fit
+inline bool short_kernels(const lsrm_relpos_desc& d) {
+  const long long S = d.n_segs, mean_q = (d.n_q_tokens + S - 1) / S, mean_k = (d.n_k_tokens + S - 1) / S;
+  return mean_q <= 64 && mean_k <= 64 && short_tables(d) <= kShTables && S * d.n_kv_heads >= kSms / 2;
+}
 
 inline FwdPlan fwd_plan(const lsrm_relpos_desc& d) {
   FwdPlan f{};
@@ -383,13 +401,25 @@ inline FwdPlan fwd_plan(const lsrm_relpos_desc& d) {
     f.ctas = (Nq / t + S) * d.n_kv_heads * hgroups;
     busy = ((mean_q + t - 1) / t) * (Nq < S ? Nq : S) * d.n_kv_heads * hgroups;
     chunks = (mean_k + 127) / 128;  // four warps of 32 keys
+  } else if (short_kernels(d)) {
+    f.rows = -1;
+    f.splits = 1;
+    f.ctas = short_ctas(d);
+    return f;
   } else {
     f.rows = mean_q <= 64 ? 64 : mean_q <= 96 ? 128 : 256;
     f.ctas = (Nq / f.rows + S) * d.n_q_heads;
     busy = ((mean_q + f.rows - 1) / f.rows) * S * d.n_q_heads;
     chunks = (mean_k + 63) / 64;
   }
-  const long long want = (f.rows == 256 ? 2 : 3) * kSms, most = chunks / 4;
+#ifndef W_FEW
+#define W_FEW 4
+#define W_TC 2
+#define W_BM 8
+#define W_BT 4
+#define W_MOST 2
+#endif
+  const long long want = (f.rows == 256 ? W_TC : f.rows == 0 ? W_FEW : 3) * kSms, most = f.rows == 0 ? chunks / W_MOST : chunks / 4;
   long long sp = busy > 0 && busy < want ? want / busy : 1;
   if (sp > most) sp = most;
   if (sp > 64) sp = 64;
@@ -408,11 +438,13 @@ inline BwdPlan bwd_plan(const lsrm_relpos_desc& d) {
   b.tc = !b.exact && mean_q > 128 &&
          bwd_tc_smem(d.head_dim, d.n_axes, d.max_distance, d.n_buckets) <= 227 * 1024;
   const int rows = b.tc ? 128 : 64;
+  b.shrt = short_kernels(d);
+  b.short_ctas = short_ctas(d);
   b.dq_tiles = d.n_q_tokens / rows + S;
   b.kv_tiles = d.n_k_tokens / rows + S;
   const long long busy = ((mean_k + rows - 1) / rows) * S * d.n_kv_heads;
   const long long qchunks = (mean_q + 63) / 64;
-  const long long want = (b.tc ? 2 : 3) * kSms;
+  const long long want = (b.tc ? W_BT : W_BM) * kSms;
   long long sp = busy > 0 ? (want + busy - 1) / busy : 1;
   if (sp > 64 * G) sp = 64 * G;
   if (sp < G) {

@@ -37,7 +37,7 @@ lsrm_status check_relpos(const lsrm_relpos_desc* d) {
   const rp::FwdPlan f = rp::fwd_plan(*d);
   const rp::BwdPlan b = rp::bwd_plan(*d);
   const long long most = INT32_MAX;
-  if (f.ctas > most || b.dq_tiles * d->n_q_heads > most || b.kv_tiles * d->n_kv_heads * b.splits > most ||
+  if (f.ctas > most || b.short_ctas > most || b.dq_tiles * d->n_q_heads > most || b.kv_tiles * d->n_kv_heads * b.splits > most ||
       d->n_q_tokens + d->n_segs > most || d->n_k_tokens + d->n_segs > most || d->n_q_heads > 65535)
     return LSRM_ERR_UNSUPPORTED;
   return LSRM_OK;

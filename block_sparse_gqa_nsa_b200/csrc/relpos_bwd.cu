@@ -721,6 +721,7 @@ static lsrm_status run_dkv(const Params& p, const BwdPlan& b, cudaStream_t s) {
 }
 
 lsrm_status launch_bwd_tc(const Params& p, int D, int NA, const BwdPlan& b, cudaStream_t s);
+lsrm_status launch_short(const Params& p, int D, int NA, long long ctas, bool dq, cudaStream_t s);
 
 template <int D, int NA>
 static lsrm_status run_bwd(const Params& p, const BwdPlan& b, cudaStream_t s) {
@@ -729,7 +730,8 @@ static lsrm_status run_bwd(const Params& p, const BwdPlan& b, cudaStream_t s) {
     if ((st = launch_bwd_tc(p, D, NA, b, s)) != LSRM_OK) return st;
   }
   if (!b.tc && p.Nq > 0) {
-    st = b.exact ? run_dq<D, NA, true>(p, b, s) : run_dq<D, NA, false>(p, b, s);
+    st = b.shrt ? launch_short(p, D, NA, b.short_ctas, true, s)
+         : b.exact ? run_dq<D, NA, true>(p, b, s) : run_dq<D, NA, false>(p, b, s);
     if (st != LSRM_OK) return st;
   }
   if (p.Nk > 0) {

@@ -108,6 +108,16 @@ FORWARD = {
     "no_keys_at_all": dict(lens_q=[40, 40], lens_k=[0, 0]),
     "no_queries_at_all": dict(lens_q=[0, 0], lens_k=[40, 40]),
     "outside": dict(lens_q=[70, 5], lead=9),
+    # many short segments: several heads a CTA
+    "short_ragged": dict(lens_q=[i * 7 % 65 for i in range(60)], heads=8, kv_heads=2, axes=3, places="scattered", maxd=9),
+    "short_gqa16": dict(lens_q=[64, 1, 17, 0, 33] * 8, heads=32, kv_heads=2, buckets=16, maxd=20),
+    "short_d64": dict(lens_q=[i * 5 % 61 for i in range(50)], heads=6, kv_heads=2, dim=64, axes=2, places="scattered"),
+    "short_mha": dict(lens_q=[40, 16, 15, 3] * 20, heads=1, kv_heads=1),
+    "short_wide_group": dict(lens_q=[30, 64, 5] * 15, heads=40, kv_heads=2, maxd=31, places="frames"),
+    "short_with_long": dict(lens_q=[20, 0, 150, 9, 64] * 10, lens_k=[64, 7, 0, 200, 1] * 10, heads=8, kv_heads=2,
+                            places="scattered"),
+    "short_outside": dict(lens_q=[33, 12, 60] * 14, lead=5, heads=4, kv_heads=2, axes=3, places="scattered", maxd=7,
+                          buckets=7),
     # long segments: 128-row tiles in the backward
     "long32": dict(lens_q=[300]),
     "long64": dict(lens_q=[300, 555], dim=64),
@@ -167,7 +177,7 @@ def test_rows_outside_segments_stay():
 
 
 # a neighbour segment's infinities and NaNs do not reach a row, whatever the tile
-@pytest.mark.parametrize("lens", [[40, 23, 61], [1, 1, 1], [130, 5, 200], [300, 310, 333]])
+@pytest.mark.parametrize("lens", [[40, 23, 61], [1, 1, 1], [130, 5, 200], [300, 310, 333], [40, 23, 61] * 14])
 def test_neighbours_do_not_leak(lens):
     c = Case(lens, dim=64)
     clean = {n: x.clone() for n, x in c.check()[0].items()}
@@ -181,7 +191,7 @@ def test_neighbours_do_not_leak(lens):
             assert torch.equal(got[n][part], clean[n][part]), n
 
 
-@pytest.mark.parametrize("lens_q,lens_k", [([130], None), ([3], [200]), ([290, 300], None)])
+@pytest.mark.parametrize("lens_q,lens_k", [([130], None), ([3], [200]), ([290, 300], None), ([40, 23] * 20, None)])
 @pytest.mark.parametrize("low", [-math.inf, torch.finfo(BF).min, -1e30])
 def test_masks_by_the_table(lens_q, lens_k, low):
     """Entries at -inf or at the type's lowest value mask a bucket; a row whose every key is at -inf
