@@ -321,20 +321,16 @@ __global__ void __launch_bounds__(kTcThreads, 2)
         tmem_wait16(s);
         tmem_wait16(d);
         float x[16];
-        if (small && cb.flat(2 * half + g)) {
-          const float b = cb.row16(cb.ub - rconst, S.pos[st], 2 * half + g, rowc, S.lut, top);
+        // small tables: in log2 units, the row's constant with the bias; others: the subtraction last
+        const float b = cb.row16(small ? cb.ub - rconst : cb.ub, S.pos[st], 2 * half + g, rowc, S.lut, top);
 #pragma unroll
-          for (int e = 0; e < 16; e += 2)
-            ffma2(x[e], x[e + 1], __uint_as_float(s[e]), __uint_as_float(s[e + 1]), mul, b);
-        } else {
-          cb.all16(x, cb.ub, S.pos[st], 2 * half + g, rowc, S.lut, top);
+        for (int e = 0; e < 16; e += 2)
+          ffma2(x[e], x[e + 1], __uint_as_float(s[e]), __uint_as_float(s[e + 1]), mul, b);
+        if (!cb.flat(2 * half + g)) cb.add16(x, S.pos[st], 2 * half + g, rowc, S.lut, top);
+        if (!small) {
+          keep_branch();
 #pragma unroll
-          for (int e = 0; e < 16; ++e) x[e] = fmaf(__uint_as_float(s[e]), mul, x[e]) - rconst;
-          if (!small) {
-            keep_branch();
-#pragma unroll
-            for (int e = 0; e < 16; ++e) x[e] = fmaf(x[e], kLog2e, -corr);
-          }
+          for (int e = 0; e < 16; ++e) x[e] = fmaf(x[e] - rconst, kLog2e, -corr);
         }
         float s0 = 0.0f, s1 = 0.0f;
 #pragma unroll
@@ -680,8 +676,8 @@ __global__ void __launch_bounds__(kTcThreads, 2)
         const float4* ls = reinterpret_cast<const float4*>(&S.nlse[st][col]);
         const float4* ds = reinterpret_cast<const float4*>(&S.ndelta[st][col]);
         float x[16];
-        if (small && cb.flat(2 * half + g)) {
-          const float b = cb.row16(cb.ub, S.pos[st], 2 * half + g, rowc, lut, top);
+        const float b = cb.row16(cb.ub, S.pos[st], 2 * half + g, rowc, lut, top);
+        if (small) {
 #pragma unroll
           for (int f = 0; f < 4; ++f) {
             float4 l = ls[f];
@@ -691,28 +687,20 @@ __global__ void __launch_bounds__(kTcThreads, 2)
             ffma2v(x[4 * f + 2], x[4 * f + 3], __uint_as_float(s[4 * f + 2]), __uint_as_float(s[4 * f + 3]), mul, l.z,
                    l.w);
           }
+          if (!cb.flat(2 * half + g)) cb.add16(x, S.pos[st], 2 * half + g, rowc, lut, top);
         } else {
-          cb.all16(x, cb.ub, S.pos[st], 2 * half + g, rowc, lut, top);
+          // natural units, the subtraction last: exact for scores of any size
+          keep_branch();
 #pragma unroll
-          for (int e = 0; e < 16; ++e) x[e] = fmaf(__uint_as_float(s[e]), mul, x[e]);
-          if (small) {
+          for (int e = 0; e < 16; ++e) x[e] = fmaf(__uint_as_float(s[e]), mul, b);
+          cb.add16(x, S.pos[st], 2 * half + g, rowc, lut, top);
+          const int q = qlo + (c0 + cc) * kTcCols + col;
 #pragma unroll
-            for (int f = 0; f < 4; ++f) {
-              const float4 l = ls[f];
-              fadd2_acc(x[4 * f], x[4 * f + 1], l.x, l.y);
-              fadd2_acc(x[4 * f + 2], x[4 * f + 3], l.z, l.w);
-            }
-          } else {
-            // natural units, the subtraction first: exact for scores of any size
-            keep_branch();
-            const int q = qlo + (c0 + cc) * kTcCols + col;
-#pragma unroll
-            for (int e = 0; e < 16; ++e) {
-              const size_t at = (size_t)min(q + e, qhi - 1) * p.Hq + hk * p.G + head;
-              float l = q + e < qhi ? p.lse_in[at] : INFINITY;
-              if (l == -INFINITY) l = INFINITY;
-              x[e] = fmaf(x[e] - l, kLog2e, -p.corr[at]);
-            }
+          for (int e = 0; e < 16; ++e) {
+            const size_t at = (size_t)min(q + e, qhi - 1) * p.Hq + hk * p.G + head;
+            float l = q + e < qhi ? p.lse_in[at] : INFINITY;
+            if (l == -INFINITY) l = INFINITY;
+            x[e] = fmaf(x[e] - l, kLog2e, -p.corr[at]);
           }
         }
         uint32_t pp[8], pd[8];

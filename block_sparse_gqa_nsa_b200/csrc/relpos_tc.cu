@@ -259,12 +259,15 @@ __global__ void __launch_bounds__(kTcThreads, 2)
       for (int g = 0; g < 4; ++g) {
         uint32_t r[16];
         float b[16];
-        cb.all16(b, cb.ub, S.pos[st], g, rowc, S.lut, top);
+        const float row_b = cb.row16(cb.ub, S.pos[st], g, rowc, S.lut, top);
         tmem_ld16(tbase + C::kColS + 16 * g, r);
         tmem_wait16(r);
 #pragma unroll
+        for (int e = 0; e < 16; ++e) b[e] = fmaf(__uint_as_float(r[e]), mul, row_b);
+        cb.add16(b, S.pos[st], g, rowc, S.lut, top);
+#pragma unroll
         for (int e = 0; e < 16; ++e)
-          if (16 * g + e < left) mx = fmaxf(mx, fmaf(__uint_as_float(r[e]), mul, b[e]));
+          if (16 * g + e < left) mx = fmaxf(mx, b[e]);
       }
       if (!fold) off = valid && (c == 0 || mx > m);
       const float f = !off ? 1.0f : m == -INFINITY ? 0.0f : ex2((m - mx) * to_log2);
@@ -286,12 +289,15 @@ __global__ void __launch_bounds__(kTcThreads, 2)
       for (int g = 0; g < 4; ++g) {
         uint32_t r[16], pk[8];
         float b[16];
-        cb.all16(b, cb.ub, S.pos[st], g, rowc, S.lut, top);
+        const float row_b = cb.row16(cb.ub, S.pos[st], g, rowc, S.lut, top);
         tmem_ld16(tbase + C::kColS + 16 * g, r);
         tmem_wait16(r);
 #pragma unroll
+        for (int e = 0; e < 16; ++e) b[e] = fmaf(__uint_as_float(r[e]), mul, row_b);
+        cb.add16(b, S.pos[st], g, rowc, S.lut, top);
+#pragma unroll
         for (int e = 0; e < 16; ++e) {
-          const float x = ex2((fmaf(__uint_as_float(r[e]), mul, b[e]) - ref) * to_log2);
+          const float x = ex2((b[e] - ref) * to_log2);
           b[e] = 16 * g + e < left ? x : 0.0f;
           sum += b[e];
         }
@@ -326,16 +332,11 @@ __global__ void __launch_bounds__(kTcThreads, 2)
 #pragma unroll
           for (int g = 0; g < 2; ++g) {
             float b[16];
-            if (!cb.flat(2 * hf + g)) {
-              cb.all16(b, base, S.pos[st], 2 * hf + g, rowc, S.lut, top);
+            const float one = cb.row16(base, S.pos[st], 2 * hf + g, rowc, S.lut, top);
 #pragma unroll
-              for (int e = 0; e < 16; ++e) b[e] = fmaf(__uint_as_float(r[16 * g + e]), mul, b[e]);
-            } else {
-              const float one = cb.row16(base, S.pos[st], 2 * hf + g, rowc, S.lut, top);
-#pragma unroll
-              for (int e = 0; e < 16; e += 2)
-                ffma2(b[e], b[e + 1], __uint_as_float(r[16 * g + e]), __uint_as_float(r[16 * g + e + 1]), mul, one);
-            }
+            for (int e = 0; e < 16; e += 2)
+              ffma2(b[e], b[e + 1], __uint_as_float(r[16 * g + e]), __uint_as_float(r[16 * g + e + 1]), mul, one);
+            if (!cb.flat(2 * hf + g)) cb.add16(b, S.pos[st], 2 * hf + g, rowc, S.lut, top);
             if (left < 32 * hf + 16 * g + 16) {
               keep_branch();
 #pragma unroll

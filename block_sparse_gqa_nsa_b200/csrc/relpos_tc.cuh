@@ -158,12 +158,9 @@ struct ChunkBias {
       if (mode(a, g) == kLane) base += lut[a * (top + 1) + clamp_index(SIGN * pos[a][16 * g], rowc[a], top)];
     return base;
   }
-  // the biases of run g on top of base
-  __device__ __forceinline__ void all16(float (&b)[16], float base, int (*pos)[kTcCols], int g, const int (&rowc)[NA],
+  // the rest of run g's biases (what row16 leaves out) added to its 16 scores
+  __device__ __forceinline__ void add16(float (&x)[16], int (*pos)[kTcCols], int g, const int (&rowc)[NA],
                                         const float* lut, int top) const {
-    base = row16(base, pos, g, rowc, lut, top);
-#pragma unroll
-    for (int e = 0; e < 16; ++e) b[e] = base;
 #pragma unroll
     for (int a = 0; a < NA; ++a) {
       const float* la = lut + a * (top + 1);
@@ -173,17 +170,18 @@ struct ChunkBias {
 #pragma unroll
         for (int f = 0; f < 4; ++f) {
           const float y = la[clamp_index(SIGN * xs[f].x, rowc[a], top)];
-          b[4 * f] += y, b[4 * f + 1] += y, b[4 * f + 2] += y, b[4 * f + 3] += y;
+          fadd2_acc(x[4 * f], x[4 * f + 1], y, y);
+          fadd2_acc(x[4 * f + 2], x[4 * f + 3], y, y);
         }
       } else if (m == kEach) {
 #pragma unroll
         for (int f = 0; f < 4; ++f) {
-          const int4 x = xs[f];
+          const int4 u = xs[f];
           // single adds: a pair of look-ups would first have to be moved into a pair of registers
-          b[4 * f] += la[clamp_index(SIGN * x.x, rowc[a], top)];
-          b[4 * f + 1] += la[clamp_index(SIGN * x.y, rowc[a], top)];
-          b[4 * f + 2] += la[clamp_index(SIGN * x.z, rowc[a], top)];
-          b[4 * f + 3] += la[clamp_index(SIGN * x.w, rowc[a], top)];
+          x[4 * f] += la[clamp_index(SIGN * u.x, rowc[a], top)];
+          x[4 * f + 1] += la[clamp_index(SIGN * u.y, rowc[a], top)];
+          x[4 * f + 2] += la[clamp_index(SIGN * u.z, rowc[a], top)];
+          x[4 * f + 3] += la[clamp_index(SIGN * u.w, rowc[a], top)];
         }
       }
     }
