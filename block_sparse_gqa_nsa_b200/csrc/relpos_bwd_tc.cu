@@ -301,7 +301,7 @@ __global__ void __launch_bounds__(kTcThreads, 2)
     __syncwarp();
     const float l2 = fmaf(lse, kLog2e, corr), rconst = small ? l2 : lse;
 
-    ChunkBias<NA, 1, true> cb;
+    ChunkBias<NA, true> cb;
     for (int c = 0; ok && c < chunks; ++c) {
       const int st = c % C::kStages, left = khi - klo - c * kTcCols;
       if (!wait_bar_w(&S.kv_full[st], (c / C::kStages) & 1, abort, p.status) ||
@@ -435,13 +435,13 @@ struct DkvTcSmem {
 // two sums into the thread's own column with both reads ahead of both writes (as in relpos_bwd.cu)
 __device__ __forceinline__ void add_two_tc(char* col, int b0, float v0, int b1, float v1) {
   float *p0 = reinterpret_cast<float*>(col + b0), *p1 = reinterpret_cast<float*>(col + b1);
-  const float x0 = *p0, x1 = *p1;
-  *p1 = x1 + v1;
-  *p0 = x0 + v0 + (b0 == b1 ? v1 : 0.0f);
+  const float s0 = *p0 + v0, x1 = *p1;
+  *p0 = s0;
+  *p1 = (b0 == b1 ? s0 : x1) + v1;
 }
 
 template <int D, int NA>
-__global__ void __launch_bounds__(kTcThreads, 2)
+__global__ void __launch_bounds__(kTcThreads, D == 64 && NA > 1 ? 1 : 2)
     rp_dkv_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
                      const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap omap,
                      const Params p) {
@@ -523,7 +523,7 @@ __global__ void __launch_bounds__(kTcThreads, 2)
       for (int i = 0; i < 2; ++i) {
         const size_t q = q0 + min(lane + 32 * i, n - 1);  // past the end the last query's
 #pragma unroll
-        for (int a = 0; a < NA; ++a) x[a][i] = p.pos_q[q * NA + a];
+        for (int a = 0; a < NA; ++a) x[a][i] = -p.pos_q[q * NA + a];  // negated, as the keys' below
         l[i] = lane + 32 * i < n ? p.lse2[q * p.Hq + h] : INFINITY;  // no query: P = 0
         dl[i] = p.delta[q * p.Hq + h];
       }
@@ -629,8 +629,9 @@ __global__ void __launch_bounds__(kTcThreads, 2)
     int rowc[NA], k_lo[NA], k_hi[NA];
 #pragma unroll
     for (int a = 0; a < NA; ++a) {
-      const int x = p.pos_k[(size_t)min(row, khi - 1) * NA + a];
-      rowc[a] = p.maxd + x;
+      // delta = (- pos_q) - (- pos_k): with both negated, columns less rows as in the other kernels
+      const int x = -p.pos_k[(size_t)min(row, khi - 1) * NA + a];
+      rowc[a] = p.maxd - x;
       k_lo[a] = __reduce_min_sync(0xffffffffu, x);
       k_hi[a] = __reduce_max_sync(0xffffffffu, x);
     }
@@ -650,7 +651,7 @@ __global__ void __launch_bounds__(kTcThreads, 2)
     EwBarrier eb{&S.ew, abort, p.status, 0};
     bool ok = true, small = false;
     float mul = 0.0f;
-    ChunkBias<NA, -1, true> cb;
+    ChunkBias<NA, true> cb;
     for (int it = 0; ok && it < steps; ++it) {
       const int st = it % C::kStages, cc = it % nc, head = h0 + it / nc;
       if (cc == 0) {
@@ -736,7 +737,7 @@ __global__ void __launch_bounds__(kTcThreads, 2)
             float s0 = 0.0f, s1 = 0.0f;
 #pragma unroll
             for (int e = 0; e < 16; e += 2) fadd2_acc(s0, s1, x[e], x[e + 1]);
-            const int b = boff[md == kOne ? cb.one[a] : clamp_index(-xs[0].x, rowc[a], top)];
+            const int b = boff[md == kOne ? cb.one[a] : clamp_index(xs[0].x, rowc[a], top)];
             if (b != run_b[a]) {
               *reinterpret_cast<float*>(to + run_b[a]) += run[a];
               run[a] = 0.0f;
@@ -746,18 +747,18 @@ __global__ void __launch_bounds__(kTcThreads, 2)
           } else if (md == kFour) {
 #pragma unroll
             for (int f = 0; f < 4; f += 2)
-              add_two_tc(to, boff[clamp_index(-xs[f].x, rowc[a], top)],
+              add_two_tc(to, boff[clamp_index(xs[f].x, rowc[a], top)],
                          (x[4 * f] + x[4 * f + 1]) + (x[4 * f + 2] + x[4 * f + 3]),
-                         boff[clamp_index(-xs[f + 1].x, rowc[a], top)],
+                         boff[clamp_index(xs[f + 1].x, rowc[a], top)],
                          (x[4 * f + 4] + x[4 * f + 5]) + (x[4 * f + 6] + x[4 * f + 7]));
           } else {
 #pragma unroll
             for (int f = 0; f < 4; ++f) {
               const int4 u = xs[f];
-              add_two_tc(to, boff[clamp_index(-u.x, rowc[a], top)], x[4 * f], boff[clamp_index(-u.y, rowc[a], top)],
+              add_two_tc(to, boff[clamp_index(u.x, rowc[a], top)], x[4 * f], boff[clamp_index(u.y, rowc[a], top)],
                          x[4 * f + 1]);
-              add_two_tc(to, boff[clamp_index(-u.z, rowc[a], top)], x[4 * f + 2],
-                         boff[clamp_index(-u.w, rowc[a], top)], x[4 * f + 3]);
+              add_two_tc(to, boff[clamp_index(u.z, rowc[a], top)], x[4 * f + 2],
+                         boff[clamp_index(u.w, rowc[a], top)], x[4 * f + 3]);
             }
           }
         }

@@ -116,11 +116,12 @@ __device__ __forceinline__ void note_positions(const int (&x)[NA][2], int (*pos)
 }
 
 // A chunk's biases for a warp's rows.  Per axis and run of 16 columns: kOne (the chunk has one clamped
-// distance), kLane (one position in the run), kFour (one per four columns), kEach.  SIGN as for add_bias.
+// distance), kLane (one position in the run), kFour (one per four columns), kEach.  Positions count so that
+// columns less rows is the distance (the key pass, whose columns are queries, negates both).
 // RUNS: told run by run, which suits rows of patches whose ends fall anywhere (six frames' training step
 // 1401 -> 1329 us); else for the chunk as a whole, which costs less per run (forward over bricks of
 // three axes 612 -> 531 us).
-template <int NA, int SIGN, bool RUNS>
+template <int NA, bool RUNS>
 struct ChunkBias {
   int one[NA];  // the chunk's only index into the table, or -1
   int whole[NA];
@@ -131,8 +132,8 @@ struct ChunkBias {
     ub = 0.0f;
 #pragma unroll
     for (int a = 0; a < NA; ++a) {
-      const int lo = clamp_index(SIGN > 0 ? m.lo[a] - row_hi[a] : row_lo[a] - m.hi[a], maxd, top);
-      const int hi = clamp_index(SIGN > 0 ? m.hi[a] - row_lo[a] : row_hi[a] - m.lo[a], maxd, top);
+      const int lo = clamp_index(m.lo[a] - row_hi[a], maxd, top);
+      const int hi = clamp_index(m.hi[a] - row_lo[a], maxd, top);
       one[a] = lo == hi ? lo : -1;
       same16[a] = m.same16[a], same4[a] = m.same4[a];
       whole[a] = lo == hi ? kOne : same16[a] == 15u ? kLane : same4[a] == 15u ? kFour : kEach;
@@ -155,7 +156,7 @@ struct ChunkBias {
                                          const float* lut, int top) const {
 #pragma unroll
     for (int a = 0; a < NA; ++a)
-      if (mode(a, g) == kLane) base += lut[a * (top + 1) + clamp_index(SIGN * pos[a][16 * g], rowc[a], top)];
+      if (mode(a, g) == kLane) base += lut[a * (top + 1) + clamp_index(pos[a][16 * g], rowc[a], top)];
     return base;
   }
   // the rest of run g's biases (what row16 leaves out) added to its 16 scores
@@ -169,7 +170,7 @@ struct ChunkBias {
       if (m == kFour) {
 #pragma unroll
         for (int f = 0; f < 4; ++f) {
-          const float y = la[clamp_index(SIGN * xs[f].x, rowc[a], top)];
+          const float y = la[clamp_index(xs[f].x, rowc[a], top)];
           fadd2_acc(x[4 * f], x[4 * f + 1], y, y);
           fadd2_acc(x[4 * f + 2], x[4 * f + 3], y, y);
         }
@@ -178,10 +179,10 @@ struct ChunkBias {
         for (int f = 0; f < 4; ++f) {
           const int4 u = xs[f];
           // single adds: a pair of look-ups would first have to be moved into a pair of registers
-          x[4 * f] += la[clamp_index(SIGN * u.x, rowc[a], top)];
-          x[4 * f + 1] += la[clamp_index(SIGN * u.y, rowc[a], top)];
-          x[4 * f + 2] += la[clamp_index(SIGN * u.z, rowc[a], top)];
-          x[4 * f + 3] += la[clamp_index(SIGN * u.w, rowc[a], top)];
+          x[4 * f] += la[clamp_index(u.x, rowc[a], top)];
+          x[4 * f + 1] += la[clamp_index(u.y, rowc[a], top)];
+          x[4 * f + 2] += la[clamp_index(u.z, rowc[a], top)];
+          x[4 * f + 3] += la[clamp_index(u.w, rowc[a], top)];
         }
       }
     }
