@@ -28,17 +28,13 @@ constexpr int kChunk = 64;  // keys a stage
 constexpr int kStages = 3;
 constexpr float kSlack = 8.0f;
 
-#ifndef RP_NT32
-#define RP_NT32 4
-#define RP_NT64 4
-#define RP_MB32 3
-#define RP_MB64 2
-#endif
 template <int D, int NA, int NW>
 struct FwdCfg {
-  static constexpr int NT = D == 32 ? RP_NT32 : RP_NT64;  // column groups a score tile
-  static constexpr int CW = 2 * NT, kCols = 8 * NT;
-  static constexpr int kMinCtas = (D == 32 ? RP_MB32 : RP_MB64) * 4 / NW;
+  // Column groups a score tile, and CTAs of 128 threads an SM.  16 and 64 segments of 24 to 64 queries against
+  // 512 keys, 32 heads of 32: 41-43 us and 112-121; four CTAs (fewer registers) 50-57; tiles of 8 groups
+  // and two CTAs 33-60 and 118-123.
+  static constexpr int NT = 4, CW = 2 * NT, kCols = 8 * NT;
+  static constexpr int kMinCtas = (D == 32 ? 3 : 2) * 4 / NW;
   static constexpr int kRows = 32 * NW, kThreads = 32 * NW;
   static constexpr int kTile = kChunk * D / 8;  // 16-byte pieces of a K or V stage
   static constexpr size_t kFixed = (size_t)kStages * (2 * kTile * 16 + kChunk * NA * 4);
@@ -603,8 +599,10 @@ static lsrm_status run_shape(const Params& p, const FwdPlan& f, cudaStream_t s) 
     st = launch_fwd_tc(p, D, NA, f.ctas, s);
   } else if (f.rows == 64) {
     st = run_fwd<D, NA, 2>(p, f.ctas, s);
-  } else {
+  } else if constexpr (D == 32) {  // (fwd_plan: 128 rows at head dim 32 only)
     st = run_fwd<D, NA, 4>(p, f.ctas, s);
+  } else {
+    return LSRM_ERR_UNSUPPORTED;
   }
   if (st != LSRM_OK || f.splits == 1) return st;
   rp_join_kernel<D><<<(unsigned)(p.Nq / kJoinRows + p.S), kJoinThreads, 0, s>>>(p);

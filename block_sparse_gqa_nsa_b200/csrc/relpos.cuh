@@ -371,7 +371,7 @@ struct FwdPlan {
   long long ctas;
 };
 struct BwdPlan {
-  bool tc;      // the tensor-memory kernels: 128 rows a CTA
+  int tc;       // the tensor-memory kernels of 128 rows a CTA: CTAs of the key pass an SM holds, or 0
   bool exact;   // short segments: the exact Delta in dq as well
   bool shrt;    // short segments' dq kernel
   int splits;   // of the key pass over heads and query chunks: a divisor of G, or a multiple of it
@@ -381,13 +381,18 @@ struct BwdPlan {
 };
 constexpr int kExactKeys = 256;
 
-size_t bwd_tc_smem(int D, int NA, int maxd, int nb);  // of rp_dkv_tc_kernel
+int bwd_tc_ctas(int D, int NA, int maxd, int nb);  // CTAs of rp_dkv_tc_kernel an SM holds, 0: too large
+
+// The kernel of few rows: 24 rows of 32 heads of 32 against 16 x 512 keys 29 us, 64-row tiles 41; 48 rows
+// 52 us against 43
+constexpr int kFewRows = 24;
 
 // Short segments' kernels: while a segment is a tile of queries or so, enough of them fill the GPU, and
-// the tables of a group's heads fit
+// the tables of a group's heads fit.  Segments of 64 tokens, 32 heads of 32 on 2 KV heads, forward and backward:
+// 64 of them 50 and 213 us, by the kernels of longer segments 35 and 179; 128 of them 53 and 292 against 64 and 306.
 inline bool short_kernels(const lsrm_relpos_desc& d) {
   const long long S = d.n_segs, mean_q = (d.n_q_tokens + S - 1) / S, mean_k = (d.n_k_tokens + S - 1) / S;
-  return mean_q <= 64 && mean_k <= 64 && short_tables(d) <= kShTables && S * d.n_kv_heads >= kSms / 2;
+  return mean_q <= 64 && mean_k <= 64 && short_tables(d) <= kShTables && 3 * S * d.n_kv_heads >= 4 * kSms;
 }
 
 inline FwdPlan fwd_plan(const lsrm_relpos_desc& d) {
@@ -395,31 +400,29 @@ inline FwdPlan fwd_plan(const lsrm_relpos_desc& d) {
   const long long S = d.n_segs, Nq = d.n_q_tokens, G = d.n_q_heads / d.n_kv_heads;
   const long long mean_q = (Nq + S - 1) / S, mean_k = (d.n_k_tokens + S - 1) / S;
   long long busy, chunks;  // CTAs with work, about; key chunks of an average segment
-  if (mean_q <= 16) {
+  long long want, most;    // CTAs that splits of the keys shall make, and splits at most
+  if (mean_q <= kFewRows) {
     const long long gh = G < 16 ? G : 16, t = 16 / gh, hgroups = (G + gh - 1) / gh;
     f.rows = 0;
     f.ctas = (Nq / t + S) * d.n_kv_heads * hgroups;
     busy = ((mean_q + t - 1) / t) * (Nq < S ? Nq : S) * d.n_kv_heads * hgroups;
     chunks = (mean_k + 127) / 128;  // four warps of 32 keys
+    // four CTAs an SM, no part below 512 keys: one token of 32 heads against 64 ragged pasts 28.9 us (two CTAs
+    // 37.0), against 8 x 8192 keys 22.7 us (no part below 256 keys 31.3)
+    want = 4 * kSms, most = chunks / 4;
   } else if (short_kernels(d)) {
     f.rows = -1;
     f.splits = 1;
     f.ctas = short_ctas(d);
     return f;
   } else {
-    f.rows = mean_q <= 64 ? 64 : mean_q <= 96 ? 128 : 256;
+    f.rows = mean_q <= 64 ? 64 : mean_q <= 96 && d.head_dim == 32 ? 128 : 256;
     f.ctas = (Nq / f.rows + S) * d.n_q_heads;
     busy = ((mean_q + f.rows - 1) / f.rows) * S * d.n_q_heads;
     chunks = (mean_k + 63) / 64;
+    // the CTAs that an SM holds of the 256-row kernel (one token count, 1024: 34 us; twice as many 38)
+    want = (f.rows == 256 ? 2 : 3) * kSms, most = chunks / 4;
   }
-#ifndef W_FEW
-#define W_FEW 4
-#define W_TC 2
-#define W_BM 8
-#define W_BT 4
-#define W_MOST 2
-#endif
-  const long long want = (f.rows == 256 ? W_TC : f.rows == 0 ? W_FEW : 3) * kSms, most = f.rows == 0 ? chunks / W_MOST : chunks / 4;
   long long sp = busy > 0 && busy < want ? want / busy : 1;
   if (sp > most) sp = most;
   if (sp > 64) sp = 64;
@@ -429,14 +432,14 @@ inline FwdPlan fwd_plan(const lsrm_relpos_desc& d) {
   return f;
 }
 
+// The key pass' splits: whole heads of a group (divisors of G) or parts of one head's query chunks.
 inline BwdPlan bwd_plan(const lsrm_relpos_desc& d) {
   BwdPlan b{};
   const long long S = d.n_segs, G = d.n_q_heads / d.n_kv_heads;
   const long long mean_q = (d.n_q_tokens + S - 1) / S, mean_k = (d.n_k_tokens + S - 1) / S;
   b.g = (int)G;
   b.exact = mean_k <= kExactKeys || mean_q <= 64;
-  b.tc = !b.exact && mean_q > 128 &&
-         bwd_tc_smem(d.head_dim, d.n_axes, d.max_distance, d.n_buckets) <= 227 * 1024;
+  b.tc = !b.exact && mean_q > 128 ? bwd_tc_ctas(d.head_dim, d.n_axes, d.max_distance, d.n_buckets) : 0;
   const int rows = b.tc ? 128 : 64;
   b.shrt = short_kernels(d);
   b.short_ctas = short_ctas(d);
@@ -444,15 +447,31 @@ inline BwdPlan bwd_plan(const lsrm_relpos_desc& d) {
   b.kv_tiles = d.n_k_tokens / rows + S;
   const long long busy = ((mean_k + rows - 1) / rows) * S * d.n_kv_heads;
   const long long qchunks = (mean_q + 63) / 64;
-  const long long want = (b.tc ? W_BT : W_BM) * kSms;
-  long long sp = busy > 0 ? (want + busy - 1) / busy : 1;
-  if (sp > 64 * G) sp = 64 * G;
-  if (sp < G) {
-    while (G % sp) ++sp;  // whole heads, evenly
+  long long sp = 1;
+  if (b.tc) {
+    // The time in chunks of work: CTAs that an SM runs one after the other (whole ones while there are few,
+    // later they even out) times a CTA's chunks and 2.5 for its beginning and end.  More splits only where they
+    // win 2%, as their sums have to be joined.  1024 tokens, 32 heads of 32: 16 splits 178 us, 32 splits 192; 4096
+    // tokens: 16 splits 2247 us, 8 splits 2312; 8 x 320 tokens: 16 splits 205 us, 4 splits 231.
+    double best = 0.0;
+    for (long long c = 1; c <= 64 * G && c <= G * (qchunks > 1 ? qchunks : 1); c = c < G ? c + 1 : c + G) {
+      if (c < G && G % c) continue;
+      const double waves = (double)(busy * c) / (b.tc * kSms);
+      const double steps = c <= G ? (double)(G / c * qchunks) : (double)((qchunks + c / G - 1) / (c / G));
+      const double cost = (waves <= 1 ? 1 : waves <= 2 ? 2 : waves + 0.3) * (steps + 2.5);
+      if (c == 1 || cost < 0.98 * best) best = cost, sp = c;
+    }
   } else {
-    sp = sp / G;          // chunks of one head
-    if (sp > qchunks) sp = qchunks;
-    sp = (sp < 1 ? 1 : sp) * G;
+    // 8 CTAs an SM (256 ragged blocks of up to 64 tokens 350 us; 4 an SM 363)
+    sp = busy > 0 ? (8 * kSms + busy - 1) / busy : 1;
+    if (sp > 64 * G) sp = 64 * G;
+    if (sp < G) {
+      while (G % sp) ++sp;  // whole heads, evenly
+    } else {
+      sp = sp / G;          // chunks of one head
+      if (sp > qchunks) sp = qchunks;
+      sp = (sp < 1 ? 1 : sp) * G;
+    }
   }
   b.splits = (int)sp;
   return b;

@@ -402,9 +402,18 @@ __global__ void __launch_bounds__(kTcThreads, 2)
 
 // ---- dk, dv and the table's gradient ---------------------------------------------------------------
 
-template <int D>
+// The table's sums stand in columns that one thread at a time adds to: a thread's own, or, with several
+// axes, one column per axis for the two threads of a key, who work on different axes at any time and change
+// over in turns.  That halves the sums (32 buckets, two axes: 68 -> 34 KB) and lets two CTAs share an SM,
+// which the work behind every score's look-ups needs: dk, dv and table of six frames of 1370 tokens (16 heads
+// of 64, two axes) 698 -> 552 us, 1024 tokens of three axes (32 heads of 32, whole backward) 226 -> 178 us.
+// Where two CTAs do not fit in any case, a CTA has the registers of both, own columns and a third stage
+// (64 buckets, whole backward: 987 us; turns without company: 1125 us).
+template <int D, int NA, int CTAS>
 struct DkvTc : TcTile<D> {
-  static constexpr int kStages = 3;
+  static constexpr int kStages = D == 32 || CTAS == 1 ? 3 : 2;
+  static constexpr bool kTurns = NA > 1 && CTAS == 2;
+  static constexpr int kSums = kTurns ? kEwThreads / 2 : kEwThreads;
   static constexpr bool kAlias = D == 64;
   static constexpr int kColS = 0, kColDp = 64;
   static constexpr int kColP = kAlias ? 0 : 128, kColDs = kAlias ? 64 : 160;
@@ -412,9 +421,9 @@ struct DkvTc : TcTile<D> {
   static constexpr int kColDv = kAlias ? 128 : 192, kColDk = kColDv + D;
   static_assert(kColDk + D <= 256, "tensor memory");
 };
-template <int D, int NA>
+template <int D, int NA, int CTAS>
 struct DkvTcSmem {
-  using C = DkvTc<D>;
+  using C = DkvTc<D, NA, CTAS>;
   uint8_t k[C::kRowsBytes];
   uint8_t v[C::kRowsBytes];
   uint8_t q[C::kStages][C::kColsBytes];
@@ -422,13 +431,13 @@ struct DkvTcSmem {
   int pos[C::kStages][NA][kTcCols];
   float nlse[C::kStages][kTcCols], ndelta[C::kStages][kTcCols];  // negated: packed adds have no signs
   ChunkMeta meta[C::kStages];
-  uint64_t k_full, q_full[C::kStages], q_empty[C::kStages], s_full[2], p_full[2], done[2], drain, ew;
+  uint64_t k_full, q_full[C::kStages], q_empty[C::kStages], s_full[2], p_full[2], done[2], drain, ew, turn[4];
   uint32_t tmem_base;
   int abort, vote, pad;
   // behind it: table fp32 [NA][2 maxd + 1], the buckets' byte offsets int32 [2 maxd + 1], and the
-  // threads' sums fp32 [NA][NB and one for ids out of range][256]
+  // columns of sums fp32 [NA][NB and one for ids out of range][kSums]
   static size_t bytes(int maxd, int nb) {
-    return sizeof(DkvTcSmem) + (size_t)(NA + 1) * (2 * maxd + 1) * 4 + (size_t)NA * (nb + 1) * kEwThreads * 4;
+    return sizeof(DkvTcSmem) + (size_t)(NA + 1) * (2 * maxd + 1) * 4 + (size_t)NA * (nb + 1) * C::kSums * 4;
   }
 };
 
@@ -440,13 +449,13 @@ __device__ __forceinline__ void add_two_tc(char* col, int b0, float v0, int b1, 
   *p1 = (b0 == b1 ? s0 : x1) + v1;
 }
 
-template <int D, int NA>
-__global__ void __launch_bounds__(kTcThreads, D == 64 && NA > 1 ? 1 : 2)
+template <int D, int NA, int CTAS>
+__global__ void __launch_bounds__(kTcThreads, CTAS)
     rp_dkv_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
                      const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap omap,
                      const Params p) {
-  using C = DkvTc<D>;
-  using Smem = DkvTcSmem<D, NA>;
+  using C = DkvTc<D, NA, CTAS>;
+  using Smem = DkvTcSmem<D, NA, CTAS>;
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   Smem& S = *reinterpret_cast<Smem*>(smem_raw);
   if (smem_u32(smem_raw) & 1023) {
@@ -493,6 +502,7 @@ __global__ void __launch_bounds__(kTcThreads, D == 64 && NA > 1 ? 1 : 2)
     }
     mbar_init(&S.drain, 1);
     mbar_init(&S.ew, kEwThreads);
+    for (int i = 0; i < 4; ++i) mbar_init(&S.turn[i], 2);
     fence_mbar_init();
   }
   __syncwarp();
@@ -637,21 +647,29 @@ __global__ void __launch_bounds__(kTcThreads, D == 64 && NA > 1 ? 1 : 2)
     }
     for (int i = ew; i < top + 1; i += kEwThreads) {
       const int b = p.bucket_of[i];
-      boff[i] = (b < 0 || b >= p.NB ? p.NB : b) * kEwThreads * 4;
+      boff[i] = (b < 0 || b >= p.NB ? p.NB : b) * C::kSums * 4;
     }
-    const int axis_bytes = (p.NB + 1) * kEwThreads * 4;
-    for (int b = 0; b < NA * (p.NB + 1); ++b) hist[b * kEwThreads + ew] = 0.0f;  // the thread's own column
-    char* mine = reinterpret_cast<char*>(hist + ew);
+    const int axis_bytes = (p.NB + 1) * C::kSums * 4;
+    for (int i = ew; i < NA * (p.NB + 1) * C::kSums; i += kEwThreads) hist[i] = 0.0f;
+    char* mine = reinterpret_cast<char*>(hist + (C::kTurns ? r : ew));
     // the running sum of chunks on one distance, and its bucket's offset
     float run[NA];
     int run_b[NA];
 #pragma unroll
-    for (int a = 0; a < NA; ++a) run[a] = 0.0f, run_b[a] = p.NB * kEwThreads * 4;
+    for (int a = 0; a < NA; ++a) run[a] = 0.0f, run_b[a] = p.NB * C::kSums * 4;
 
     EwBarrier eb{&S.ew, abort, p.status, 0};
     bool ok = true, small = false;
     float mul = 0.0f;
     ChunkBias<NA, true> cb;
+    uint32_t turn = 0;
+    // a turn: the two warps that share keys have both come here
+    auto swap = [&]() {
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&S.turn[quarter]);
+      ok = wait_bar_w(&S.turn[quarter], turn & 1, abort, p.status) && ok;
+      ++turn;
+    };
     for (int it = 0; ok && it < steps; ++it) {
       const int st = it % C::kStages, cc = it % nc, head = h0 + it / nc;
       if (cc == 0) {
@@ -727,38 +745,45 @@ __global__ void __launch_bounds__(kTcThreads, D == 64 && NA > 1 ? 1 : 2)
           for (int e = 0; e < 16; ++e) x[e] = 0.0f;
         }
         __syncwarp();
-        // the table's gradient
+        // the table's gradient.  In turns: the halves are on axes ph and ph + 1, forwards in a run of
+        // columns and back in the next, so that a run begins where the one before it ended.
+#pragma unroll 1
+        for (int ph = 0; ph < (C::kTurns ? NA : 1); ++ph) {
+          if (ph > 0) swap();
+          const int place = (g == 0 ? ph : NA - 1 - ph) + half, axis = place < NA ? place : place - NA;
 #pragma unroll
-        for (int a = 0; a < NA; ++a) {
-          char* to = mine + a * axis_bytes;
-          const int4* xs = reinterpret_cast<const int4*>(&S.pos[st][a][col]);
-          const int md = cb.mode(a, 2 * half + g);
-          if (md <= kLane) {
-            float s0 = 0.0f, s1 = 0.0f;
+          for (int a = 0; a < NA; ++a) {
+            if (C::kTurns && a != axis) continue;
+            char* to = mine + a * axis_bytes;
+            const int4* xs = reinterpret_cast<const int4*>(&S.pos[st][a][col]);
+            const int md = cb.mode(a, 2 * half + g);
+            if (md <= kLane) {
+              float s0 = 0.0f, s1 = 0.0f;
 #pragma unroll
-            for (int e = 0; e < 16; e += 2) fadd2_acc(s0, s1, x[e], x[e + 1]);
-            const int b = boff[md == kOne ? cb.one[a] : clamp_index(xs[0].x, rowc[a], top)];
-            if (b != run_b[a]) {
-              *reinterpret_cast<float*>(to + run_b[a]) += run[a];
-              run[a] = 0.0f;
-              run_b[a] = b;
-            }
-            run[a] += s0 + s1;
-          } else if (md == kFour) {
+              for (int e = 0; e < 16; e += 2) fadd2_acc(s0, s1, x[e], x[e + 1]);
+              const int b = boff[md == kOne ? cb.one[a] : clamp_index(xs[0].x, rowc[a], top)];
+              if (b != run_b[a]) {
+                *reinterpret_cast<float*>(to + run_b[a]) += run[a];
+                run[a] = 0.0f;
+                run_b[a] = b;
+              }
+              run[a] += s0 + s1;
+            } else if (md == kFour) {
 #pragma unroll
-            for (int f = 0; f < 4; f += 2)
-              add_two_tc(to, boff[clamp_index(xs[f].x, rowc[a], top)],
-                         (x[4 * f] + x[4 * f + 1]) + (x[4 * f + 2] + x[4 * f + 3]),
-                         boff[clamp_index(xs[f + 1].x, rowc[a], top)],
-                         (x[4 * f + 4] + x[4 * f + 5]) + (x[4 * f + 6] + x[4 * f + 7]));
-          } else {
+              for (int f = 0; f < 4; f += 2)
+                add_two_tc(to, boff[clamp_index(xs[f].x, rowc[a], top)],
+                           (x[4 * f] + x[4 * f + 1]) + (x[4 * f + 2] + x[4 * f + 3]),
+                           boff[clamp_index(xs[f + 1].x, rowc[a], top)],
+                           (x[4 * f + 4] + x[4 * f + 5]) + (x[4 * f + 6] + x[4 * f + 7]));
+            } else {
 #pragma unroll
-            for (int f = 0; f < 4; ++f) {
-              const int4 u = xs[f];
-              add_two_tc(to, boff[clamp_index(u.x, rowc[a], top)], x[4 * f], boff[clamp_index(u.y, rowc[a], top)],
-                         x[4 * f + 1]);
-              add_two_tc(to, boff[clamp_index(u.z, rowc[a], top)], x[4 * f + 2],
-                         boff[clamp_index(u.w, rowc[a], top)], x[4 * f + 3]);
+              for (int f = 0; f < 4; ++f) {
+                const int4 u = xs[f];
+                add_two_tc(to, boff[clamp_index(u.x, rowc[a], top)], x[4 * f], boff[clamp_index(u.y, rowc[a], top)],
+                           x[4 * f + 1]);
+                add_two_tc(to, boff[clamp_index(u.z, rowc[a], top)], x[4 * f + 2],
+                           boff[clamp_index(u.w, rowc[a], top)], x[4 * f + 3]);
+              }
             }
           }
         }
@@ -770,16 +795,21 @@ __global__ void __launch_bounds__(kTcThreads, D == 64 && NA > 1 ? 1 : 2)
       if (cc == nc - 1) {
         // the head's sums of the CTA's threads to global memory, and the columns back to 0
 #pragma unroll
-        for (int a = 0; a < NA; ++a) {
-          *reinterpret_cast<float*>(mine + a * axis_bytes + run_b[a]) += run[a];
-          run[a] = 0.0f;
+        for (int turns = 0; turns < (C::kTurns ? 2 : 1); ++turns) {
+          if (C::kTurns) ok = eb.sync() && ok;
+          if (C::kTurns && turns != half) continue;
+#pragma unroll
+          for (int a = 0; a < NA; ++a) {
+            *reinterpret_cast<float*>(mine + a * axis_bytes + run_b[a]) += run[a];
+            run[a] = 0.0f;
+          }
         }
         ok = eb.sync() && ok;
         for (int b = warp - 2; b < bins; b += kEwThreads / 32) {
-          float* of = hist + (b + b / p.NB) * kEwThreads + lane;  // past each axis' entry for ids out of range
+          float* of = hist + (b + b / p.NB) * C::kSums + lane;  // past each axis' entry for ids out of range
           float v = 0.0f;
 #pragma unroll
-          for (int t = 0; t < kEwThreads; t += 32) {
+          for (int t = 0; t < C::kSums; t += 32) {
             v += of[t];
             of[t] = 0.0f;
           }
@@ -838,6 +868,17 @@ static bool map_of(CUtensorMap* m, const uint16_t* base, const uint16_t* other, 
   return make_map(m, n > 0 ? base : other, D, heads, n > 0 ? n : 1, 1, box);
 }
 
+template <int D, int NA, int CTAS>
+static lsrm_status run_dkv_tc(const Params& p, const BwdPlan& b, const CUtensorMap& k128, const CUtensorMap& v128,
+                              const CUtensorMap& q64, const CUtensorMap& o64, cudaStream_t s) {
+  const size_t bytes = DkvTcSmem<D, NA, CTAS>::bytes(p.maxd, p.NB);
+  auto* kernel = rp_dkv_tc_kernel<D, NA, CTAS>;
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes) != cudaSuccess)
+    return LSRM_ERR_CUDA;
+  kernel<<<(unsigned)(b.kv_tiles * p.Hkv * p.splits), kTcThreads, bytes, s>>>(k128, v128, q64, o64, p);
+  return cudaGetLastError() == cudaSuccess ? LSRM_OK : LSRM_ERR_CUDA;
+}
+
 template <int D, int NA>
 static lsrm_status run_bwd_tc(const Params& p, const BwdPlan& b, cudaStream_t s) {
   CUtensorMap q128, o128, k64, v64, k128, v128, q64, o64;
@@ -854,14 +895,9 @@ static lsrm_status run_bwd_tc(const Params& p, const BwdPlan& b, cudaStream_t s)
     rp_dq_tc_kernel<D, NA><<<(unsigned)(b.dq_tiles * p.Hq), kTcThreads, bytes, s>>>(q128, o128, k64, v64, p);
     if (cudaGetLastError() != cudaSuccess) return LSRM_ERR_CUDA;
   }
-  if (p.Nk > 0) {
-    const size_t bytes = DkvTcSmem<D, NA>::bytes(p.maxd, p.NB);
-    if (cudaFuncSetAttribute(rp_dkv_tc_kernel<D, NA>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes) !=
-        cudaSuccess)
-      return LSRM_ERR_CUDA;
-    rp_dkv_tc_kernel<D, NA><<<(unsigned)(b.kv_tiles * p.Hkv * p.splits), kTcThreads, bytes, s>>>(k128, v128, q64, o64, p);
-    if (cudaGetLastError() != cudaSuccess) return LSRM_ERR_CUDA;
-  }
+  if (p.Nk > 0)
+    return b.tc == 2 ? run_dkv_tc<D, NA, 2>(p, b, k128, v128, q64, o64, s)
+                     : run_dkv_tc<D, NA, 1>(p, b, k128, v128, q64, o64, s);
   return LSRM_OK;
 }
 
@@ -870,12 +906,14 @@ lsrm_status launch_bwd_tc(const Params& p, int D, int NA, const BwdPlan& b, cuda
     return NA == 1 ? run_bwd_tc<32, 1>(p, b, s) : NA == 2 ? run_bwd_tc<32, 2>(p, b, s) : run_bwd_tc<32, 3>(p, b, s);
   return NA == 1 ? run_bwd_tc<64, 1>(p, b, s) : NA == 2 ? run_bwd_tc<64, 2>(p, b, s) : run_bwd_tc<64, 3>(p, b, s);
 }
-size_t bwd_tc_smem(int D, int NA, int maxd, int nb) {
-  if (D == 32)
-    return NA == 1 ? DkvTcSmem<32, 1>::bytes(maxd, nb) : NA == 2 ? DkvTcSmem<32, 2>::bytes(maxd, nb)
-                                                                : DkvTcSmem<32, 3>::bytes(maxd, nb);
-  return NA == 1 ? DkvTcSmem<64, 1>::bytes(maxd, nb) : NA == 2 ? DkvTcSmem<64, 2>::bytes(maxd, nb)
-                                                              : DkvTcSmem<64, 3>::bytes(maxd, nb);
+template <int D, int NA>
+static int dkv_fit(int maxd, int nb) {
+  if (2 * (DkvTcSmem<D, NA, 2>::bytes(maxd, nb) + 1024) <= 228 * 1024) return 2;
+  return DkvTcSmem<D, NA, 1>::bytes(maxd, nb) <= 227 * 1024 ? 1 : 0;
+}
+int bwd_tc_ctas(int D, int NA, int maxd, int nb) {
+  if (D == 32) return NA == 1 ? dkv_fit<32, 1>(maxd, nb) : NA == 2 ? dkv_fit<32, 2>(maxd, nb) : dkv_fit<32, 3>(maxd, nb);
+  return NA == 1 ? dkv_fit<64, 1>(maxd, nb) : NA == 2 ? dkv_fit<64, 2>(maxd, nb) : dkv_fit<64, 3>(maxd, nb);
 }
 
 }  // namespace rp

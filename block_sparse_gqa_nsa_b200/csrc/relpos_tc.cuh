@@ -82,11 +82,11 @@ __device__ __forceinline__ void copy_tail(uint8_t* dst, const uint16_t* src, int
 }
 __device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory"); }
 
-// what a chunk's column positions have in common on each axis: their range, and bit g of same16 / same4:
-// columns 16 g .. 16 g + 15 have one position / one position per aligned run of four
+// what a chunk's column positions have in common on each axis: their range, and in bits 2 g, 2 g + 1 of
+// runs kLane, kFour or kEach: columns 16 g .. 16 g + 15 have one position, one per aligned run of four, any
 struct ChunkMeta {
   int lo[kMaxAxes], hi[kMaxAxes];
-  uint32_t same16[kMaxAxes], same4[kMaxAxes];
+  uint32_t runs[kMaxAxes];
 };
 // the producer warp's part: lane i holds the positions of columns i and i + 32
 template <int NA>
@@ -102,15 +102,13 @@ __device__ __forceinline__ void note_positions(const int (&x)[NA][2], int (*pos)
     pos[a][lane] = x[a][0];
     pos[a][lane + 32] = x[a][1];
     if (lane == 0) {
-      uint32_t same16 = 0, same4 = 0;
+      uint32_t runs = 0;
 #pragma unroll
       for (int g = 0; g < 4; ++g) {
         const uint32_t e = (g < 2 ? e0 : e1) >> (16 * (g & 1));
-        if ((e & 0x7fffu) == 0x7fffu) same16 |= 1u << g;
-        if ((e & 0x7777u) == 0x7777u) same4 |= 1u << g;
+        runs |= (uint32_t)((e & 0x7fffu) == 0x7fffu ? kLane : (e & 0x7777u) == 0x7777u ? kFour : kEach) << (2 * g);
       }
-      m.lo[a] = lo, m.hi[a] = hi;
-      m.same16[a] = same16, m.same4[a] = same4;
+      m.lo[a] = lo, m.hi[a] = hi, m.runs[a] = runs;
     }
   }
 }
@@ -124,8 +122,7 @@ __device__ __forceinline__ void note_positions(const int (&x)[NA][2], int (*pos)
 template <int NA, bool RUNS>
 struct ChunkBias {
   int one[NA];  // the chunk's only index into the table, or -1
-  int whole[NA];
-  uint32_t same16[NA], same4[NA];
+  uint32_t runs[NA];  // 0 (kOne) with one; !RUNS: the mode of the whole chunk
   float ub;  // the bias common to the chunk
   __device__ __forceinline__ void set(const ChunkMeta& m, const int (&row_lo)[NA], const int (&row_hi)[NA], int maxd,
                                       const float* lut, int top) {
@@ -135,14 +132,16 @@ struct ChunkBias {
       const int lo = clamp_index(m.lo[a] - row_hi[a], maxd, top);
       const int hi = clamp_index(m.hi[a] - row_lo[a], maxd, top);
       one[a] = lo == hi ? lo : -1;
-      same16[a] = m.same16[a], same4[a] = m.same4[a];
-      whole[a] = lo == hi ? kOne : same16[a] == 15u ? kLane : same4[a] == 15u ? kFour : kEach;
-      if (lo == hi) ub += lut[a * (top + 1) + lo];
+      runs[a] = m.runs[a];
+      if (!RUNS) runs[a] = runs[a] == 0x55u ? kLane : (runs[a] & runs[a] >> 1 & 0x55u) == 0 ? kFour : kEach;
+      if (lo == hi) {
+        runs[a] = kOne;
+        ub += lut[a * (top + 1) + lo];
+      }
     }
   }
   __device__ __forceinline__ int mode(int a, int g) const {
-    if (!RUNS) return whole[a];
-    return one[a] >= 0 ? kOne : (same16[a] >> g & 1) ? kLane : (same4[a] >> g & 1) ? kFour : kEach;
+    return RUNS ? runs[a] >> (2 * g) & 3 : runs[a];
   }
   // whether run g has one bias per row
   __device__ __forceinline__ bool flat(int g) const {

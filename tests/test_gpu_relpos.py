@@ -129,6 +129,15 @@ FORWARD = {
     "long_frames": dict(lens_q=[640], dim=64, axes=2, places="frames", maxd=7, buckets=8),
     "long_widest": dict(lens_q=[330], axes=3, maxd=1023, buckets=64, dim=64, places="scattered"),
     "long_odd_buckets": dict(lens_q=[400, 300], axes=3, buckets=7, maxd=9, places="scattered"),
+    # the key pass with two CTAs an SM and several heads, and where one CTA's sums fill the shared memory
+    "long_turns": dict(lens_q=[520, 300], heads=8, kv_heads=2, axes=3, places="scattered", maxd=40),
+    "long_turns64": dict(lens_q=[290, 310], heads=6, kv_heads=1, axes=2, places="frames", maxd=20, dim=64),
+    "long_one_cta": dict(lens_q=[300, 411], axes=3, places="scattered", maxd=60, buckets=48),
+    "long_one_cta64": dict(lens_q=[350], axes=3, places="scattered", dim=64),
+    # 64 and 128 rows a CTA, and the most rows of the kernel for few
+    "rows64": dict(lens_q=[61, 40], lens_k=[300, 33], axes=2, places="scattered"),
+    "rows128": dict(lens_q=[90, 75, 101], lens_k=[400, 257, 70], axes=3, places="scattered"),
+    "rows_few": dict(lens_q=[24, 19, 23], lens_k=[400, 257, 70], heads=32, axes=2, places="scattered"),
 }
 
 
