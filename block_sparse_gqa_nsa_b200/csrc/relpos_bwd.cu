@@ -29,17 +29,18 @@
 namespace lsrm {
 namespace rp {
 
-constexpr int kBThreads = 128, kBChunk = 64, kBStages = 3;
+constexpr int kBThreads = 128, kBChunk = 64, kBStages = 3, kKeyStages = 2;
 constexpr int kBNT = 4, kBCW = 8, kBCols = 32;  // columns of a score tile
 
 template <int D, int NA>
 struct BwdCfg {
   static constexpr int kTile = kBChunk * D / 8;
   static constexpr size_t kRing = (size_t)kBStages * (2 * kTile * 16 + kBChunk * NA * 4);
+  static constexpr size_t kKeyRing = (size_t)kKeyStages * (2 * kTile * 16 + kBChunk * (NA * 4 + 8));
   __host__ __device__ static size_t lut(int maxd) { return (((size_t)NA * (2 * maxd + 1) * 4) + 15) & ~(size_t)15; }
   static size_t smem_dq(int maxd) { return kRing + lut(maxd); }
   static size_t smem_dkv(int maxd, int nb) {
-    return kRing + (size_t)kBStages * kBChunk * 8 + lut(maxd) + (size_t)NA * (nb + 1) * kBThreads * 4 +
+    return kKeyRing + lut(maxd) + (size_t)NA * (nb + 1) * kBThreads * 4 +
            ((size_t)2 * maxd + 1) * 4;
   }
 };
@@ -316,10 +317,10 @@ __global__ void __launch_bounds__(kBThreads, D == 32 ? 4 : 2) rp_dkv_kernel(cons
   constexpr int kRows = 64 * MT;
   extern __shared__ __align__(16) unsigned char smem_raw[];
   uint4* qs = reinterpret_cast<uint4*>(smem_raw);
-  uint4* ds = qs + kBStages * C::kTile;
-  int* ps = reinterpret_cast<int*>(ds + kBStages * C::kTile);
-  float* ls = reinterpret_cast<float*>(smem_raw + C::kRing);  // [stage][2][chunk]: LSE (log2 units), Delta
-  float* lut = ls + kBStages * 2 * kBChunk;
+  uint4* ds = qs + kKeyStages * C::kTile;
+  int* ps = reinterpret_cast<int*>(ds + kKeyStages * C::kTile);
+  float* ls = reinterpret_cast<float*>(ps + kKeyStages * kBChunk * NA);  // [stage][2][chunk]: LSE (log2 units), Delta
+  float* lut = ls + kKeyStages * 2 * kBChunk;
   float* hist = lut + C::lut(p.maxd) / 4;  // [NA][NB and one for ids out of range][threads]
   int* boff = reinterpret_cast<int*>(hist + (size_t)NA * (p.NB + 1) * kBThreads);  // a bucket's byte offset
 
@@ -349,7 +350,7 @@ __global__ void __launch_bounds__(kBThreads, D == 32 ? 4 : 2) rp_dkv_kernel(cons
   auto load = [&](int it) {
     if (it < steps) {
       const int h = hk * p.G + h0 + it / nc, q0 = qlo + (c0 + it % nc) * kBChunk, n = min(kBChunk, qhi - q0);
-      const int st = it % kBStages;
+      const int st = it % kKeyStages;
       load_tile<D, kBCW, kBChunk, kBThreads>(qs + st * C::kTile, p.q, q0, n, p.Hq, h, tid);
       load_tile<D, kBCW, kBChunk, kBThreads>(ds + st * C::kTile, p.dout, q0, n, p.Hq, h, tid);
       for (int i = tid; i < kBChunk * NA; i += kBThreads)
@@ -361,7 +362,6 @@ __global__ void __launch_bounds__(kBThreads, D == 32 ? 4 : 2) rp_dkv_kernel(cons
     cp_async_commit();
   };
   load(0);
-  load(1);
   for (int i = tid; i < top + 1; i += kBThreads) {
     const int b = p.bucket_of[i];
     boff[i] = (b < 0 || b >= p.NB ? p.NB : b) * kBThreads * 4;
@@ -435,14 +435,14 @@ __global__ void __launch_bounds__(kBThreads, D == 32 ? 4 : 2) rp_dkv_kernel(cons
   float mul = 0.0f;
   for (int it = 0; it < steps; ++it) {
     const int head = h0 + it / nc, cc = it % nc;
-    cp_async_wait<1>();
+    cp_async_wait<0>();
     __syncthreads();
-    load(it + 2);
+    load(it + 1);
     if (cc == 0) {  // the barriers since the last head's tiles ended the old table's use
       small = fill_units<NA, kBThreads>(p, lut, hk * p.G + head, tid);
       mul = small ? p.scale * kLog2e : p.scale;
     }
-    const int st = it % kBStages;
+    const int st = it % kKeyStages;
     const uint4* qt = qs + st * C::kTile;
     const uint4* dt = ds + st * C::kTile;
 #pragma unroll 1
