@@ -416,18 +416,7 @@ __global__ void __launch_bounds__(kBThreads, D == 32 ? 4 : 2) rp_dkv_kernel(cons
       run[a] = 0.0f;
     }
     __syncthreads();
-    for (int b = warp; b < bins; b += kBThreads / 32) {
-      float* of = hist + (b + b / p.NB) * kBThreads + lane;  // past each axis' entry for ids out of range
-      float x = 0.0f;
-#pragma unroll
-      for (int t = 0; t < kBThreads; t += 32) {
-        x += of[t];
-        of[t] = 0.0f;
-      }
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
-      if (lane == 0) tab_part[head * bins + b] = x;
-    }
+    flush_sums<kBThreads, kBThreads>(hist, bins, p.NB, tid, tab_part + head * bins);
     __syncthreads();
   };
 

@@ -805,18 +805,7 @@ __global__ void __launch_bounds__(kTcThreads, CTAS)
           }
         }
         ok = eb.sync() && ok;
-        for (int b = warp - 2; b < bins; b += kEwThreads / 32) {
-          float* of = hist + (b + b / p.NB) * C::kSums + lane;  // past each axis' entry for ids out of range
-          float v = 0.0f;
-#pragma unroll
-          for (int t = 0; t < C::kSums; t += 32) {
-            v += of[t];
-            of[t] = 0.0f;
-          }
-#pragma unroll
-          for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-          if (lane == 0) tab_part[head * bins + b] = v;
-        }
+        flush_sums<C::kSums, kEwThreads>(hist, bins, p.NB, ew, tab_part + head * bins);
         ok = eb.sync() && ok;
       }
     }
