@@ -49,7 +49,7 @@ struct BwdCfg {
 // (every key masked by a huge finite bias): corr = log2 sum_j exp(t - lse), a row at a time, lanes over
 // keys.  The tile's rows are wrow .. wrow + 15; lane (g, .) holds the LSE of rows g and g + 8.
 template <int D, int NA>
-__device__ __noinline__ float2 huge_rows(const Params& p, const float* lut, bool small, float lse0, float lse1,
+__device__ __forceinline__ float2 huge_rows(const Params& p, const float* lut, bool small, float lse0, float lse1,
                                          int wrow, int h, int hk, int klo, int khi, int lane) {
   const float units = small ? kLn2 : 1.0f;  // the table's to natural ones
   float2 corr = make_float2(0.0f, 0.0f);

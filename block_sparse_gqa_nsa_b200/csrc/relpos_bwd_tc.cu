@@ -72,7 +72,7 @@ __device__ __forceinline__ bool ew_fill(const Params& p, float* lut, int h, int 
 
 // log2 sum_j exp(t - l) of one row whose |LSE| is huge (see huge_rows), by a whole warp
 template <int D, int NA>
-__device__ __noinline__ float huge_row(const Params& p, const float* lut, bool small, float l, int row, int h, int hk,
+__device__ __forceinline__ float huge_row(const Params& p, const float* lut, bool small, float l, int row, int h, int hk,
                                        int klo, int khi, int lane) {
   const float units = small ? kLn2 : 1.0f;
   const uint16_t* q = p.q + ((size_t)row * p.Hq + h) * D;

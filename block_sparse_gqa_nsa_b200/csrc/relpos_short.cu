@@ -20,7 +20,11 @@ template <int D, int NA>
 struct ShCfg {
   static constexpr int kTile = kShKeys * D / 8;  // 16-byte pieces of a K or V block
   static constexpr size_t kRing = 2 * ((size_t)2 * kTile * 16 + kShKeys * NA * 4);
-  static size_t smem(int maxd, int heads) { return kRing + (size_t)heads * NA * (2 * maxd + 1) * 4; }
+  static constexpr int kUnit = 16 * D / 8;  // pieces of 16 rows
+  static constexpr size_t kUnits = (size_t)kShWarps * 3 * kUnit * 16;  // dq: the next queries, dO and out of a warp
+  static size_t smem(int maxd, int heads, bool dq) {
+    return kRing + (dq ? kUnits : 0) + (size_t)heads * NA * (2 * maxd + 1) * 4;
+  }
 };
 
 // the CTA's place: a tile of 64 queries of a segment, heads h0 .. h0 + nh - 1 of KV head hk
@@ -78,6 +82,28 @@ __device__ __forceinline__ void sh_rows(uint32_t (*a)[4], const uint16_t* src, c
                                         int lane) {
   load_a_rows<D>(a, r < qhi ? src + ((size_t)r * p.Hq + h) * D : nullptr,
                  r + 8 < qhi ? src + ((size_t)(r + 8) * p.Hq + h) * D : nullptr, lane);
+}
+
+// 16 rows of one head into a warp's buffer (zeros past the segment), and from there as an A operand
+template <int D>
+__device__ __forceinline__ int sh_piece(int row, int c) {
+  return D == 32 ? row * 4 + (c ^ ((row >> 1) & 3)) : row * 8 + (c ^ (row & 7));
+}
+template <int D>
+__device__ __forceinline__ void sh_copy(uint4* dst, const uint16_t* src, int row0, int n, int heads, int h, int lane) {
+#pragma unroll
+  for (int i = lane; i < 16 * (D / 8); i += 32) {
+    const int r = i / (D / 8), c = i % (D / 8);
+    const bool ok = r < n;
+    cp_async16(dst + sh_piece<D>(r, c), src + ((size_t)(row0 + (ok ? r : 0)) * heads + h) * D + c * 8, ok);
+  }
+}
+template <int D>
+__device__ __forceinline__ void sh_take(uint32_t (*a)[4], const uint4* src, int lane) {
+#pragma unroll
+  for (int ks = 0; ks < D / 16; ++ks)
+    ldmatrix_x4(a[ks][0], a[ks][1], a[ks][2], a[ks][3],
+                smem_u32(src + sh_piece<D>(lane & 15, 2 * ks + (lane >> 4))));
 }
 
 // positions of rows r and r + 8 as the bias takes them, and the warp's range
@@ -261,9 +287,10 @@ __global__ void __launch_bounds__(kShThreads, 2) rp_short_fwd_kernel(const Param
   }
 }
 
-// log2 sum_j exp(t - l) of the rows whose |LSE| is huge among the 16 of a unit (see relpos_bwd.cu)
+// log2 sum_j exp(t - l) of the rows whose |LSE| is huge among the 16 of a unit (see relpos_bwd.cu).  Inline,
+// rare as it is: around a call the kernel kept its registers in local memory (256 ragged blocks 118 -> 89 us).
 template <int D, int NA>
-__device__ __noinline__ float2 sh_huge(const Params& p, const float* lut, bool small, float lse0, float lse1, int row0,
+__device__ __forceinline__ float2 sh_huge(const Params& p, const float* lut, bool small, float lse0, float lse1, int row0,
                                        int h, int hk, int klo, int khi, int lane) {
   const float units = small ? kLn2 : 1.0f;
   float2 corr = make_float2(0.0f, 0.0f);
@@ -296,7 +323,8 @@ __global__ void __launch_bounds__(kShThreads, D == 32 ? 2 : 1) rp_short_dq_kerne
   extern __shared__ __align__(16) unsigned char smem_raw[];
   uint4* ring = reinterpret_cast<uint4*>(smem_raw);  // [2][K, V]
   int* ps = reinterpret_cast<int*>(ring + 4 * C::kTile);
-  float* lut = reinterpret_cast<float*>(smem_raw + C::kRing);
+  uint4* next = reinterpret_cast<uint4*>(smem_raw + C::kRing) + (threadIdx.x >> 5) * 3 * C::kUnit;
+  float* lut = reinterpret_cast<float*>(smem_raw + C::kRing + C::kUnits);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, tq = lane & 3;
   const ShPlace P = sh_place(p);
   if (!P.live) return;
@@ -317,18 +345,20 @@ __global__ void __launch_bounds__(kShThreads, D == 32 ? 2 : 1) rp_short_dq_kerne
   load(0);
   auto row_of = [&](int u) { return P.row0 + u / P.nh * 16 + g; };
   auto head_of = [&](int u) { return u % P.nh; };
-  // a unit's operands: queries, dO, out, LSE
-  uint32_t qa[D / 16][4], da[D / 16][4], oa[D / 16][4];
-  float lse[2];
-  auto fetch = [&](int u, uint32_t (*q)[4], uint32_t (*d)[4], uint32_t (*o)[4], float* ls) {
-    const int r = row_of(u), h = P.h0 + head_of(u);
-    sh_rows<D>(q, p.q, p, r, P.qhi, h, lane);
-    sh_rows<D>(d, p.dout, p, r, P.qhi, h, lane);
-    sh_rows<D>(o, p.o_in, p, r, P.qhi, h, lane);
-    ls[0] = r < P.qhi ? p.lse_in[(size_t)r * p.Hq + h] : INFINITY;
-    ls[1] = r + 8 < P.qhi ? p.lse_in[(size_t)(r + 8) * p.Hq + h] : INFINITY;
+  // a unit's operands: queries, dO and out by asynchronous copies, LSE
+  float lse[2], next_lse[2];
+  auto fetch = [&](int u) {
+    if (u < units) {
+      const int r0 = P.row0 + u / P.nh * 16, r = r0 + g, n = P.qhi - r0, h = P.h0 + head_of(u);
+      sh_copy<D>(next, p.q, r0, n, p.Hq, h, lane);
+      sh_copy<D>(next + C::kUnit, p.dout, r0, n, p.Hq, h, lane);
+      sh_copy<D>(next + 2 * C::kUnit, p.o_in, r0, n, p.Hq, h, lane);
+      next_lse[0] = r < P.qhi ? p.lse_in[(size_t)r * p.Hq + h] : INFINITY;
+      next_lse[1] = r + 8 < P.qhi ? p.lse_in[(size_t)(r + 8) * p.Hq + h] : INFINITY;
+    }
+    cp_async_commit();
   };
-  if (warp < units) fetch(warp, qa, da, oa, lse);
+  fetch(warp);
   const bool small = sh_fill<NA>(p, lut, P.h0, P.nh, tid);
   const float mul = small ? p.scale * kLog2e : p.scale;
 
@@ -337,6 +367,17 @@ __global__ void __launch_bounds__(kShThreads, D == 32 ? 2 : 1) rp_short_dq_kerne
     const bool work = u < units;
     const int r = row_of(work ? u : 0), hh = head_of(work ? u : 0), h = P.h0 + hh;
     const float* mine = lut + hh * NA * (top + 1);
+    uint32_t qa[D / 16][4], da[D / 16][4], oa[D / 16][4];
+    cp_async_wait<0>();
+    __syncwarp();
+    if (work) {
+      sh_take<D>(qa, next, lane);
+      sh_take<D>(da, next + C::kUnit, lane);
+      sh_take<D>(oa, next + 2 * C::kUnit, lane);
+      lse[0] = next_lse[0], lse[1] = next_lse[1];
+    }
+    __syncwarp();
+    fetch(u + kShWarps);
     int rowc[1][2][NA], q_lo[NA], q_hi[NA];
     sh_row_positions<NA>(p, r, P.qhi, rowc, q_lo, q_hi);
     float delta[2] = {0.0f, 0.0f}, rest[2] = {0.0f, 0.0f}, corr[2] = {0.0f, 0.0f}, row[2], l2[2];
@@ -372,7 +413,10 @@ __global__ void __launch_bounds__(kShThreads, D == 32 ? 2 : 1) rp_short_dq_kerne
     for (int blk = 0; blk < blocks; ++blk) {
       const int i = blocks == 1 ? 0 : round * blocks + blk;
       if (blocks > 1 || round == 0) {
-        cp_async_wait<0>();
+        if (blocks == 1)
+          cp_async_wait<1>();  // all but the next operands
+        else
+          cp_async_wait<0>();
         __syncthreads();  // the block is here, and the other buffer's readers are done
         load(i + 1);
       }
@@ -469,14 +513,12 @@ __global__ void __launch_bounds__(kShThreads, D == 32 ? 2 : 1) rp_short_dq_kerne
                     fmaf(-more, pk[n][2 * k + 1], dq[n][2 * k + 1]) * p.scale);
       }
     }
-    __syncwarp();
-    if (u + kShWarps < units) fetch(u + kShWarps, qa, da, oa, lse);
   }
 }
 
 template <int D, int NA>
 static lsrm_status run_short(const Params& p, long long ctas, bool dq, cudaStream_t s) {
-  const size_t bytes = ShCfg<D, NA>::smem(p.maxd, p.G < kShHeads ? p.G : kShHeads);
+  const size_t bytes = ShCfg<D, NA>::smem(p.maxd, p.G < kShHeads ? p.G : kShHeads, dq);
   const void* kernel = dq ? (const void*)rp_short_dq_kernel<D, NA> : (const void*)rp_short_fwd_kernel<D, NA>;
   if (bytes > 48 * 1024 &&
       cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes) != cudaSuccess)
