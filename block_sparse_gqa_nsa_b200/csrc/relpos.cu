@@ -30,10 +30,8 @@ constexpr float kSlack = 8.0f;
 
 template <int D, int NA, int NW>
 struct FwdCfg {
-  // Column groups a score tile, and CTAs of 128 threads an SM.  16 and 64 segments of 24 to 64 queries against
-  // 512 keys, 32 heads of 32: 41-43 us and 112-121; four CTAs (fewer registers) 50-57; tiles of 8 groups
-  // and two CTAs 33-60 and 118-123.
-  static constexpr int NT = 4, CW = 2 * NT, kCols = 8 * NT;
+  // CTAs of 128 threads an SM.  16 and 64 segments of 24 to 64 queries against 512 keys, 32 heads of 32: 41-43 us
+  // and 112-121; four CTAs (fewer registers) 50-57; score tiles of 64 columns and two CTAs 33-60 and 118-123.
   static constexpr int kMinCtas = (D == 32 ? 3 : 2) * 4 / NW;
   static constexpr int kRows = 32 * NW, kThreads = 32 * NW;
   static constexpr int kTile = kChunk * D / 8;  // 16-byte pieces of a K or V stage
@@ -101,8 +99,8 @@ __global__ void __launch_bounds__(32 * NW, FwdCfg<D, NA, NW>::kMinCtas) rp_fwd_k
   auto load = [&](int c) {
     if (c < c1) {
       const int st = c % kStages, k0 = klo + c * kChunk, n = min(kChunk, khi - k0);
-      load_tile<D, C::CW, kChunk, C::kThreads>(ks + st * C::kTile, p.k, k0, n, p.Hkv, hk, tid);
-      load_tile<D, C::CW, kChunk, C::kThreads>(vs + st * C::kTile, p.v, k0, n, p.Hkv, hk, tid);
+      load_tile<D, kChunk, C::kThreads>(ks + st * C::kTile, p.k, k0, n, p.Hkv, hk, tid);
+      load_tile<D, kChunk, C::kThreads>(vs + st * C::kTile, p.v, k0, n, p.Hkv, hk, tid);
       // positions past the end repeat the last key's, so they do not widen the tile's range
       for (int i = tid; i < kChunk * NA; i += C::kThreads)
         cp_async4(ps + st * kChunk * NA + i, p.pos_k + (size_t)(k0 + min(i / NA, n - 1)) * NA + i % NA, true);
@@ -163,14 +161,14 @@ __global__ void __launch_bounds__(32 * NW, FwdCfg<D, NA, NW>::kMinCtas) rp_fwd_k
     const uint4* vt = vs + (c % kStages) * C::kTile;
     const int* pt = ps + (c % kStages) * kChunk * NA;
 #pragma unroll 1
-    for (int kb = 0; kb < kChunk; kb += C::kCols) {
+    for (int kb = 0; kb < kChunk; kb += kCols) {
       const int left = nk - c * kChunk - kb;  // keys from here on
       if (left <= 0 || wrow >= qhi) break;
-      float s[2][C::NT][4];
+      float s[2][kGroups][4];
 #pragma unroll
-      for (int n = 0; n < C::NT; ++n) {
+      for (int n = 0; n < kGroups; ++n) {
         uint32_t b[D / 8];
-        load_b_rows<D, C::CW>(b, kt, kb, n, lane);
+        load_b_rows<D>(b, kt, kb, n, lane);
 #pragma unroll
         for (int mt = 0; mt < 2; ++mt) {
 #pragma unroll
@@ -182,16 +180,16 @@ __global__ void __launch_bounds__(32 * NW, FwdCfg<D, NA, NW>::kMinCtas) rp_fwd_k
       int mode[NA], one[NA];
 #pragma unroll
       for (int a = 0; a < NA; ++a)
-        mode[a] = axis_mode<NA, C::kCols>(pt + kb * NA + a, q_lo[a], q_hi[a], false, p.maxd, lane, one[a], p.status);
+        mode[a] = axis_mode<NA>(pt + kb * NA + a, q_lo[a], q_hi[a], false, p.maxd, lane, one[a], p.status);
       float base[2][2];
-      const bool fold = add_bias<NA, 2, C::NT, 1>(s, base, mode, one, pt + kb * NA, lut, top, qp, mul, small, tq);
-      if (left < C::kCols) {
+      const bool fold = add_bias<NA, 2, 1>(s, base, mode, one, pt + kb * NA, lut, top, qp, mul, small, tq);
+      if (left < kCols) {
         keep_branch();
 #pragma unroll
-        for (int n = 0; n < C::NT; ++n)
+        for (int n = 0; n < kGroups; ++n)
 #pragma unroll
           for (int e = 0; e < 2; ++e)
-            if (tq * C::CW + 2 * n + e >= left)
+            if (tq * kLaneCols + 2 * n + e >= left)
 #pragma unroll
               for (int mt = 0; mt < 2; ++mt) s[mt][n][e] = s[mt][n][2 + e] = -INFINITY;
       }
@@ -203,13 +201,13 @@ __global__ void __launch_bounds__(32 * NW, FwdCfg<D, NA, NW>::kMinCtas) rp_fwd_k
           float x = fmax3(s[mt][0][2 * i], s[mt][0][2 * i + 1], s[mt][1][2 * i]);
           x = fmaxf(x, s[mt][1][2 * i + 1]);
 #pragma unroll
-          for (int n = 2; n < C::NT; ++n) x = fmax3(x, s[mt][n][2 * i], s[mt][n][2 * i + 1]);
+          for (int n = 2; n < kGroups; ++n) x = fmax3(x, s[mt][n][2 * i], s[mt][n][2 * i + 1]);
           mx[mt][i] = fold ? fmaf(x, mul, base[mt][i]) : x;
         }
       move_reference<2, D / 8>(st, o, mx, to_log2);
       // P = exp(t - m): with the bias in the scores the subtraction comes first (exact for equal scores
       // of any size); with a bias common to a row everything folds into one multiply-add
-      uint32_t pa[2][C::NT / 2][4];
+      uint32_t pa[2][kGroups / 2][4];
 #pragma unroll
       for (int mt = 0; mt < 2; ++mt)
 #pragma unroll
@@ -218,7 +216,7 @@ __global__ void __launch_bounds__(32 * NW, FwdCfg<D, NA, NW>::kMinCtas) rp_fwd_k
           const float cst = base[mt][i] - m;
           float sum0 = 0.0f, sum1 = 0.0f;
 #pragma unroll
-          for (int n = 0; n < C::NT; ++n) {
+          for (int n = 0; n < kGroups; ++n) {
             float p0 = s[mt][n][2 * i], p1 = s[mt][n][2 * i + 1];
             if (fold) {
               ffma2(p0, p1, p0, p1, mul, cst);
@@ -234,11 +232,11 @@ __global__ void __launch_bounds__(32 * NW, FwdCfg<D, NA, NW>::kMinCtas) rp_fwd_k
           st.l[mt][i] += sum0 + sum1;
         }
 #pragma unroll
-      for (int j = 0; j < C::NT / 2; ++j)
+      for (int j = 0; j < kGroups / 2; ++j)
 #pragma unroll
         for (int dc = 0; dc < D / 8; dc += 2) {
           uint32_t b[4];
-          load_b_cols<D, C::CW>(b, vt, kb, j, dc, lane);
+          load_b_cols<D>(b, vt, kb, j, dc, lane);
 #pragma unroll
           for (int mt = 0; mt < 2; ++mt) {
             mma16816(o[mt][dc], pa[mt][j], b);
@@ -323,8 +321,8 @@ __global__ void __launch_bounds__(kFewThreads) rp_few_kernel(const Params p) {
   auto load = [&](int c) {
     if (c < c1) {
       const int st = ((c - c0) / kFewWarps) % kStages, k0 = klo + c * kFewKeys, n = min(kFewKeys, khi - k0);
-      load_tile<D, 8, kFewKeys, 32>(ring + st * 2 * C::kTile, p.k, k0, n, p.Hkv, hk, lane);
-      load_tile<D, 8, kFewKeys, 32>(ring + (st * 2 + 1) * C::kTile, p.v, k0, n, p.Hkv, hk, lane);
+      load_tile<D, kFewKeys, 32>(ring + st * 2 * C::kTile, p.k, k0, n, p.Hkv, hk, lane);
+      load_tile<D, kFewKeys, 32>(ring + (st * 2 + 1) * C::kTile, p.v, k0, n, p.Hkv, hk, lane);
 #pragma unroll
       for (int i = lane; i < kFewKeys * NA; i += 32)
         cp_async4(ps + st * kFewKeys * NA + i, p.pos_k + (size_t)(k0 + min(i / NA, n - 1)) * NA + i % NA, true);
@@ -399,7 +397,7 @@ __global__ void __launch_bounds__(kFewThreads) rp_few_kernel(const Params p) {
 #pragma unroll
     for (int n = 0; n < 4; ++n) {
       uint32_t b[D / 8];
-      load_b_rows<D, 8>(b, kt, 0, n, lane);
+      load_b_rows<D>(b, kt, 0, n, lane);
 #pragma unroll
       for (int e = 0; e < 4; ++e) s[n][e] = 0.0f;
 #pragma unroll
@@ -470,7 +468,7 @@ __global__ void __launch_bounds__(kFewThreads) rp_few_kernel(const Params p) {
 #pragma unroll
       for (int dc = 0; dc < D / 8; dc += 2) {
         uint32_t b[4];
-        load_b_cols<D, 8>(b, vt, 0, j, dc, lane);
+        load_b_cols<D>(b, vt, 0, j, dc, lane);
         mma16816(o[0][dc], pa[j], b);
         mma16816(o[0][dc + 1], pa[j], b + 2);
       }

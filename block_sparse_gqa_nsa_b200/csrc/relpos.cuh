@@ -142,23 +142,22 @@ __device__ __forceinline__ int checked_bucket(const Params& p, int i) {
 __device__ __forceinline__ int clamp_index(int x, int y, int top) { return __viaddmin_s32_relu(x, y, top); }
 
 // ---- tiles in shared memory ----
-// A score tile of 8 NT columns: the accumulator layout gives the lane with tq = lane % 4 the columns
-// 2 tq, 2 tq + 1 of each of the NT groups of 8.  Which stored row a column stands for is free (the
-// softmax and the sums do not care), so column 2 tq + e of group n is stored row tq CW + 2 n + e with
-// CW = 2 NT: a lane then holds CW consecutive tokens, whose positions often are the same on an axis
-// (one look-up for all of them) and load as vectors.
+// A score tile of 32 columns: the accumulator layout gives the lane with tq = lane % 4 the columns
+// 2 tq, 2 tq + 1 of each of the four groups of 8.  Which stored row a column stands for is free (the
+// softmax and the sums do not care), so column 2 tq + e of group n is stored row 8 tq + 2 n + e: a lane
+// then holds 8 consecutive tokens, whose positions often are the same on an axis (one look-up for all
+// of them) and load as vectors.
 //
-// Rows of D bf16 lie in 16-byte pieces, swizzled so that the eight rows of one 8x8 matrix (0, 1, CW,
-// CW + 1, 2 CW, .. behind 2 n) fall into different banks.
-template <int D, int CW>
+// Rows of D bf16 lie in 16-byte pieces, swizzled so that the eight rows of one 8x8 matrix (0, 1, 8, 9,
+// 16, .. behind 2 n) fall into different banks.
+constexpr int kCols = 32, kGroups = 4, kLaneCols = 8;
+template <int D>
 __device__ __forceinline__ int piece(int row, int c) {
-  constexpr int kShift = CW == 16 ? 4 : 3;
-  static_assert(CW == 16 || CW == 8, "64 or 32 columns a tile");
-  return D == 32 ? row * 4 + (c ^ ((row >> kShift) & 3)) : row * 8 + (c ^ ((row & 1) | ((row >> (kShift - 1)) & 6)));
+  return D == 32 ? row * 4 + (c ^ ((row >> 3) & 3)) : row * 8 + (c ^ ((row & 1) | ((row >> 2) & 6)));
 }
 
 // rows [r0, r0 + n_valid) of a [tokens][heads][D] tensor, head h; rows past n_valid are filled with zeros
-template <int D, int CW, int ROWS, int NT>
+template <int D, int ROWS, int NT>
 __device__ __forceinline__ void load_tile(uint4* dst, const uint16_t* src, int r0, int n_valid, int heads, int h,
                                           int tid) {
   constexpr int kPieces = D / 8;
@@ -166,7 +165,7 @@ __device__ __forceinline__ void load_tile(uint4* dst, const uint16_t* src, int r
   for (int i = tid; i < ROWS * kPieces; i += NT) {
     const int r = i / kPieces, c = i % kPieces;
     const bool ok = r < n_valid;
-    cp_async16(dst + piece<D, CW>(r, c), src + ((size_t)(r0 + (ok ? r : 0)) * heads + h) * D + c * 8, ok);
+    cp_async16(dst + piece<D>(r, c), src + ((size_t)(r0 + (ok ? r : 0)) * heads + h) * D + c * 8, ok);
   }
 }
 __device__ __forceinline__ void cp_async4(void* smem, const void* gmem, bool pred) {
@@ -175,20 +174,20 @@ __device__ __forceinline__ void cp_async4(void* smem, const void* gmem, bool pre
 }
 
 // B operand for X Y^T: column group n (8 columns) by all of D (k): b[2 * ks], b[2 * ks + 1] per k step
-template <int D, int CW>
+template <int D>
 __device__ __forceinline__ void load_b_rows(uint32_t* b, const uint4* tile, int row0, int n, int lane) {
-  const int row = row0 + ((lane & 7) >> 1) * CW + 2 * n + (lane & 1);
+  const int row = row0 + ((lane & 7) >> 1) * kLaneCols + 2 * n + (lane & 1);
 #pragma unroll
   for (int c = 0; c < D / 8; c += 4) {
-    const uint32_t a = smem_u32(tile + piece<D, CW>(row, c + (lane >> 3)));
+    const uint32_t a = smem_u32(tile + piece<D>(row, c + (lane >> 3)));
     ldmatrix_x4(b[c], b[c + 1], b[c + 2], b[c + 3], a);
   }
 }
 // B operand for P Y: column groups 2 j and 2 j + 1 (16 rows of Y, k) by columns [8 c, 8 c + 16) of Y
-template <int D, int CW>
+template <int D>
 __device__ __forceinline__ void load_b_cols(uint32_t* b, const uint4* tile, int row0, int j, int c, int lane) {
-  const int row = row0 + ((lane & 7) >> 1) * CW + 2 * (2 * j + ((lane >> 3) & 1)) + (lane & 1);
-  ldmatrix_x4_trans(b[0], b[1], b[2], b[3], smem_u32(tile + piece<D, CW>(row, c + (lane >> 4))));
+  const int row = row0 + ((lane & 7) >> 1) * kLaneCols + 2 * (2 * j + ((lane >> 3) & 1)) + (lane & 1);
+  ldmatrix_x4_trans(b[0], b[1], b[2], b[3], smem_u32(tile + piece<D>(row, c + (lane >> 4))));
 }
 // A operand straight from global memory: rows g and g + 8 of a 16-row tile; row pointers may be null
 template <int D>
@@ -214,32 +213,33 @@ __device__ __forceinline__ float quad_max(float v) {
 }
 
 // ---- what a tile's distances have in common ----
-// Per axis, for a warp's tile of 32 or 64 columns whose column positions are xs[col * NA]:
+// Per axis, for a warp's tile of 32 columns whose column positions are xs[col * NA]:
 //   kOne   every (row, column) pair has one clamped distance (all pairs at or past +-maxd, or single
 //          positions): one look-up for the tile;
-//   kLane  each lane's CW columns have one position: one look-up per row;
+//   kLane  each lane's columns have one position: one look-up per row;
 //   kFour  aligned runs of four columns have one position: one look-up per row and run;
+//   kTurn  the same four positions in every run: four look-ups per row;
 //   kEach  a look-up per pair (following arbitrary runs with a branch per column measured 10-20% slower
 //          on every training case: the branches cost more than the look-ups they save).
-// Lattice orders (bricks, patches, frames) make the slow axes kLane or kFour; distances past
-// max_distance make kOne.  The tests cost about 20 instructions a tile and axis.
-enum : int { kOne = 0, kLane = 1, kFour = 2, kEach = 3 };
+// Lattice orders (bricks, patches, frames) make the slow axes kLane or kFour, bricks of four the fast one
+// kTurn; distances past max_distance make kOne.  The tests cost about 20 instructions a tile and axis.
+enum : int { kOne = 0, kLane = 1, kFour = 2, kTurn = 3, kEach = 4 };
 
-template <int NA, int COLS>
+template <int NA>
 __device__ __forceinline__ int axis_mode(const int* xs, int row_lo, int row_hi, bool rows_are_keys, int maxd, int lane,
                                          int& one, uint32_t* status) {
-  constexpr int CW = COLS / 4;
-  const int x0 = xs[lane * NA], x1 = COLS == 64 ? xs[(lane + 32) * NA] : x0;
-  const int lo = __reduce_min_sync(0xffffffffu, min(x0, x1)), hi = __reduce_max_sync(0xffffffffu, max(x0, x1));
+  const int x = xs[lane * NA];
+  const int lo = __reduce_min_sync(0xffffffffu, x), hi = __reduce_max_sync(0xffffffffu, x);
   if (lo < -kPosLimit || hi > kPosLimit) raise_status(status, LSRM_ERR_BOUNDS);
   const int a = clamp_index(rows_are_keys ? row_lo - hi : lo - row_hi, maxd, 2 * maxd);
   const int b = clamp_index(rows_are_keys ? row_hi - lo : hi - row_lo, maxd, 2 * maxd);
   one = a;
   if (a == b) return kOne;
-  uint32_t same = __ballot_sync(0xffffffffu, x0 == __shfl_down_sync(0xffffffffu, x0, 1));
-  if (COLS == 64) same &= __ballot_sync(0xffffffffu, x1 == __shfl_down_sync(0xffffffffu, x1, 1));
-  constexpr uint32_t kLaneMask = CW == 16 ? 0x7fff7fffu : 0x7f7f7f7fu, kFourMask = 0x77777777u;
-  return (same & kLaneMask) == kLaneMask ? kLane : (same & kFourMask) == kFourMask ? kFour : kEach;
+  const uint32_t same = __ballot_sync(0xffffffffu, x == __shfl_down_sync(0xffffffffu, x, 1));
+  if ((same & 0x7f7f7f7fu) == 0x7f7f7f7fu) return kLane;
+  if ((same & 0x77777777u) == 0x77777777u) return kFour;
+  const uint32_t turn = __ballot_sync(0xffffffffu, x == __shfl_down_sync(0xffffffffu, x, 4));
+  return (turn & 0x0f0f0f0fu) == 0x0f0f0f0fu ? kTurn : kEach;
 }
 
 // The bias table of one head in shared memory, and whether it may fold: in log2 units (true) when every
@@ -268,16 +268,15 @@ __device__ __forceinline__ bool fill_units(const Params& p, float* lut, int h, i
   return fold;
 }
 
-// The bias of a lane's MT x 2 rows by CW columns, in the table's units.  What is constant per row goes
+// The bias of a lane's MT x 2 rows by 8 columns, in the table's units.  What is constant per row goes
 // to base; when that is all and the table folds, returns true and leaves the scores raw.  Otherwise the
 // scores become s * mul + bias.  SIGN: column positions count up (+1, columns are keys: rowc = maxd - pos_q)
 // or down (-1, columns are queries: rowc = maxd + pos_k).
-template <int NA, int MT, int NT, int SIGN>
-__device__ __forceinline__ bool add_bias(float (&s)[MT][NT][4], float (&base)[MT][2], const int (&mode)[NA],
+template <int NA, int MT, int SIGN>
+__device__ __forceinline__ bool add_bias(float (&s)[MT][kGroups][4], float (&base)[MT][2], const int (&mode)[NA],
                                          const int (&one)[NA], const int* xs, const float* lut, int top,
                                          const int (&rowc)[MT][2][NA], float mul, bool fold, int tq) {
-  constexpr int CW = 2 * NT;
-  const int* mine = xs + tq * CW * NA;
+  const int* mine = xs + tq * kLaneCols * NA;
   int worst = kOne;
   float ub = 0.0f;
 #pragma unroll
@@ -303,14 +302,14 @@ __device__ __forceinline__ bool add_bias(float (&s)[MT][NT][4], float (&base)[MT
 #pragma unroll
     for (int i = 0; i < 2; ++i)
 #pragma unroll
-      for (int n = 0; n < NT; ++n)
+      for (int n = 0; n < kGroups; ++n)
         ffma2(s[mt][n][2 * i], s[mt][n][2 * i + 1], s[mt][n][2 * i], s[mt][n][2 * i + 1], mul, base[mt][i]);
 #pragma unroll
   for (int a = 0; a < NA; ++a) {
     const float* la = lut + a * (top + 1);
     if (mode[a] == kFour) {
 #pragma unroll
-      for (int r = 0; r < NT / 2; ++r) {
+      for (int r = 0; r < 2; ++r) {
         const int x = SIGN * mine[4 * r * NA + a];
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt)
@@ -321,9 +320,22 @@ __device__ __forceinline__ bool add_bias(float (&s)[MT][NT][4], float (&base)[MT
             s[mt][2 * r + 1][2 * i] += b, s[mt][2 * r + 1][2 * i + 1] += b;
           }
       }
+    } else if (mode[a] == kTurn) {
+#pragma unroll
+      for (int n = 0; n < 2; ++n) {
+        const int x0 = SIGN * mine[2 * n * NA + a], x1 = SIGN * mine[(2 * n + 1) * NA + a];
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const float b0 = la[clamp_index(x0, rowc[mt][i][a], top)], b1 = la[clamp_index(x1, rowc[mt][i][a], top)];
+            s[mt][n][2 * i] += b0, s[mt][n][2 * i + 1] += b1;
+            s[mt][n + 2][2 * i] += b0, s[mt][n + 2][2 * i + 1] += b1;
+          }
+      }
     } else if (mode[a] == kEach) {
 #pragma unroll
-      for (int n = 0; n < NT; ++n) {
+      for (int n = 0; n < kGroups; ++n) {
         const int x0 = SIGN * mine[2 * n * NA + a], x1 = SIGN * mine[(2 * n + 1) * NA + a];
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt)

@@ -30,7 +30,6 @@ namespace lsrm {
 namespace rp {
 
 constexpr int kBThreads = 128, kBChunk = 64, kBStages = 3, kKeyStages = 2;
-constexpr int kBNT = 4, kBCW = 8, kBCols = 32;  // columns of a score tile
 
 template <int D, int NA>
 struct BwdCfg {
@@ -98,8 +97,8 @@ __global__ void __launch_bounds__(kBThreads, D == 32 ? 3 : 2) rp_dq_kernel(const
   auto load = [&](int c) {
     if (c < chunks) {
       const int st = c % kBStages, k0 = klo + c * kBChunk, n = min(kBChunk, khi - k0);
-      load_tile<D, kBCW, kBChunk, kBThreads>(ks + st * C::kTile, p.k, k0, n, p.Hkv, hk, tid);
-      load_tile<D, kBCW, kBChunk, kBThreads>(vs + st * C::kTile, p.v, k0, n, p.Hkv, hk, tid);
+      load_tile<D, kBChunk, kBThreads>(ks + st * C::kTile, p.k, k0, n, p.Hkv, hk, tid);
+      load_tile<D, kBChunk, kBThreads>(vs + st * C::kTile, p.v, k0, n, p.Hkv, hk, tid);
       for (int i = tid; i < kBChunk * NA; i += kBThreads)
         cp_async4(ps + st * kBChunk * NA + i, p.pos_k + (size_t)(k0 + min(i / NA, n - 1)) * NA + i % NA, true);
     }
@@ -197,15 +196,15 @@ __global__ void __launch_bounds__(kBThreads, D == 32 ? 3 : 2) rp_dq_kernel(const
     const uint4* kt = ks + (c % kBStages) * C::kTile;
     const uint4* vt = vs + (c % kBStages) * C::kTile;
 #pragma unroll 1
-    for (int kb = 0; kb < kBChunk; kb += kBCols) {
+    for (int kb = 0; kb < kBChunk; kb += kCols) {
       const int left = nk - c * kBChunk - kb;
       if (left <= 0 || wrow >= qhi) break;
       const int* pt = ps + (c % kBStages) * kBChunk * NA + kb * NA;
-      float s[MT][kBNT][4], dp[MT][kBNT][4];
+      float s[MT][kGroups][4], dp[MT][kGroups][4];
 #pragma unroll
-      for (int n = 0; n < kBNT; ++n) {
+      for (int n = 0; n < kGroups; ++n) {
         uint32_t b[D / 8];
-        load_b_rows<D, kBCW>(b, kt, kb, n, lane);
+        load_b_rows<D>(b, kt, kb, n, lane);
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt) {
 #pragma unroll
@@ -213,7 +212,7 @@ __global__ void __launch_bounds__(kBThreads, D == 32 ? 3 : 2) rp_dq_kernel(const
 #pragma unroll
           for (int d = 0; d < D / 16; ++d) mma16816(s[mt][n], qa[mt][d], b + 2 * d);
         }
-        load_b_rows<D, kBCW>(b, vt, kb, n, lane);
+        load_b_rows<D>(b, vt, kb, n, lane);
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
@@ -222,16 +221,16 @@ __global__ void __launch_bounds__(kBThreads, D == 32 ? 3 : 2) rp_dq_kernel(const
       int mode[NA], one[NA];
 #pragma unroll
       for (int a = 0; a < NA; ++a)
-        mode[a] = axis_mode<NA, kBCols>(pt + a, q_lo[a], q_hi[a], false, p.maxd, lane, one[a], p.status);
+        mode[a] = axis_mode<NA>(pt + a, q_lo[a], q_hi[a], false, p.maxd, lane, one[a], p.status);
       float base[MT][2];
-      const bool fold = add_bias<NA, MT, kBNT, 1>(s, base, mode, one, pt, lut, top, qp, mul, small, tq);
-      if (left < kBCols) {
+      const bool fold = add_bias<NA, MT, 1>(s, base, mode, one, pt, lut, top, qp, mul, small, tq);
+      if (left < kCols) {
         keep_branch();
 #pragma unroll
-        for (int n = 0; n < kBNT; ++n)
+        for (int n = 0; n < kGroups; ++n)
 #pragma unroll
           for (int e = 0; e < 2; ++e)
-            if (tq * kBCW + 2 * n + e >= left)
+            if (tq * kLaneCols + 2 * n + e >= left)
 #pragma unroll
               for (int mt = 0; mt < MT; ++mt) s[mt][n][e] = s[mt][n][2 + e] = -INFINITY;
       }
@@ -243,7 +242,7 @@ __global__ void __launch_bounds__(kBThreads, D == 32 ? 3 : 2) rp_dq_kernel(const
           const float cst = base[mt][i] - row[mt][i];
           float sum0 = 0.0f, sum1 = 0.0f;
 #pragma unroll
-          for (int n = 0; n < kBNT; ++n) {
+          for (int n = 0; n < kGroups; ++n) {
             float p0 = s[mt][n][2 * i], p1 = s[mt][n][2 * i + 1];
             if (fold) {
               ffma2(p0, p1, p0, p1, mul, cst);
@@ -267,7 +266,7 @@ __global__ void __launch_bounds__(kBThreads, D == 32 ? 3 : 2) rp_dq_kernel(const
 #pragma unroll
         for (int dc = 0; dc < D / 8; dc += 2) {
           uint32_t b[4];
-          load_b_cols<D, kBCW>(b, kt, kb, j, dc, lane);
+          load_b_cols<D>(b, kt, kb, j, dc, lane);
 #pragma unroll
           for (int mt = 0; mt < MT; ++mt) {
             mma16816(dq[mt][dc], sa[mt][j], b);
@@ -351,8 +350,8 @@ __global__ void __launch_bounds__(kBThreads, D == 32 ? 4 : 2) rp_dkv_kernel(cons
     if (it < steps) {
       const int h = hk * p.G + h0 + it / nc, q0 = qlo + (c0 + it % nc) * kBChunk, n = min(kBChunk, qhi - q0);
       const int st = it % kKeyStages;
-      load_tile<D, kBCW, kBChunk, kBThreads>(qs + st * C::kTile, p.q, q0, n, p.Hq, h, tid);
-      load_tile<D, kBCW, kBChunk, kBThreads>(ds + st * C::kTile, p.dout, q0, n, p.Hq, h, tid);
+      load_tile<D, kBChunk, kBThreads>(qs + st * C::kTile, p.q, q0, n, p.Hq, h, tid);
+      load_tile<D, kBChunk, kBThreads>(ds + st * C::kTile, p.dout, q0, n, p.Hq, h, tid);
       for (int i = tid; i < kBChunk * NA; i += kBThreads)
         cp_async4(ps + st * kBChunk * NA + i, p.pos_q + (size_t)(q0 + min(i / NA, n - 1)) * NA + i % NA, true);
       static_assert(kBThreads == 2 * kBChunk, "one row constant a thread");
@@ -435,16 +434,16 @@ __global__ void __launch_bounds__(kBThreads, D == 32 ? 4 : 2) rp_dkv_kernel(cons
     const uint4* qt = qs + st * C::kTile;
     const uint4* dt = ds + st * C::kTile;
 #pragma unroll 1
-    for (int qb = 0; qb < kBChunk; qb += kBCols) {
+    for (int qb = 0; qb < kBChunk; qb += kCols) {
       const int left = nq - (c0 + cc) * kBChunk - qb;
       if (left <= 0 || wrow >= khi) break;
       const int* pt = ps + st * kBChunk * NA + qb * NA;
-      const float* lt = ls + st * 2 * kBChunk + qb + tq * kBCW;
-      float s[MT][kBNT][4], dp[MT][kBNT][4];
+      const float* lt = ls + st * 2 * kBChunk + qb + tq * kLaneCols;
+      float s[MT][kGroups][4], dp[MT][kGroups][4];
 #pragma unroll
-      for (int n = 0; n < kBNT; ++n) {
+      for (int n = 0; n < kGroups; ++n) {
         uint32_t b[D / 8];
-        load_b_rows<D, kBCW>(b, qt, qb, n, lane);
+        load_b_rows<D>(b, qt, qb, n, lane);
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt) {
 #pragma unroll
@@ -452,7 +451,7 @@ __global__ void __launch_bounds__(kBThreads, D == 32 ? 4 : 2) rp_dkv_kernel(cons
 #pragma unroll
           for (int d = 0; d < D / 16; ++d) mma16816(s[mt][n], ka[mt][d], b + 2 * d);
         }
-        load_b_rows<D, kBCW>(b, dt, qb, n, lane);
+        load_b_rows<D>(b, dt, qb, n, lane);
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
@@ -461,21 +460,21 @@ __global__ void __launch_bounds__(kBThreads, D == 32 ? 4 : 2) rp_dkv_kernel(cons
       int mode[NA], one[NA];
 #pragma unroll
       for (int a = 0; a < NA; ++a)
-        mode[a] = axis_mode<NA, kBCols>(pt + a, k_lo[a], k_hi[a], true, p.maxd, lane, one[a], p.status);
+        mode[a] = axis_mode<NA>(pt + a, k_lo[a], k_hi[a], true, p.maxd, lane, one[a], p.status);
       float base[MT][2];
-      const bool fold = add_bias<NA, MT, kBNT, -1>(s, base, mode, one, pt, lut, top, kp, mul, small, tq);
+      const bool fold = add_bias<NA, MT, -1>(s, base, mode, one, pt, lut, top, kp, mul, small, tq);
       bool flat = true;  // one bias for the tile
 #pragma unroll
       for (int a = 0; a < NA; ++a) flat = flat && mode[a] == kOne;
       // s becomes dS^T, dp becomes P^T
 #pragma unroll
-      for (int n = 0; n < kBNT; ++n) {
+      for (int n = 0; n < kGroups; ++n) {
         float2 l = *reinterpret_cast<const float2*>(lt + 2 * n);
         const float2 dl = *reinterpret_cast<const float2*>(lt + kBChunk + 2 * n);
-        if (left < kBCols) {  // no query: P = 0
+        if (left < kCols) {  // no query: P = 0
           keep_branch();
-          if (tq * kBCW + 2 * n >= left) l.x = INFINITY;
-          if (tq * kBCW + 2 * n + 1 >= left) l.y = INFINITY;
+          if (tq * kLaneCols + 2 * n >= left) l.x = INFINITY;
+          if (tq * kLaneCols + 2 * n + 1 >= left) l.y = INFINITY;
         }
         if (small) {
           if (fold) {
@@ -500,8 +499,8 @@ __global__ void __launch_bounds__(kBThreads, D == 32 ? 4 : 2) rp_dkv_kernel(cons
           float ln[2], cr[2];
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            const bool there = tq * kBCW + 2 * n + e < left;
-            const size_t at = (size_t)(qlo + (c0 + cc) * kBChunk + qb + (there ? tq * kBCW + 2 * n + e : 0)) * p.Hq +
+            const bool there = tq * kLaneCols + 2 * n + e < left;
+            const size_t at = (size_t)(qlo + (c0 + cc) * kBChunk + qb + (there ? tq * kLaneCols + 2 * n + e : 0)) * p.Hq +
                               hk * p.G + head;
             ln[e] = there ? p.lse_in[at] : INFINITY;
             if (ln[e] == -INFINITY) ln[e] = INFINITY;
@@ -535,7 +534,7 @@ __global__ void __launch_bounds__(kBThreads, D == 32 ? 4 : 2) rp_dkv_kernel(cons
           for (int i = 0; i < 2; ++i)
             if (wrow + mt * 16 + g + 8 * i >= khi)
 #pragma unroll
-              for (int n = 0; n < kBNT; ++n) s[mt][n][2 * i] = s[mt][n][2 * i + 1] = 0.0f;
+              for (int n = 0; n < kGroups; ++n) s[mt][n][2 * i] = s[mt][n][2 * i + 1] = 0.0f;
       }
       // the table's gradient
 #pragma unroll
@@ -552,14 +551,14 @@ __global__ void __launch_bounds__(kBThreads, D == 32 ? 4 : 2) rp_dkv_kernel(cons
 #pragma unroll
           for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-            for (int n = 0; n < kBNT; ++n) {
+            for (int n = 0; n < kGroups; ++n) {
               fadd2_acc(sum0, sum1, s[mt][n][0], s[mt][n][1]);
               fadd2_acc(sum0, sum1, s[mt][n][2], s[mt][n][3]);
             }
           run[a] += sum0 + sum1;
         } else if (mode[a] <= kFour) {
           // runs of eight or four queries on one position
-          const int x0 = -pt[tq * kBCW * NA + a], x1 = -pt[(tq * kBCW + 4) * NA + a];
+          const int x0 = -pt[tq * kLaneCols * NA + a], x1 = -pt[(tq * kLaneCols + 4) * NA + a];
 #pragma unroll
           for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
@@ -568,10 +567,21 @@ __global__ void __launch_bounds__(kBThreads, D == 32 ? 4 : 2) rp_dkv_kernel(cons
                       (s[mt][0][2 * i] + s[mt][0][2 * i + 1]) + (s[mt][1][2 * i] + s[mt][1][2 * i + 1]),
                       boff[clamp_index(x1, kp[mt][i][a], top)],
                       (s[mt][2][2 * i] + s[mt][2][2 * i + 1]) + (s[mt][3][2 * i] + s[mt][3][2 * i + 1]));
+        } else if (mode[a] == kTurn) {
+#pragma unroll
+          for (int n = 0; n < 2; ++n) {
+            const int x0 = -pt[(tq * kLaneCols + 2 * n) * NA + a], x1 = -pt[(tq * kLaneCols + 2 * n + 1) * NA + a];
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+              for (int i = 0; i < 2; ++i)
+                add_two(ca, boff[clamp_index(x0, kp[mt][i][a], top)], s[mt][n][2 * i] + s[mt][n + 2][2 * i],
+                        boff[clamp_index(x1, kp[mt][i][a], top)], s[mt][n][2 * i + 1] + s[mt][n + 2][2 * i + 1]);
+          }
         } else {
 #pragma unroll
-          for (int n = 0; n < kBNT; ++n) {
-            const int x0 = -pt[(tq * kBCW + 2 * n) * NA + a], x1 = -pt[(tq * kBCW + 2 * n + 1) * NA + a];
+          for (int n = 0; n < kGroups; ++n) {
+            const int x0 = -pt[(tq * kLaneCols + 2 * n) * NA + a], x1 = -pt[(tq * kLaneCols + 2 * n + 1) * NA + a];
 #pragma unroll
             for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
@@ -585,7 +595,7 @@ __global__ void __launch_bounds__(kBThreads, D == 32 ? 4 : 2) rp_dkv_kernel(cons
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-        for (int n = 0; n < kBNT; ++n)
+        for (int n = 0; n < kGroups; ++n)
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
             sa[mt][n >> 1][(n & 1) * 2 + i] = pack2(s[mt][n][2 * i], s[mt][n][2 * i + 1]);
@@ -596,13 +606,13 @@ __global__ void __launch_bounds__(kBThreads, D == 32 ? 4 : 2) rp_dkv_kernel(cons
 #pragma unroll
         for (int dc = 0; dc < D / 8; dc += 2) {
           uint32_t b[4];
-          load_b_cols<D, kBCW>(b, qt, qb, j, dc, lane);
+          load_b_cols<D>(b, qt, qb, j, dc, lane);
 #pragma unroll
           for (int mt = 0; mt < MT; ++mt) {
             mma16816(dk[mt][dc], sa[mt][j], b);
             mma16816(dk[mt][dc + 1], sa[mt][j], b + 2);
           }
-          load_b_cols<D, kBCW>(b, dt, qb, j, dc, lane);
+          load_b_cols<D>(b, dt, qb, j, dc, lane);
 #pragma unroll
           for (int mt = 0; mt < MT; ++mt) {
             mma16816(dv[mt][dc], pa[mt][j], b);

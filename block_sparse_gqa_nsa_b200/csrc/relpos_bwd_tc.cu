@@ -775,6 +775,12 @@ __global__ void __launch_bounds__(kTcThreads, CTAS)
                            (x[4 * f] + x[4 * f + 1]) + (x[4 * f + 2] + x[4 * f + 3]),
                            boff[clamp_index(xs[f + 1].x, rowc[a], top)],
                            (x[4 * f + 4] + x[4 * f + 5]) + (x[4 * f + 6] + x[4 * f + 7]));
+            } else if (kHasTurn<NA> && md == kTurn) {
+              const int4 u = xs[0];
+              add_two_tc(to, boff[clamp_index(u.x, rowc[a], top)], (x[0] + x[4]) + (x[8] + x[12]),
+                         boff[clamp_index(u.y, rowc[a], top)], (x[1] + x[5]) + (x[9] + x[13]));
+              add_two_tc(to, boff[clamp_index(u.z, rowc[a], top)], (x[2] + x[6]) + (x[10] + x[14]),
+                         boff[clamp_index(u.w, rowc[a], top)], (x[3] + x[7]) + (x[11] + x[15]));
             } else {
 #pragma unroll
               for (int f = 0; f < 4; ++f) {

@@ -13,7 +13,6 @@ namespace lsrm {
 namespace rp {
 
 constexpr int kShWarps = 8, kShThreads = 32 * kShWarps, kShKeys = 64;
-constexpr int kShNT = 4, kShCW = 8, kShCols = 32;  // columns of a score tile
 constexpr float kShSlack = 8.0f;
 
 template <int D, int NA>
@@ -139,8 +138,8 @@ __global__ void __launch_bounds__(kShThreads, 2) rp_short_fwd_kernel(const Param
   auto load = [&](int i) {
     if (i < loads) {
       const int st = i & 1, k0 = P.klo + i % blocks * kShKeys, n = min(kShKeys, P.khi - k0);
-      load_tile<D, kShCW, kShKeys, kShThreads>(ring + st * 2 * C::kTile, p.k, k0, n, p.Hkv, P.hk, tid);
-      load_tile<D, kShCW, kShKeys, kShThreads>(ring + (st * 2 + 1) * C::kTile, p.v, k0, n, p.Hkv, P.hk, tid);
+      load_tile<D, kShKeys, kShThreads>(ring + st * 2 * C::kTile, p.k, k0, n, p.Hkv, P.hk, tid);
+      load_tile<D, kShKeys, kShThreads>(ring + (st * 2 + 1) * C::kTile, p.v, k0, n, p.Hkv, P.hk, tid);
       for (int j = tid; j < kShKeys * NA; j += kShThreads)
         cp_async4(ps + st * kShKeys * NA + j, p.pos_k + (size_t)(k0 + min(j / NA, n - 1)) * NA + j % NA, true);
     }
@@ -183,15 +182,15 @@ __global__ void __launch_bounds__(kShThreads, 2) rp_short_fwd_kernel(const Param
       const uint4* vt = kt + C::kTile;
       const int* pt0 = ps + (i & 1) * kShKeys * NA;
 #pragma unroll 1
-      for (int kb = 0; kb < kShKeys; kb += kShCols) {
+      for (int kb = 0; kb < kShKeys; kb += kCols) {
         const int left = nk - blk * kShKeys - kb;
         if (left <= 0) break;
         const int* pt = pt0 + kb * NA;
-        float s[1][kShNT][4];
+        float s[1][kGroups][4];
 #pragma unroll
-        for (int n = 0; n < kShNT; ++n) {
+        for (int n = 0; n < kGroups; ++n) {
           uint32_t b[D / 8];
-          load_b_rows<D, kShCW>(b, kt, kb, n, lane);
+          load_b_rows<D>(b, kt, kb, n, lane);
 #pragma unroll
           for (int e = 0; e < 4; ++e) s[0][n][e] = 0.0f;
 #pragma unroll
@@ -200,16 +199,16 @@ __global__ void __launch_bounds__(kShThreads, 2) rp_short_fwd_kernel(const Param
         int mode[NA], one[NA];
 #pragma unroll
         for (int a = 0; a < NA; ++a)
-          mode[a] = axis_mode<NA, kShCols>(pt + a, q_lo[a], q_hi[a], false, p.maxd, lane, one[a], p.status);
+          mode[a] = axis_mode<NA>(pt + a, q_lo[a], q_hi[a], false, p.maxd, lane, one[a], p.status);
         float base[1][2];
-        const bool fold = add_bias<NA, 1, kShNT, 1>(s, base, mode, one, pt, mine, top, rowc, mul, small, tq);
-        if (left < kShCols) {
+        const bool fold = add_bias<NA, 1, 1>(s, base, mode, one, pt, mine, top, rowc, mul, small, tq);
+        if (left < kCols) {
           keep_branch();
 #pragma unroll
-          for (int n = 0; n < kShNT; ++n)
+          for (int n = 0; n < kGroups; ++n)
 #pragma unroll
             for (int e = 0; e < 2; ++e)
-              if (tq * kShCW + 2 * n + e >= left) s[0][n][e] = s[0][n][2 + e] = -INFINITY;
+              if (tq * kLaneCols + 2 * n + e >= left) s[0][n][e] = s[0][n][2 + e] = -INFINITY;
         }
         float mx[2];
         bool need = false;
@@ -217,7 +216,7 @@ __global__ void __launch_bounds__(kShThreads, 2) rp_short_fwd_kernel(const Param
         for (int k = 0; k < 2; ++k) {
           float x = fmaxf(s[0][0][2 * k], s[0][0][2 * k + 1]);
 #pragma unroll
-          for (int n = 1; n < kShNT; ++n) x = fmax3(x, s[0][n][2 * k], s[0][n][2 * k + 1]);
+          for (int n = 1; n < kGroups; ++n) x = fmax3(x, s[0][n][2 * k], s[0][n][2 * k + 1]);
           mx[k] = fold ? fmaf(x, mul, base[0][k]) : x;
           need = need || mx[k] > m[k] + kShSlack;
         }
@@ -238,7 +237,7 @@ __global__ void __launch_bounds__(kShThreads, 2) rp_short_fwd_kernel(const Param
           const float ref = m[k] == -INFINITY ? 0.0f : m[k], cst = base[0][k] - ref;
           float s0 = 0.0f, s1 = 0.0f;
 #pragma unroll
-          for (int n = 0; n < kShNT; ++n) {
+          for (int n = 0; n < kGroups; ++n) {
             float p0 = s[0][n][2 * k], p1 = s[0][n][2 * k + 1];
             if (fold) {
               ffma2(p0, p1, p0, p1, mul, cst);
@@ -258,7 +257,7 @@ __global__ void __launch_bounds__(kShThreads, 2) rp_short_fwd_kernel(const Param
 #pragma unroll
           for (int dc = 0; dc < D / 8; dc += 2) {
             uint32_t b[4];
-            load_b_cols<D, kShCW>(b, vt, kb, j, dc, lane);
+            load_b_cols<D>(b, vt, kb, j, dc, lane);
             mma16816(o[dc], pa[j], b);
             mma16816(o[dc + 1], pa[j], b + 2);
           }
@@ -335,8 +334,8 @@ __global__ void __launch_bounds__(kShThreads, D == 32 ? 2 : 1) rp_short_dq_kerne
   auto load = [&](int i) {
     if (i < loads) {
       const int st = i & 1, k0 = P.klo + i % blocks * kShKeys, n = min(kShKeys, P.khi - k0);
-      load_tile<D, kShCW, kShKeys, kShThreads>(ring + st * 2 * C::kTile, p.k, k0, n, p.Hkv, P.hk, tid);
-      load_tile<D, kShCW, kShKeys, kShThreads>(ring + (st * 2 + 1) * C::kTile, p.v, k0, n, p.Hkv, P.hk, tid);
+      load_tile<D, kShKeys, kShThreads>(ring + st * 2 * C::kTile, p.k, k0, n, p.Hkv, P.hk, tid);
+      load_tile<D, kShKeys, kShThreads>(ring + (st * 2 + 1) * C::kTile, p.v, k0, n, p.Hkv, P.hk, tid);
       for (int j = tid; j < kShKeys * NA; j += kShThreads)
         cp_async4(ps + st * kShKeys * NA + j, p.pos_k + (size_t)(k0 + min(j / NA, n - 1)) * NA + j % NA, true);
     }
@@ -425,36 +424,36 @@ __global__ void __launch_bounds__(kShThreads, D == 32 ? 2 : 1) rp_short_dq_kerne
       const uint4* vt = kt + C::kTile;
       const int* pt0 = ps + (i & 1) * kShKeys * NA;
 #pragma unroll 1
-      for (int kb = 0; kb < kShKeys; kb += kShCols) {
+      for (int kb = 0; kb < kShKeys; kb += kCols) {
         const int left = nk - blk * kShKeys - kb;
         if (left <= 0) break;
         const int* pt = pt0 + kb * NA;
-        float s[1][kShNT][4], dp[kShNT][4];
+        float s[1][kGroups][4], dp[kGroups][4];
 #pragma unroll
-        for (int n = 0; n < kShNT; ++n) {
+        for (int n = 0; n < kGroups; ++n) {
           uint32_t b[D / 8];
-          load_b_rows<D, kShCW>(b, kt, kb, n, lane);
+          load_b_rows<D>(b, kt, kb, n, lane);
 #pragma unroll
           for (int e = 0; e < 4; ++e) s[0][n][e] = dp[n][e] = 0.0f;
 #pragma unroll
           for (int d = 0; d < D / 16; ++d) mma16816(s[0][n], qa[d], b + 2 * d);
-          load_b_rows<D, kShCW>(b, vt, kb, n, lane);
+          load_b_rows<D>(b, vt, kb, n, lane);
 #pragma unroll
           for (int d = 0; d < D / 16; ++d) mma16816(dp[n], da[d], b + 2 * d);
         }
         int mode[NA], one[NA];
 #pragma unroll
         for (int a = 0; a < NA; ++a)
-          mode[a] = axis_mode<NA, kShCols>(pt + a, q_lo[a], q_hi[a], false, p.maxd, lane, one[a], p.status);
+          mode[a] = axis_mode<NA>(pt + a, q_lo[a], q_hi[a], false, p.maxd, lane, one[a], p.status);
         float base[1][2];
-        const bool fold = add_bias<NA, 1, kShNT, 1>(s, base, mode, one, pt, mine, top, rowc, mul, small, tq);
-        if (left < kShCols) {
+        const bool fold = add_bias<NA, 1, 1>(s, base, mode, one, pt, mine, top, rowc, mul, small, tq);
+        if (left < kCols) {
           keep_branch();
 #pragma unroll
-          for (int n = 0; n < kShNT; ++n)
+          for (int n = 0; n < kGroups; ++n)
 #pragma unroll
             for (int e = 0; e < 2; ++e)
-              if (tq * kShCW + 2 * n + e >= left) s[0][n][e] = s[0][n][2 + e] = -INFINITY;
+              if (tq * kLaneCols + 2 * n + e >= left) s[0][n][e] = s[0][n][2 + e] = -INFINITY;
         }
         uint32_t sa[2][4], pa[2][4];
 #pragma unroll
@@ -462,7 +461,7 @@ __global__ void __launch_bounds__(kShThreads, D == 32 ? 2 : 1) rp_short_dq_kerne
           const float cst = base[0][k] - row[k];
           float s0 = 0.0f, s1 = 0.0f;
 #pragma unroll
-          for (int n = 0; n < kShNT; ++n) {
+          for (int n = 0; n < kGroups; ++n) {
             float p0 = s[0][n][2 * k], p1 = s[0][n][2 * k + 1];
             if (fold) {
               ffma2(p0, p1, p0, p1, mul, cst);
@@ -486,7 +485,7 @@ __global__ void __launch_bounds__(kShThreads, D == 32 ? 2 : 1) rp_short_dq_kerne
 #pragma unroll
           for (int dc = 0; dc < D / 8; dc += 2) {
             uint32_t b[4];
-            load_b_cols<D, kShCW>(b, kt, kb, j, dc, lane);
+            load_b_cols<D>(b, kt, kb, j, dc, lane);
             mma16816(dq[dc], sa[j], b);
             mma16816(dq[dc + 1], sa[j], b + 2);
             mma16816(pk[dc], pa[j], b);

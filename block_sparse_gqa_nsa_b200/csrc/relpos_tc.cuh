@@ -82,8 +82,13 @@ __device__ __forceinline__ void copy_tail(uint8_t* dst, const uint16_t* src, int
 }
 __device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory"); }
 
-// what a chunk's column positions have in common on each axis: their range, and in bits 2 g, 2 g + 1 of
-// runs kLane, kFour or kEach: columns 16 g .. 16 g + 15 have one position, one per aligned run of four, any
+// kTurn is for positions on three axes (volumes, in bricks: forward of 4096 tokens, 32 heads of 32, 453 -> 430 us);
+// with two, the further branch costs frames by rows more than it can save (8 of 1370 patches 267 -> 291 us)
+template <int NA>
+constexpr bool kHasTurn = NA == 3;
+// what a chunk's column positions have in common on each axis: their range, and in byte g of runs kLane,
+// kFour, kTurn or kEach: columns 16 g .. 16 g + 15 have one position, one per aligned run of four, the same
+// four in every such run, any
 struct ChunkMeta {
   int lo[kMaxAxes], hi[kMaxAxes];
   uint32_t runs[kMaxAxes];
@@ -99,14 +104,20 @@ __device__ __forceinline__ void note_positions(const int (&x)[NA][2], int (*pos)
     if (lo < -kPosLimit || hi > kPosLimit) raise_status(status, LSRM_ERR_BOUNDS);
     const uint32_t e0 = __ballot_sync(0xffffffffu, x[a][0] == __shfl_down_sync(0xffffffffu, x[a][0], 1));
     const uint32_t e1 = __ballot_sync(0xffffffffu, x[a][1] == __shfl_down_sync(0xffffffffu, x[a][1], 1));
+    const uint32_t f0 = __ballot_sync(0xffffffffu, x[a][0] == __shfl_down_sync(0xffffffffu, x[a][0], 4));
+    const uint32_t f1 = __ballot_sync(0xffffffffu, x[a][1] == __shfl_down_sync(0xffffffffu, x[a][1], 4));
     pos[a][lane] = x[a][0];
     pos[a][lane + 32] = x[a][1];
     if (lane == 0) {
       uint32_t runs = 0;
 #pragma unroll
       for (int g = 0; g < 4; ++g) {
-        const uint32_t e = (g < 2 ? e0 : e1) >> (16 * (g & 1));
-        runs |= (uint32_t)((e & 0x7fffu) == 0x7fffu ? kLane : (e & 0x7777u) == 0x7777u ? kFour : kEach) << (2 * g);
+        const uint32_t e = (g < 2 ? e0 : e1) >> (16 * (g & 1)), f = (g < 2 ? f0 : f1) >> (16 * (g & 1));
+        runs |= (uint32_t)((e & 0x7fffu) == 0x7fffu   ? kLane
+                           : (e & 0x7777u) == 0x7777u ? kFour
+                           : kHasTurn<NA> && (f & 0x0fffu) == 0x0fffu ? kTurn
+                                                                      : kEach)
+                << (8 * g);
       }
       m.lo[a] = lo, m.hi[a] = hi, m.runs[a] = runs;
     }
@@ -114,7 +125,7 @@ __device__ __forceinline__ void note_positions(const int (&x)[NA][2], int (*pos)
 }
 
 // A chunk's biases for a warp's rows.  Per axis and run of 16 columns: kOne (the chunk has one clamped
-// distance), kLane (one position in the run), kFour (one per four columns), kEach.  Positions count so that
+// distance), kLane (one position in the run), kFour (one per four columns), kTurn (the same four), kEach.  Positions count so that
 // columns less rows is the distance (the key pass, whose columns are queries, negates both).
 // RUNS: told run by run, which suits rows of patches whose ends fall anywhere (six frames' training step
 // 1401 -> 1329 us); else for the chunk as a whole, which costs less per run (forward over bricks of
@@ -133,7 +144,14 @@ struct ChunkBias {
       const int hi = clamp_index(m.hi[a] - row_lo[a], maxd, top);
       one[a] = lo == hi ? lo : -1;
       runs[a] = m.runs[a];
-      if (!RUNS) runs[a] = runs[a] == 0x55u ? kLane : (runs[a] & runs[a] >> 1 & 0x55u) == 0 ? kFour : kEach;
+      // as a whole: a kind that holds for all four runs (kLane is kFour and kTurn too), or kEach
+      if (!RUNS) {
+        const uint32_t r = runs[a];
+        runs[a] = r == 0x01010101u * kLane   ? kLane
+                  : (r & 0x04040404u) == 0 && (r & r >> 1 & 0x01010101u) == 0 ? kFour
+                  : (r & 0x01010101u) == 0x01010101u ? kTurn
+                                                     : kEach;
+      }
       if (lo == hi) {
         runs[a] = kOne;
         ub += lut[a * (top + 1) + lo];
@@ -141,7 +159,7 @@ struct ChunkBias {
     }
   }
   __device__ __forceinline__ int mode(int a, int g) const {
-    return RUNS ? runs[a] >> (2 * g) & 3 : runs[a];
+    return RUNS ? runs[a] >> (8 * g) & 7 : runs[a];
   }
   // whether run g has one bias per row
   __device__ __forceinline__ bool flat(int g) const {
@@ -172,6 +190,15 @@ struct ChunkBias {
           const float y = la[clamp_index(xs[f].x, rowc[a], top)];
           fadd2_acc(x[4 * f], x[4 * f + 1], y, y);
           fadd2_acc(x[4 * f + 2], x[4 * f + 3], y, y);
+        }
+      } else if (kHasTurn<NA> && m == kTurn) {
+        const int4 u = xs[0];
+        const float y0 = la[clamp_index(u.x, rowc[a], top)], y1 = la[clamp_index(u.y, rowc[a], top)];
+        const float y2 = la[clamp_index(u.z, rowc[a], top)], y3 = la[clamp_index(u.w, rowc[a], top)];
+#pragma unroll
+        for (int f = 0; f < 4; ++f) {
+          fadd2_acc(x[4 * f], x[4 * f + 1], y0, y1);
+          fadd2_acc(x[4 * f + 2], x[4 * f + 3], y2, y3);
         }
       } else if (m == kEach) {
 #pragma unroll

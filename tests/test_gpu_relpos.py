@@ -37,6 +37,9 @@ class Case:
                 return torch.arange(n)[:, None].expand(n, axes).contiguous().int()
             if places == "far":  # the ends of the allowed range
                 return (torch.randint(0, 3, (n, axes), generator=g) - 1).int() * 2 ** 29
+            if places == "bricks":  # 4 x 4 x 4 tokens, the last axis the fastest
+                i = torch.arange(n)
+                return torch.stack([i // 16, i // 4 % 4 + i // 64, i % 4 + i // 64 % 3], 1)[:, 3 - axes:].int().contiguous()
             if places == "frames":  # long runs on one position
                 return (torch.arange(n) // 40)[:, None].expand(n, axes).contiguous().int()
             return torch.randint(-2 * maxd, 2 * maxd + 1, (n, axes), generator=g).int()
@@ -134,6 +137,14 @@ FORWARD = {
     "long_turns64": dict(lens_q=[290, 310], heads=6, kv_heads=1, axes=2, places="frames", maxd=20, dim=64),
     "long_one_cta": dict(lens_q=[300, 411], axes=3, places="scattered", maxd=60, buckets=48),
     "long_one_cta64": dict(lens_q=[350], axes=3, places="scattered", dim=64),
+    # columns whose positions repeat
+    "bricks": dict(lens_q=[200, 64, 77], axes=3, places="bricks", maxd=6, buckets=12),
+    "bricks_short": dict(lens_q=[64, 50, 64, 9] * 12, heads=8, kv_heads=2, axes=3, places="bricks", maxd=16, buckets=16),
+    "bricks_short64": dict(lens_q=[64, 33, 0] * 20, dim=64, axes=2, places="bricks", maxd=3, buckets=6),
+    "bricks_long": dict(lens_q=[333, 448], axes=3, places="bricks", maxd=16, buckets=16),
+    "bricks_long64": dict(lens_q=[320, 290], axes=1, places="bricks", maxd=9, buckets=8, dim=64),
+    "bricks_one_cta": dict(lens_q=[448], axes=3, places="bricks", maxd=20, buckets=48, dim=64),
+    "bricks_cross": dict(lens_q=[3, 20, 1], lens_k=[600, 64, 128], axes=3, places="bricks", maxd=5, buckets=10),
     # 64 and 128 rows a CTA, and the most rows of the kernel for few
     "rows64": dict(lens_q=[61, 40], lens_k=[300, 33], axes=2, places="scattered"),
     "rows128": dict(lens_q=[90, 75, 101], lens_k=[400, 257, 70], axes=3, places="scattered"),
