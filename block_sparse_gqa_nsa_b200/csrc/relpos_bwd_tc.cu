@@ -301,7 +301,7 @@ __global__ void __launch_bounds__(kTcThreads, 2)
     __syncwarp();
     const float l2 = fmaf(lse, kLog2e, corr), rconst = small ? l2 : lse;
 
-    ChunkBias<NA, true> cb;
+    ChunkBias<NA> cb;
     for (int c = 0; ok && c < chunks; ++c) {
       const int st = c % C::kStages, left = khi - klo - c * kTcCols;
       if (!wait_bar_w(&S.kv_full[st], (c / C::kStages) & 1, abort, p.status) ||
@@ -661,7 +661,7 @@ __global__ void __launch_bounds__(kTcThreads, CTAS)
     EwBarrier eb{&S.ew, abort, p.status, 0};
     bool ok = true, small = false;
     float mul = 0.0f;
-    ChunkBias<NA, true> cb;
+    ChunkBias<NA> cb;
     uint32_t turn = 0;
     // a turn: the two warps that share keys have both come here
     auto swap = [&]() {

@@ -248,7 +248,7 @@ __global__ void __launch_bounds__(kTcThreads, 2)
     float m = 0.0f, l = 0.0f;  // the row's reference (in the scores' units) and sum
     bool ok = true;
     int st = 0, left = 0;  // the current chunk's stage and keys from here on
-    ChunkBias<NA, false> cb;
+    ChunkBias<NA> cb;
 
     // The chunk again, or a chunk of a table too large to fold: its maximum, the reference of the rows
     // that are `off` (or, without folding, behind their maximum) moved to it, and P from the scores in

@@ -127,13 +127,12 @@ __device__ __forceinline__ void note_positions(const int (&x)[NA][2], int (*pos)
 // A chunk's biases for a warp's rows.  Per axis and run of 16 columns: kOne (the chunk has one clamped
 // distance), kLane (one position in the run), kFour (one per four columns), kTurn (the same four), kEach.  Positions count so that
 // columns less rows is the distance (the key pass, whose columns are queries, negates both).
-// RUNS: told run by run, which suits rows of patches whose ends fall anywhere (six frames' training step
-// 1401 -> 1329 us); else for the chunk as a whole, which costs less per run (forward over bricks of
-// three axes 612 -> 531 us).
-template <int NA, bool RUNS>
+// Told run by run, as rows of patches end anywhere (forward of 8 x 1370 patches, 16 heads of 64: 250 us; one
+// kind for the chunk 272).
+template <int NA>
 struct ChunkBias {
   int one[NA];  // the chunk's only index into the table, or -1
-  uint32_t runs[NA];  // 0 (kOne) with one; !RUNS: the mode of the whole chunk
+  uint32_t runs[NA];  // as ChunkMeta's, or 0 (kOne) for all
   float ub;  // the bias common to the chunk
   __device__ __forceinline__ void set(const ChunkMeta& m, const int (&row_lo)[NA], const int (&row_hi)[NA], int maxd,
                                       const float* lut, int top) {
@@ -144,14 +143,6 @@ struct ChunkBias {
       const int hi = clamp_index(m.hi[a] - row_lo[a], maxd, top);
       one[a] = lo == hi ? lo : -1;
       runs[a] = m.runs[a];
-      // as a whole: a kind that holds for all four runs (kLane is kFour and kTurn too), or kEach
-      if (!RUNS) {
-        const uint32_t r = runs[a];
-        runs[a] = r == 0x01010101u * kLane   ? kLane
-                  : (r & 0x04040404u) == 0 && (r & r >> 1 & 0x01010101u) == 0 ? kFour
-                  : (r & 0x01010101u) == 0x01010101u ? kTurn
-                                                     : kEach;
-      }
       if (lo == hi) {
         runs[a] = kOne;
         ub += lut[a * (top + 1) + lo];
@@ -159,7 +150,7 @@ struct ChunkBias {
     }
   }
   __device__ __forceinline__ int mode(int a, int g) const {
-    return RUNS ? runs[a] >> (8 * g) & 7 : runs[a];
+    return runs[a] >> (8 * g) & 7;
   }
   // whether run g has one bias per row
   __device__ __forceinline__ bool flat(int g) const {
