@@ -1,22 +1,24 @@
 // Forward of the attention with a learned relative position bias by buckets (relpos.cuh has the
 // formulas).
 //
-// Each score costs one exponential, one table look-up per axis and 4 d tensor FLOP, so at d = 32 / 64
-// the per-score work of the softmax warps, not the tensor pipe, is the bound.  Scores stay in
-// registers from Q K^T to P V (mma.sync row tiles: a lane sees its rows' distances directly, and P
-// goes from the accumulator layout to the operand layout without leaving the registers).  Two
-// kernels, chosen by how many query rows share a key stream:
-//   * rp_fwd_kernel: 128 or 64 queries of one head a CTA, 32 a warp; keys stream through shared
-//     memory in chunks of 64 (cp.async, three stages).  Per head the bias is a table over the clamped
-//     distance, so a score needs one clamp and one shared load per axis, and none where a whole
-//     32 x 32 tile lies on one distance (every pair past max_distance, or single positions).
-//   * rp_few_kernel: 16 rows (tokens x heads of one KV group) a CTA, each warp its own keys, the
-//     warps joined in shared memory: single tokens and other short query runs, bound by reading K, V.
-// Both split the keys over CTAs when there are too few rows to fill the GPU; rp_join_kernel then adds
-// the parts by their softmax references and sums in a fixed order.
+// Each score costs one exponential, a table look-up per axis and 4 d tensor FLOP, so at d = 32 / 64 the
+// per-score work of the softmax warps, not the tensor pipe, is the bound.  fwd_plan chooses among four
+// kernels by how many query rows share a key stream:
+//   * rp_few_kernel (here): 16 rows (tokens x heads of one KV group) a CTA, each warp its own keys, the
+//     warps joined in shared memory: single tokens and other short query runs, bound by reading K, V.  64 single
+//     tokens against ragged pasts of up to 8192 (32 heads of 32) 25 us, 72 MB of K and V at 2.9 TB/s;
+//   * rp_short_fwd_kernel (relpos_short.cu): many short segments;
+//   * rp_fwd_kernel (here): 64 or 128 queries of one head a CTA, 32 a warp, some tens of queries a segment: keys
+//     stream through shared memory in chunks of 64 (cp.async, three stages), scores stay in registers from
+//     Q K^T to P V (mma.sync row tiles: a lane sees its rows' distances directly, and P goes from the
+//     accumulator layout to the operand layout without leaving the registers; tcgen05's 128-row tiles would be
+//     half empty);
+//   * rp_fwd_tc_kernel (relpos_tc.cu): 256 queries a CTA on tcgen05.
+// All but the second split the keys over CTAs when there are too few rows to fill the GPU; rp_join_kernel then
+// adds the parts by their softmax references and sums in a fixed order.
 //
-// The softmax keeps a reference per row that moves only when a score exceeds it by more than 8
-// (P stays below e^8, far inside fp32 and bf16), so most tiles need no rescaling and no shuffles.
+// The softmax keeps a reference per row that moves only when a score exceeds it by more than 8 in the table's
+// units (P stays below e^8, far inside fp32 and bf16), so most tiles need no rescaling and no shuffles.
 // Row sums are fp32 over the unrounded P; P is rounded to bf16 for the second product, as its
 // operand V is bf16.
 #include "relpos.cuh"
@@ -39,9 +41,9 @@ struct FwdCfg {
   static size_t smem(int maxd) { return kFixed + (size_t)NA * (2 * maxd + 1) * 4; }
 };
 
-// Softmax of a warp's score tile (MT row tiles of 16, NT key tiles of 8) and its P V.
-// t holds the scores (x = multiplier, c = per-row constant of the exponent's argument: p =
-// exp2(t x + c)), mx the lane's largest score per row in natural units.
+// The softmax references and sums of a warp's rows (MT row tiles of 16), in the table's units (to_log2: their
+// factor to log2); mx is the lane's largest score per row.  Where one passes the reference by more than kSlack,
+// the tile's references move to their rows' maxima and the sums and outputs are rescaled.
 template <int MT>
 struct RowState {
   float m[MT][2], l[MT][2];

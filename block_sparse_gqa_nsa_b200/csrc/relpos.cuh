@@ -1,5 +1,7 @@
-// Shared pieces of the attention with a learned relative position bias by buckets
-// (relpos.cu: forward, relpos_bwd.cu: backward).
+// Shared pieces of the attention with a learned relative position bias by buckets.  Which file has which
+// kernels: relpos.cu forward of few and of some tens of queries a segment, joins; relpos_short.cu forward and
+// dq of many short segments; relpos_tc.cu forward of long ones on tcgen05; relpos_bwd.cu the backward's
+// mathematics, its kernels up to middle lengths, joins; relpos_bwd_tc.cu the backward of long segments.
 //
 // Segment s holds the queries off_q[s] .. off_q[s+1]-1 and the keys off_k[s] .. off_k[s+1]-1; every
 // query attends every key of its segment.  With D = max_distance, per axis a of the positions
@@ -349,6 +351,48 @@ __device__ __forceinline__ bool add_bias(float (&s)[MT][kGroups][4], float (&bas
     }
   }
   return false;
+}
+
+// ---- backward ----
+// Rows whose |LSE| is so large that fp32 lost the logarithm of their sum beside the largest score
+// (every key masked by a huge finite bias): corr = log2 sum_j exp(t - lse), a row at a time, lanes over
+// keys.  The tile's rows are wrow .. wrow + 15; lane (g, .) holds the LSE of rows g and g + 8.  Inline, rare as it
+// is: around a call the kernels kept registers in local memory (dq of 256 ragged blocks 118 -> 89 us).
+template <int D, int NA>
+__device__ __forceinline__ float2 huge_rows(const Params& p, const float* lut, bool small, float lse0, float lse1,
+                                         int wrow, int h, int hk, int klo, int khi, int lane) {
+  const float units = small ? kLn2 : 1.0f;  // the table's to natural ones
+  float2 corr = make_float2(0.0f, 0.0f);
+  for (int r = 0; r < 16; ++r) {
+    const float l = __shfl_sync(0xffffffffu, r < 8 ? lse0 : lse1, (r & 7) * 4);
+    if (!(fabsf(l) >= kFoldLimit) || l == INFINITY) continue;
+    const size_t row = wrow + r;
+    const uint16_t* q = p.q + (row * p.Hq + h) * D;
+    float sum = 0.0f;
+    for (int j = klo + lane; j < khi; j += 32) {
+      const uint16_t* k = p.k + ((size_t)j * p.Hkv + hk) * D;
+      float t = 0.0f;
+      for (int d = 0; d < D; ++d) t = fmaf(bf16_to_f32(q[d]), bf16_to_f32(k[d]), t);
+      t *= p.scale;
+      for (int a = 0; a < NA; ++a)
+        t += units * lut[a * (2 * p.maxd + 1) + clamp_index(p.pos_k[(size_t)j * NA + a],
+                                                            p.maxd - p.pos_q[row * NA + a], 2 * p.maxd)];
+      sum += ex2((t - l) * kLog2e);
+    }
+    __syncwarp();
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    if ((lane >> 2) == (r & 7)) (r < 8 ? corr.x : corr.y) = log2f(sum);
+  }
+  return corr;
+}
+
+// Two sums into a column of the table's gradient (byte offsets of the buckets' entries) with both reads ahead
+// of both writes: one latency for two, and right when the buckets are the same.
+__device__ __forceinline__ void add_two(char* col, int b0, float v0, int b1, float v1) {
+  float *p0 = reinterpret_cast<float*>(col + b0), *p1 = reinterpret_cast<float*>(col + b1);
+  const float s0 = *p0 + v0, x1 = *p1;
+  *p0 = s0;
+  *p1 = (b0 == b1 ? s0 : x1) + v1;
 }
 
 // A head's table gradient from its columns hist[axis][NB and one for ids out of range][COLS]: the sum of each

@@ -37,10 +37,20 @@ lsrm_status check_relpos(const lsrm_relpos_desc* d) {
   const rp::FwdPlan f = rp::fwd_plan(*d);
   const rp::BwdPlan b = rp::bwd_plan(*d);
   const long long most = INT32_MAX;
-  if (f.ctas > most || b.short_ctas > most || b.dq_tiles * d->n_q_heads > most || b.kv_tiles * d->n_kv_heads * b.splits > most ||
-      d->n_q_tokens + d->n_segs > most || d->n_k_tokens + d->n_segs > most || d->n_q_heads > 65535)
+  if (f.ctas > most || b.short_ctas > most || b.dq_tiles * d->n_q_heads > most ||
+      b.kv_tiles * d->n_kv_heads * b.splits > most || d->n_segs > most / 2 || d->n_q_tokens + d->n_segs > most ||
+      d->n_k_tokens + d->n_segs > most || d->n_q_heads > 65535)
     return LSRM_ERR_UNSUPPORTED;
   return LSRM_OK;
+}
+
+// the inputs that both calls have, by the alignment that the kernels read them with
+bool inputs_aligned(const int32_t* off_q, const int32_t* off_k, const int32_t* pos_q, const int32_t* pos_k,
+                    const int32_t* bucket_of, const void* table, const void* q, const void* k, const void* v) {
+  for (const void* x : {(const void*)off_q, (const void*)off_k, (const void*)pos_q, (const void*)pos_k,
+                        (const void*)bucket_of})
+    if (!on(x, 4)) return false;
+  return on(table, 2) && on(q, 16) && on(k, 16) && on(v, 16);
 }
 
 lsrm_status check_relpos_ws(const lsrm_relpos_desc& d, const void* ws, size_t bytes) {
@@ -145,7 +155,8 @@ lsrm_status lsrm_relpos_forward(const lsrm_relpos_desc* desc, const int32_t* off
   if (off_q == nullptr || off_k == nullptr || bucket_of == nullptr || table == nullptr) return LSRM_ERR_INVALID_ARG;
   if (desc->n_q_tokens > 0 && (pos_q == nullptr || q == nullptr || out == nullptr)) return LSRM_ERR_INVALID_ARG;
   if (desc->n_k_tokens > 0 && (pos_k == nullptr || k == nullptr || v == nullptr)) return LSRM_ERR_INVALID_ARG;
-  if (!on(q, 16) || !on(k, 16) || !on(v, 16) || !on(out, 16)) return LSRM_ERR_INVALID_ARG;
+  if (!inputs_aligned(off_q, off_k, pos_q, pos_k, bucket_of, table, q, k, v) || !on(out, 16) || !on(lse_or_null, 4))
+    return LSRM_ERR_INVALID_ARG;
   if (desc->n_q_tokens == 0) return LSRM_OK;
   rp::Params p = params_of(*desc, off_q, off_k, pos_q, pos_k, bucket_of, table, q, k, v, ws);
   const rp::FwdPlan f = rp::fwd_plan(*desc);
@@ -169,7 +180,9 @@ lsrm_status lsrm_relpos_backward(const lsrm_relpos_desc* desc, const int32_t* of
     return LSRM_ERR_INVALID_ARG;
   if (desc->n_k_tokens > 0 && (pos_k == nullptr || k == nullptr || v == nullptr || dk == nullptr || dv == nullptr))
     return LSRM_ERR_INVALID_ARG;
-  for (const void* x : {q, k, v, out, dout, (const void*)dq, (const void*)dk, (const void*)dv})
+  if (!inputs_aligned(off_q, off_k, pos_q, pos_k, bucket_of, table, q, k, v) || !on(lse, 4) || !on(dtable, 2))
+    return LSRM_ERR_INVALID_ARG;
+  for (const void* x : {out, dout, (const void*)dq, (const void*)dk, (const void*)dv})
     if (!on(x, 16)) return LSRM_ERR_INVALID_ARG;
   rp::Params p = params_of(*desc, off_q, off_k, pos_q, pos_k, bucket_of, table, q, k, v, ws);
   const rp::BwdPlan b = rp::bwd_plan(*desc);
@@ -192,7 +205,9 @@ lsrm_status lsrm_layer_norm_forward(int64_t rows, int32_t width, int32_t dtype, 
   if (rows == 0) return LSRM_OK;
   const size_t el = dtype == LSRM_BF16 ? 2 : 4;
   if (x == nullptr || y == nullptr) return LSRM_ERR_INVALID_ARG;
-  if (!on(x, el) || !on(y, el) || !on(gamma_or_null, el) || !on(beta_or_null, el)) return LSRM_ERR_INVALID_ARG;
+  if (!on(x, el) || !on(y, el) || !on(gamma_or_null, el) || !on(beta_or_null, el) || !on(mean_or_null, 4) ||
+      !on(rstd_or_null, 4))
+    return LSRM_ERR_INVALID_ARG;
   return launch_layer_norm_forward(rows, width, dtype, x, gamma_or_null, beta_or_null, eps, y, mean_or_null,
                                    rstd_or_null, (cudaStream_t)stream);
 }
@@ -212,6 +227,7 @@ lsrm_status lsrm_layer_norm_backward(int64_t rows, int32_t width, int32_t dtype,
     return LSRM_ERR_INVALID_ARG;
   for (const void* a : {dy, x, gamma_or_null, (const void*)dx, (const void*)dgamma_or_null, (const void*)dbeta_or_null})
     if (!on(a, el)) return LSRM_ERR_INVALID_ARG;
+  if (!on(mean, 4) || !on(rstd, 4)) return LSRM_ERR_INVALID_ARG;
   if (ws == nullptr || !on(ws, 256) || ws_bytes < lsrm_layer_norm_workspace_size(rows, width))
     return LSRM_ERR_WORKSPACE;
   return launch_layer_norm_backward(rows, width, dtype, dy, x, gamma_or_null, mean, rstd, dx, dgamma_or_null,

@@ -8,6 +8,11 @@
 //   * rp_dq_kernel: queries of one head a CTA, keys streaming: dq, and Delta for the other pass;
 //   * rp_dkv_kernel: keys of one KV head a CTA, the queries of its heads streaming: dk, dv and the
 //     table's gradient.
+// Both passes take 64-row tiles and mma.sync: with segments of up to a few hundred tokens, 128-row tiles of
+// tcgen05 are half empty (8 segments of 192 tokens, 32 heads of 32: 119 us, by relpos_bwd_tc.cu 127; of 512
+// tokens 508 against 418).  Many short segments have a dq pass of their own (relpos_short.cu).  What bounds the
+// passes is the per-score work (exponential, look-ups, and in the key pass the table's sums: 256 ragged blocks of
+// up to 64 tokens, 32 heads of 32: 132 us, 71M warp instructions at 1.9 a clock), not the tensor pipe (6%).
 //
 // Delta.  sum_d dO o with the forward's out is off by that output's bf16 rounding, which a gradient
 // that adds up a whole row of dS (the table's) or few keys (short segments) would show.  With D~ that
@@ -29,6 +34,7 @@
 namespace lsrm {
 namespace rp {
 
+constexpr int MT = 1;  // row tiles of 16 a warp: a second one's operands and sums would halve the warps an SM holds
 constexpr int kBThreads = 128, kBChunk = 64, kBStages = 3, kKeyStages = 2;
 
 template <int D, int NA>
@@ -44,37 +50,7 @@ struct BwdCfg {
   }
 };
 
-// Rows whose |LSE| is so large that fp32 lost the logarithm of their sum beside the largest score
-// (every key masked by a huge finite bias): corr = log2 sum_j exp(t - lse), a row at a time, lanes over
-// keys.  The tile's rows are wrow .. wrow + 15; lane (g, .) holds the LSE of rows g and g + 8.
-template <int D, int NA>
-__device__ __forceinline__ float2 huge_rows(const Params& p, const float* lut, bool small, float lse0, float lse1,
-                                         int wrow, int h, int hk, int klo, int khi, int lane) {
-  const float units = small ? kLn2 : 1.0f;  // the table's to natural ones
-  float2 corr = make_float2(0.0f, 0.0f);
-  for (int r = 0; r < 16; ++r) {
-    const float l = __shfl_sync(0xffffffffu, r < 8 ? lse0 : lse1, (r & 7) * 4);
-    if (!(fabsf(l) >= kFoldLimit) || l == INFINITY) continue;
-    const size_t row = wrow + r;
-    const uint16_t* q = p.q + (row * p.Hq + h) * D;
-    float sum = 0.0f;
-    for (int j = klo + lane; j < khi; j += 32) {
-      const uint16_t* k = p.k + ((size_t)j * p.Hkv + hk) * D;
-      float t = 0.0f;
-      for (int d = 0; d < D; ++d) t = fmaf(bf16_to_f32(q[d]), bf16_to_f32(k[d]), t);
-      t *= p.scale;
-      for (int a = 0; a < NA; ++a)
-        t += units * lut[a * (2 * p.maxd + 1) + clamp_index(p.pos_k[(size_t)j * NA + a],
-                                                            p.maxd - p.pos_q[row * NA + a], 2 * p.maxd)];
-      sum += ex2((t - l) * kLog2e);
-    }
-    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    if ((lane >> 2) == (r & 7)) (r < 8 ? corr.x : corr.y) = log2f(sum);
-  }
-  return corr;
-}
-
-template <int D, int NA, int MT, bool kExact>
+template <int D, int NA, bool kExact>
 __global__ void __launch_bounds__(kBThreads, D == 32 ? 3 : 2) rp_dq_kernel(const Params p) {
   using C = BwdCfg<D, NA>;
   constexpr int kRows = 64 * MT;
@@ -301,16 +277,7 @@ __global__ void __launch_bounds__(kBThreads, D == 32 ? 3 : 2) rp_dq_kernel(const
     }
 }
 
-// two sums into the thread's own column (byte offsets of the buckets' entries) with both reads ahead of
-// both writes: one latency for two, and right when the buckets are the same
-__device__ __forceinline__ void add_two(char* col, int b0, float v0, int b1, float v1) {
-  float *p0 = reinterpret_cast<float*>(col + b0), *p1 = reinterpret_cast<float*>(col + b1);
-  const float x0 = *p0, x1 = *p1;
-  *p1 = x1 + v1;
-  *p0 = x0 + v0 + (b0 == b1 ? v1 : 0.0f);
-}
-
-template <int D, int NA, int MT>
+template <int D, int NA>
 __global__ void __launch_bounds__(kBThreads, D == 32 ? 4 : 2) rp_dkv_kernel(const Params p) {
   using C = BwdCfg<D, NA>;
   constexpr int kRows = 64 * MT;
@@ -500,8 +467,8 @@ __global__ void __launch_bounds__(kBThreads, D == 32 ? 4 : 2) rp_dkv_kernel(cons
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
             const bool there = tq * kLaneCols + 2 * n + e < left;
-            const size_t at = (size_t)(qlo + (c0 + cc) * kBChunk + qb + (there ? tq * kLaneCols + 2 * n + e : 0)) * p.Hq +
-                              hk * p.G + head;
+            const int col = there ? tq * kLaneCols + 2 * n + e : 0;
+            const size_t at = (size_t)(qlo + (c0 + cc) * kBChunk + qb + col) * p.Hq + hk * p.G + head;
             ln[e] = there ? p.lse_in[at] : INFINITY;
             if (ln[e] == -INFINITY) ln[e] = INFINITY;
             cr[e] = there ? p.corr[at] : 0.0f;
@@ -707,15 +674,15 @@ static bool allow_smem(K kernel, size_t bytes) {
 template <int D, int NA, bool kExact>
 static lsrm_status run_dq(const Params& p, const BwdPlan& b, cudaStream_t s) {
   const size_t bytes = BwdCfg<D, NA>::smem_dq(p.maxd);
-  if (!allow_smem(rp_dq_kernel<D, NA, 1, kExact>, bytes)) return LSRM_ERR_CUDA;
-  rp_dq_kernel<D, NA, 1, kExact><<<(unsigned)(b.dq_tiles * p.Hq), kBThreads, bytes, s>>>(p);
+  if (!allow_smem(rp_dq_kernel<D, NA, kExact>, bytes)) return LSRM_ERR_CUDA;
+  rp_dq_kernel<D, NA, kExact><<<(unsigned)(b.dq_tiles * p.Hq), kBThreads, bytes, s>>>(p);
   return launched();
 }
 template <int D, int NA>
 static lsrm_status run_dkv(const Params& p, const BwdPlan& b, cudaStream_t s) {
   const size_t bytes = BwdCfg<D, NA>::smem_dkv(p.maxd, p.NB);
-  if (!allow_smem(rp_dkv_kernel<D, NA, 1>, bytes)) return LSRM_ERR_CUDA;
-  rp_dkv_kernel<D, NA, 1><<<(unsigned)(b.kv_tiles * p.Hkv * p.splits), kBThreads, bytes, s>>>(p);
+  if (!allow_smem(rp_dkv_kernel<D, NA>, bytes)) return LSRM_ERR_CUDA;
+  rp_dkv_kernel<D, NA><<<(unsigned)(b.kv_tiles * p.Hkv * p.splits), kBThreads, bytes, s>>>(p);
   return launched();
 }
 

@@ -10,9 +10,10 @@
 //
 // 320 threads: warp 0 brings the streamed operands by TMA and the columns' positions and row constants by
 // plain loads, warp 1 issues the MMAs, warps 2-9 do the scores: two threads a row, 32 columns each.  Each
-// half of the columns is a pipeline of its own (scores, products, barriers), so that with two tiles an SM
-// four pipelines cover each other's hand-overs between the score warps and the tensor cores (one pipeline
-// a tile: dq 375 us, dk/dv 573 us at 4096 tokens and 32 heads of 32).
+// half of the columns is a pipeline of its own (scores, products, barriers), so that with two CTAs an SM
+// four pipelines cover each other's hand-overs between the score warps and the tensor cores (4096 tokens, 32
+// heads of 32: dq 334 us, dk/dv 476; with one pipeline a tile dq went 375 -> 338 and dk/dv 573 -> 483 when it
+// was split).  The score warps are the bound: 2.1 to 2.3 warp instructions a clock and SM, the tensor pipe 14%.
 // Against the mma.sync kernels, which they replace on long segments, the operands need no shared-memory
 // reads by the warps that compute, and runs of columns on one position share look-ups and sums.
 //
@@ -72,8 +73,8 @@ __device__ __forceinline__ bool ew_fill(const Params& p, float* lut, int h, int 
 
 // log2 sum_j exp(t - l) of one row whose |LSE| is huge (see huge_rows), by a whole warp
 template <int D, int NA>
-__device__ __forceinline__ float huge_row(const Params& p, const float* lut, bool small, float l, int row, int h, int hk,
-                                       int klo, int khi, int lane) {
+__device__ __forceinline__ float huge_row(const Params& p, const float* lut, bool small, float l, int row, int h,
+                                          int hk, int klo, int khi, int lane) {
   const float units = small ? kLn2 : 1.0f;
   const uint16_t* q = p.q + ((size_t)row * p.Hq + h) * D;
   float sum = 0.0f;
@@ -441,14 +442,6 @@ struct DkvTcSmem {
   }
 };
 
-// two sums into the thread's own column with both reads ahead of both writes (as in relpos_bwd.cu)
-__device__ __forceinline__ void add_two_tc(char* col, int b0, float v0, int b1, float v1) {
-  float *p0 = reinterpret_cast<float*>(col + b0), *p1 = reinterpret_cast<float*>(col + b1);
-  const float s0 = *p0 + v0, x1 = *p1;
-  *p0 = s0;
-  *p1 = (b0 == b1 ? s0 : x1) + v1;
-}
-
 template <int D, int NA, int CTAS>
 __global__ void __launch_bounds__(kTcThreads, CTAS)
     rp_dkv_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
@@ -771,23 +764,23 @@ __global__ void __launch_bounds__(kTcThreads, CTAS)
             } else if (md == kFour) {
 #pragma unroll
               for (int f = 0; f < 4; f += 2)
-                add_two_tc(to, boff[clamp_index(xs[f].x, rowc[a], top)],
+                add_two(to, boff[clamp_index(xs[f].x, rowc[a], top)],
                            (x[4 * f] + x[4 * f + 1]) + (x[4 * f + 2] + x[4 * f + 3]),
                            boff[clamp_index(xs[f + 1].x, rowc[a], top)],
                            (x[4 * f + 4] + x[4 * f + 5]) + (x[4 * f + 6] + x[4 * f + 7]));
             } else if (kHasTurn<NA> && md == kTurn) {
               const int4 u = xs[0];
-              add_two_tc(to, boff[clamp_index(u.x, rowc[a], top)], (x[0] + x[4]) + (x[8] + x[12]),
+              add_two(to, boff[clamp_index(u.x, rowc[a], top)], (x[0] + x[4]) + (x[8] + x[12]),
                          boff[clamp_index(u.y, rowc[a], top)], (x[1] + x[5]) + (x[9] + x[13]));
-              add_two_tc(to, boff[clamp_index(u.z, rowc[a], top)], (x[2] + x[6]) + (x[10] + x[14]),
+              add_two(to, boff[clamp_index(u.z, rowc[a], top)], (x[2] + x[6]) + (x[10] + x[14]),
                          boff[clamp_index(u.w, rowc[a], top)], (x[3] + x[7]) + (x[11] + x[15]));
             } else {
 #pragma unroll
               for (int f = 0; f < 4; ++f) {
                 const int4 u = xs[f];
-                add_two_tc(to, boff[clamp_index(u.x, rowc[a], top)], x[4 * f], boff[clamp_index(u.y, rowc[a], top)],
+                add_two(to, boff[clamp_index(u.x, rowc[a], top)], x[4 * f], boff[clamp_index(u.y, rowc[a], top)],
                            x[4 * f + 1]);
-                add_two_tc(to, boff[clamp_index(u.z, rowc[a], top)], x[4 * f + 2],
+                add_two(to, boff[clamp_index(u.z, rowc[a], top)], x[4 * f + 2],
                            boff[clamp_index(u.w, rowc[a], top)], x[4 * f + 3]);
               }
             }
@@ -841,7 +834,8 @@ __global__ void __launch_bounds__(kTcThreads, CTAS)
         dst[0] = make_uint4(u[0], u[1], u[2], u[3]);
         dst[1] = make_uint4(u[4], u[5], u[6], u[7]);
       } else {
-        uint4* dst = reinterpret_cast<uint4*>(p.kv_part + ((size_t)split * 2 + (half == 0 ? 1 : 0)) * stride + at + 16 * i);
+        float* part = p.kv_part + ((size_t)split * 2 + (half == 0 ? 1 : 0)) * stride;
+        uint4* dst = reinterpret_cast<uint4*>(part + at + 16 * i);
 #pragma unroll
         for (int e = 0; e < 4; ++e) dst[e] = make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
       }
@@ -907,7 +901,8 @@ static int dkv_fit(int maxd, int nb) {
   return DkvTcSmem<D, NA, 1>::bytes(maxd, nb) <= 227 * 1024 ? 1 : 0;
 }
 int bwd_tc_ctas(int D, int NA, int maxd, int nb) {
-  if (D == 32) return NA == 1 ? dkv_fit<32, 1>(maxd, nb) : NA == 2 ? dkv_fit<32, 2>(maxd, nb) : dkv_fit<32, 3>(maxd, nb);
+  if (D == 32)
+    return NA == 1 ? dkv_fit<32, 1>(maxd, nb) : NA == 2 ? dkv_fit<32, 2>(maxd, nb) : dkv_fit<32, 3>(maxd, nb);
   return NA == 1 ? dkv_fit<64, 1>(maxd, nb) : NA == 2 ? dkv_fit<64, 2>(maxd, nb) : dkv_fit<64, 3>(maxd, nb);
 }
 

@@ -14,6 +14,10 @@
 // only when a chunk's sum of P leaves [2^-64, 2^16], and the chunk is done again), stores of P straight
 // to tensor memory.
 //
+// Measured: 4096 tokens of 32 heads of 32 on one axis 246 us, as bricks on three axes 431 us, eight frames of
+// 1370 patches of 16 heads of 64 on two axes 250 us; 2.2 warp instructions a clock and SM, exponentials 25-40% of
+// their rate, tensor pipe 12%.
+//
 // Tensor memory a tile, 128 columns: S [64 fp32] | P [32, bf16 pairs] | O [32] at d = 32; at d = 64 P lies
 // over S (S 64 | O 64), is kept in registers until the chunk's sum has passed, and the next S waits for
 // P V.  Either way four tiles are in flight an SM.
@@ -434,7 +438,8 @@ static lsrm_status run_tc(const Params& p, long long ctas, cudaStream_t s) {
 }
 
 lsrm_status launch_fwd_tc(const Params& p, int D, int NA, long long ctas, cudaStream_t s) {
-  if (D == 32) return NA == 1 ? run_tc<32, 1>(p, ctas, s) : NA == 2 ? run_tc<32, 2>(p, ctas, s) : run_tc<32, 3>(p, ctas, s);
+  if (D == 32)
+    return NA == 1 ? run_tc<32, 1>(p, ctas, s) : NA == 2 ? run_tc<32, 2>(p, ctas, s) : run_tc<32, 3>(p, ctas, s);
   return NA == 1 ? run_tc<64, 1>(p, ctas, s) : NA == 2 ? run_tc<64, 2>(p, ctas, s) : run_tc<64, 3>(p, ctas, s);
 }
 

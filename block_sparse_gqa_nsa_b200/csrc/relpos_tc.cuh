@@ -69,7 +69,8 @@ __device__ __forceinline__ bool wait_bar_w(uint64_t* bar, uint32_t parity, volat
 // lies behind a segment may be anything, and a weight of 0 does not hide an infinity.  A whole warp;
 // the caller makes it visible to the tensor cores (fence_async) before its arrive.
 template <int D>
-__device__ __forceinline__ void copy_tail(uint8_t* dst, const uint16_t* src, int r0, int n, int heads, int h, int lane) {
+__device__ __forceinline__ void copy_tail(uint8_t* dst, const uint16_t* src, int r0, int n, int heads, int h,
+                                          int lane) {
   constexpr int kPieces = D / 8;
   for (int i = lane; i < kTcCols * kPieces; i += 32) {
     const int r = i / kPieces, c = i % kPieces;
@@ -125,8 +126,9 @@ __device__ __forceinline__ void note_positions(const int (&x)[NA][2], int (*pos)
 }
 
 // A chunk's biases for a warp's rows.  Per axis and run of 16 columns: kOne (the chunk has one clamped
-// distance), kLane (one position in the run), kFour (one per four columns), kTurn (the same four), kEach.  Positions count so that
-// columns less rows is the distance (the key pass, whose columns are queries, negates both).
+// distance), kLane (one position in the run), kFour (one per four columns), kTurn (the same
+// four), kEach.  Positions count so that columns less rows is the distance (the key pass, whose columns are
+// queries, negates both).
 // Told run by run, as rows of patches end anywhere (forward of 8 x 1370 patches, 16 heads of 64: 250 us; one
 // kind for the chunk 272).
 template <int NA>
@@ -149,9 +151,7 @@ struct ChunkBias {
       }
     }
   }
-  __device__ __forceinline__ int mode(int a, int g) const {
-    return runs[a] >> (8 * g) & 7;
-  }
+  __device__ __forceinline__ int mode(int a, int g) const { return runs[a] >> (8 * g) & 7; }
   // whether run g has one bias per row
   __device__ __forceinline__ bool flat(int g) const {
     bool f = true;

@@ -344,8 +344,8 @@ LSRM_API lsrm_status lsrm_relpos_log_buckets(int32_t n_buckets, int32_t max_dist
 /* Forward.  off_q, off_k int32 [S+1] (ascending, within [0, Nq] / [0, Nk]); pos_q int32 [Nq][n_axes],
  * pos_k int32 [Nk][n_axes] within [-2^29, 2^29]; bucket_of int32 [2 D + 1]; table bf16
  * [n_axes][n_buckets][Hq] (added to the scaled scores as it is); q bf16 [Nq][Hq][d], k, v bf16
- * [Nk][Hkv][d], out bf16 [Nq][Hq][d], all 16-byte aligned; lse_or_null fp32 [Nq][Hq].  Rows that
- * belong to no segment are left as they were.  Segment bounds, positions or bucket ids outside their
+ * [Nk][Hkv][d], out bf16 [Nq][Hq][d], these four 16-byte aligned; lse_or_null fp32 [Nq][Hq].  Outputs
+ * must not overlap inputs.  Rows that belong to no segment are left as they were.  Segment bounds, positions or bucket ids outside their
  * ranges raise LSRM_ERR_BOUNDS in the device status (the bounds and distances are clipped, such a
  * bucket counts as bias 0); nothing outside the arrays is read or written.  Errors:
  * LSRM_ERR_INVALID_ARG (descriptor, null or misaligned pointer), LSRM_ERR_UNSUPPORTED (head_dim; a
@@ -358,7 +358,7 @@ LSRM_API lsrm_status lsrm_relpos_forward(const lsrm_relpos_desc* desc, const int
 
 /* Backward of L = sum(out * dout): dq bf16 [Nq][Hq][d], dk, dv bf16 [Nk][Hkv][d], dtable bf16
  * [n_axes][n_buckets][Hq] (all overwritten; dk, dv of keys without queries and the entries of buckets
- * that no pair has are 0).  out and lse are the forward's; dout bf16 [Nq][Hq][d].  All sums have a
+ * that no pair has are 0; rows that belong to no segment are left as they were).  out and lse are the forward's; dout bf16 [Nq][Hq][d].  All sums have a
  * fixed order: results are reproducible bit for bit.  Errors as above. */
 LSRM_API lsrm_status lsrm_relpos_backward(const lsrm_relpos_desc* desc, const int32_t* off_q, const int32_t* off_k,
                                           const int32_t* pos_q, const int32_t* pos_k, const int32_t* bucket_of,
@@ -379,7 +379,7 @@ LSRM_API lsrm_status lsrm_layer_norm_forward(int64_t rows, int32_t width, int32_
                                              float* mean_or_null, float* rstd_or_null, void* stream);
 
 /* Bytes of device workspace of lsrm_layer_norm_backward (any type; nothing in it needs initialising
- * or is kept between calls); 0 for rows < 0 or width < 1. */
+ * or is kept between calls; calls that may overlap on the GPU need one each); 0 for rows < 0 or width < 1. */
 LSRM_API size_t lsrm_layer_norm_workspace_size(int64_t rows, int32_t width);
 
 /* Backward: with xh = (x - mean) rstd and g = dy gamma, dx = rstd (g - mean(g) - xh mean(g xh)),

@@ -259,8 +259,10 @@ def test_differences():
         assert abs(have - want) <= bound + 1e-4 * abs(want), (name, have, want, bound)
 
 
-def test_captured_and_other_stream():
-    c = Case([100, 260], heads=8, kv_heads=2, dim=64)
+@pytest.mark.parametrize("lens_q,lens_k", [([100, 260], None), ([300, 410], None), ([40, 23] * 50, None),
+                                           ([1, 1, 2], [900, 40, 700])])
+def test_captured_and_other_stream(lens_q, lens_k):
+    c = Case(lens_q, lens_k, heads=8, kv_heads=2, dim=64)
     want = {**c.forward()}
     want.update({n: x.clone() for n, x in c.backward(want).items()})
     f = {"out": torch.zeros_like(c.q), "lse": torch.zeros_like(want["lse"])}
@@ -309,6 +311,49 @@ def test_bad_tables_are_reported_not_followed():
     c.forward()
     assert nsa.lsrm_nsa_last_device_status(c.ws) == 5
     assert nsa.lsrm_nsa_last_device_status(c.ws) == 0
+
+
+@pytest.mark.parametrize("lens", [[40, 40], [300, 310, 290], [40, 24, 9] * 30])
+@pytest.mark.parametrize("what", ["off_q", "off_k", "bucket_of", "pos_q", "pos_k"])
+def test_bad_tables_in_every_kernel(lens, what):
+    c = Case(lens, heads=8, kv_heads=2, axes=2, places="scattered")
+    if what == "pos_q":
+        c.pos_q = c.pos_q.clone()  # not the keys' any more
+    x = getattr(c, what)
+    keep = x.clone()
+    if what.startswith("off"):
+        x[1] = 2 ** 31 - 1
+        x[2] = -5
+    elif what == "bucket_of":
+        x[:100] = 32
+        x[150:] = -2 ** 31
+    else:
+        x[3], x[20] = 2 ** 31 - 1, -2 ** 31
+    c.backward(c.forward())
+    assert nsa.lsrm_nsa_last_device_status(c.ws) == 5
+    x.copy_(keep)
+    c.check()
+
+
+def test_two_calls_at_once():
+    cases = [Case([700, 300], heads=8, kv_heads=2), Case([40, 64, 1] * 40, heads=8, kv_heads=2, axes=3, places="bricks")]
+    want = []
+    for c in cases:
+        f = c.forward()
+        want.append({**f, **c.backward(f)})
+    torch.cuda.synchronize()
+    sides = [torch.cuda.Stream() for _ in cases]
+    got = [[] for _ in cases]
+    for _ in range(3):
+        for c, side, g in zip(cases, sides, got):
+            with torch.cuda.stream(side):
+                f = c.forward()
+                g.append({**f, **c.backward(f)})
+    torch.cuda.synchronize()
+    for w, g in zip(want, got):
+        for r in g:
+            for n, x in r.items():
+                assert torch.equal(x, w[n]), n
 
 
 def test_norm_then_attend_then_back():

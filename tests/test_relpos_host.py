@@ -75,6 +75,9 @@ def test_relpos_refusals_before_any_launch(lib):
         assert fwd(d, good[:i] + [None] + good[i + 1:]) == 1, i
     for i in (6, 7, 8, 9):
         assert fwd(d, good[:i] + [24] + good[i + 1:]) == 1, i
+    for i in (0, 1, 2, 3, 4, 10):
+        assert fwd(d, good[:i] + [18] + good[i + 1:]) == 1, i
+    assert fwd(d, good[:5] + [17] + good[6:]) == 1
     assert lib.lsrm_relpos_forward(None, *good, 256, n, None) == 1
     bwd = lambda dd, p, ws=256, size=n: lib.lsrm_relpos_backward(ctypes.byref(dd), *p, ws, size, None)  # noqa: E731
     good = [16] * 16
@@ -83,6 +86,10 @@ def test_relpos_refusals_before_any_launch(lib):
         assert bwd(d, good[:i] + [None] + good[i + 1:]) == 1, i
     for i in (6, 7, 8, 9, 11, 12, 13, 14):
         assert bwd(d, good[:i] + [24] + good[i + 1:]) == 1, i
+    for i in (0, 1, 2, 3, 4, 10):
+        assert bwd(d, good[:i] + [18] + good[i + 1:]) == 1, i
+    for i in (5, 15):
+        assert bwd(d, good[:i] + [17] + good[i + 1:]) == 1, i
     assert lib.lsrm_relpos_workspace_init(ctypes.byref(d), 256, n - 1, None) == 6
 
 
@@ -102,6 +109,9 @@ def test_layer_norm_refusals_before_any_launch(lib):
     good = [16, 16, None, 16, 16, 16, None, None]
     for i in (0, 1, 3, 4, 5):
         assert bwd(4, 8, 0, *(good[:i] + [None] + good[i + 1:]), 256, n, None) == 1, i
+    for i in (3, 4):
+        assert bwd(4, 8, 0, *(good[:i] + [18] + good[i + 1:]), 256, n, None) == 1, i
+    assert fwd(4, 8, 0, 16, None, None, 1e-6, 16, 18, None, None) == 1
     assert bwd(4, 8, 0, *good, None, n, None) == 6 and bwd(4, 8, 0, *good, 256, n - 1, None) == 6
     assert bwd(4, 8, 0, *good, 128, n, None) == 6
 
