@@ -338,10 +338,18 @@ __global__ void __launch_bounds__(kFewThreads) rp_few_kernel(const Params p) {
     const int b = checked_bucket(p, i);
     bk[i] = (uint8_t)(b < 0 ? 255 : b);
   }
+  // the heads' tables, in log2 units when every entry is small or -inf (fill_units)
+  bool mine_small = true;
   for (int i = tid; i < NA * p.NB * GH; i += kFewThreads) {
     const int hh = i % GH;
-    tab[i] = hh < nh ? bf16_to_f32(p.table[(size_t)(i / GH) * p.Hq + h0 + hh]) : 0.0f;
+    const float x = hh < nh ? bf16_to_f32(p.table[(size_t)(i / GH) * p.Hq + h0 + hh]) : 0.0f;
+    mine_small = mine_small && (fabsf(x) <= kSmallBias || x == -INFINITY);
+    tab[i] = x;
   }
+  const bool small = __syncthreads_and(mine_small);
+  if (small)  // every thread scales the entries that it wrote
+    for (int i = tid; i < NA * p.NB * GH; i += kFewThreads) tab[i] *= kLog2e;
+  const float mul = small ? p.scale * kLog2e : p.scale, to_log2 = small ? 1.0f : kLog2e;
 
   // rows g and g + 8: (token, head) pairs
   uint32_t qa[D / 16][4];
@@ -422,7 +430,7 @@ __global__ void __launch_bounds__(kFewThreads) rp_few_kernel(const Params p) {
 #pragma unroll
     for (int n = 0; n < 4; ++n)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) s[n][e] = fmaf(s[n][e], p.scale, ub[e >> 1]);
+      for (int i = 0; i < 2; ++i) ffma2(s[n][2 * i], s[n][2 * i + 1], s[n][2 * i], s[n][2 * i + 1], mul, ub[i]);
 #pragma unroll
     for (int a = 0; a < NA; ++a) {
       if (uni[a] >= 0) continue;
@@ -448,22 +456,26 @@ __global__ void __launch_bounds__(kFewThreads) rp_few_kernel(const Params p) {
     for (int i = 0; i < 2; ++i) {
       float x = fmaxf(s[0][2 * i], s[0][2 * i + 1]);
 #pragma unroll
-      for (int n = 1; n < 4; ++n) x = fmaxf(fmaxf(x, s[n][2 * i]), s[n][2 * i + 1]);
+      for (int n = 1; n < 4; ++n) x = fmax3(x, s[n][2 * i], s[n][2 * i + 1]);
       mx[0][i] = x;
     }
-    move_reference<1, D / 8>(st, o, mx, kLog2e);
+    move_reference<1, D / 8>(st, o, mx, to_log2);
     uint32_t pa[2][4];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const float m = st.m[0][i] == -INFINITY ? 0.0f : st.m[0][i];
-      float sum = 0.0f;
+      float sum0 = 0.0f, sum1 = 0.0f;
 #pragma unroll
-      for (int n = 0; n < 4; ++n) {
-        const float a = ex2((s[n][2 * i] - m) * kLog2e), b = ex2((s[n][2 * i + 1] - m) * kLog2e);
-        sum += a + b;
+      for (int n = 0; n < 4; ++n) {  // the subtraction first: exact for scores of any size
+        float a = s[n][2 * i], b = s[n][2 * i + 1];
+        fadd2_acc(a, b, -m, -m);
+        if (!small) fmul2(a, b, a, b, kLog2e, kLog2e);
+        a = ex2(a);
+        b = ex2(b);
+        fadd2_acc(sum0, sum1, a, b);
         pa[n >> 1][(n & 1) * 2 + i] = pack2(a, b);
       }
-      st.l[0][i] += sum;
+      st.l[0][i] += sum0 + sum1;
     }
 #pragma unroll
     for (int j = 0; j < 2; ++j)
@@ -506,12 +518,13 @@ __global__ void __launch_bounds__(kFewThreads) rp_few_kernel(const Params p) {
 #pragma unroll
     for (int w = 0; w < kFewWarps; ++w) {
       const float mw = jm[w * 16 + r];
-      const float f = mw == -INFINITY && jl[w * 16 + r] == 0.0f ? 0.0f : ex2((mw - m) * kLog2e);
+      const float f = mw == -INFINITY && jl[w * 16 + r] == 0.0f ? 0.0f : ex2((mw - m) * to_log2);
       l = fmaf(f, jl[w * 16 + r], l);
       x = fmaf(f, jo[(w * 16 + r) * D + d], x);
       y = fmaf(f, jo[(w * 16 + r) * D + d + 1], y);
     }
-    const float inv = l == 0.0f ? 0.0f : 1.0f / l, lse = l == 0.0f ? -INFINITY : m + logf(l);
+    const float ref = small ? m * kLn2 : m;
+    const float inv = l == 0.0f ? 0.0f : 1.0f / l, lse = l == 0.0f ? -INFINITY : ref + logf(l);
     const size_t to = (size_t)(row0 + t) * p.Hq + h0 + head;
     if (p.splits == 1) {
       *reinterpret_cast<uint32_t*>(p.out + to * D + d) = pack2(x * inv, y * inv);
@@ -519,7 +532,7 @@ __global__ void __launch_bounds__(kFewThreads) rp_few_kernel(const Params p) {
     } else {
       const size_t pat = (size_t)split * p.Nq * p.Hq + to;
       *reinterpret_cast<float2*>(p.o_part + pat * D + d) = make_float2(x * inv, y * inv);
-      if (d == 0) p.ml_part[pat] = make_float2(m, l);
+      if (d == 0) p.ml_part[pat] = make_float2(ref, l);
     }
   }
 }

@@ -163,11 +163,14 @@ template <int D, int ROWS, int NT>
 __device__ __forceinline__ void load_tile(uint4* dst, const uint16_t* src, int r0, int n_valid, int heads, int h,
                                           int tid) {
   constexpr int kPieces = D / 8;
+  static_assert(NT % kPieces == 0 && ROWS * kPieces % NT == 0, "a thread keeps its column, all have as many rows");
+  const int c = tid % kPieces, step = heads * D;
+  const uint16_t* from = src + ((size_t)r0 * heads + h) * D + c * 8;
 #pragma unroll
-  for (int i = tid; i < ROWS * kPieces; i += NT) {
-    const int r = i / kPieces, c = i % kPieces;
+  for (int i = 0; i < ROWS * kPieces / NT; ++i) {
+    const int r = tid / kPieces + i * (NT / kPieces);
     const bool ok = r < n_valid;
-    cp_async16(dst + piece<D>(r, c), src + ((size_t)(r0 + (ok ? r : 0)) * heads + h) * D + c * 8, ok);
+    cp_async16(dst + piece<D>(r, c), from + (ok ? r * step : 0), ok);  // (65535 heads x 64 x 64 rows fit 32 bits)
   }
 }
 __device__ __forceinline__ void cp_async4(void* smem, const void* gmem, bool pred) {
