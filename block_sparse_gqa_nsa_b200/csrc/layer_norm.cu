@@ -73,6 +73,87 @@ struct LnVec {
   __device__ __forceinline__ void set(int e, float f) { v[e] = ln_from_f32<T>(f); }
 };
 
+// ---- two fp32 values at once: packed f32x2 ----
+// The forward issued 3.1 to 3.2 of 4 instructions a clock and SM without it (head rows of 32: 20.6 -> 18.6 us,
+// hidden rows of 1024: 91 -> 87.7).  The backward waits for its loads (2.5 a clock) and stays scalar: packed, rows
+// of 256 went 117 -> 135 us and rows of 4096 182 -> 202, others within 2%.
+using P2 = uint64_t;
+__device__ __forceinline__ P2 p2(float a, float b) {
+  P2 r;
+  asm("mov.b64 %0, {%1, %2};\n" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ P2 p2_add(P2 a, P2 b) {
+  P2 r;
+  asm("add.rn.f32x2 %0, %1, %2;\n" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ P2 p2_mul(P2 a, P2 b) {
+  P2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;\n" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ P2 p2_fma(P2 a, P2 b, P2 c) {
+  P2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;\n" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ void p2_out(P2 a, float& x, float& y) {
+  asm("mov.b64 {%0, %1}, %2;\n" : "=f"(x), "=f"(y) : "l"(a));
+}
+__device__ __forceinline__ float p2_sum(P2 a) {
+  float x, y;
+  p2_out(a, x, y);
+  return x + y;
+}
+
+// As LnVec, in pairs (a single element's pair is the element and 0): two bf16 of a word are its shifted and
+// its masked half, one instruction each, where an array of 16-bit elements costs two more to take apart.
+template <typename T, int VEC>
+struct LnPairs {
+  static_assert(VEC * sizeof(T) == 16, "16-byte vectors or single elements");
+  static constexpr int kPairs = VEC / 2;
+  uint32_t w[4];
+  __device__ __forceinline__ void load(const T* p) {
+    const uint4 u = *reinterpret_cast<const uint4*>(p);
+    w[0] = u.x, w[1] = u.y, w[2] = u.z, w[3] = u.w;
+  }
+  __device__ __forceinline__ void store(T* p) const {
+    *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+  }
+  __device__ __forceinline__ void zero() { w[0] = w[1] = w[2] = w[3] = 0; }
+  __device__ __forceinline__ P2 get(int e) const {
+    if constexpr (sizeof(T) == 2)
+      return p2(__uint_as_float(w[e] << 16), __uint_as_float(w[e] & 0xffff0000u));
+    else
+      return p2(__uint_as_float(w[2 * e]), __uint_as_float(w[2 * e + 1]));
+  }
+  __device__ __forceinline__ void set(int e, P2 a) {
+    float x, y;
+    p2_out(a, x, y);
+    if constexpr (sizeof(T) == 2) {
+      asm("cvt.rn.bf16x2.f32 %0, %1, %2;\n" : "=r"(w[e]) : "f"(y), "f"(x));
+    } else {
+      w[2 * e] = __float_as_uint(x);
+      w[2 * e + 1] = __float_as_uint(y);
+    }
+  }
+};
+template <typename T>
+struct LnPairs<T, 1> {
+  static constexpr int kPairs = 1;
+  T v;
+  __device__ __forceinline__ void load(const T* p) { v = *p; }
+  __device__ __forceinline__ void store(T* p) const { *p = v; }
+  __device__ __forceinline__ void zero() { v = T(0); }
+  __device__ __forceinline__ P2 get(int) const { return p2(ln_to_f32<T>(v), 0.0f); }
+  __device__ __forceinline__ void set(int, P2 a) {
+    float x, y;
+    p2_out(a, x, y);
+    v = ln_from_f32<T>(x);
+  }
+};
+
 // sum over the TPR threads that share a row: a lane group of a warp, or the whole CTA
 template <int TPR>
 __device__ __forceinline__ float ln_row_sum(float v, float* red) {
@@ -111,7 +192,8 @@ __global__ void __launch_bounds__(kLnThreads) ln_fwd_kernel(const LnFwd p) {
   constexpr int kGroups = kLnThreads / TPR;
   const int sub = threadIdx.x % TPR;
   const long long row0 = (long long)blockIdx.x * (kGroups * R) + threadIdx.x / TPR;
-  LnVec<T, VEC> xv[R][NV];
+  using V = LnPairs<T, VEC>;
+  V xv[R][NV];
 #pragma unroll
   for (int k = 0; k < R; ++k) {
     const long long row = row0 + k * kGroups;
@@ -128,44 +210,50 @@ __global__ void __launch_bounds__(kLnThreads) ln_fwd_kernel(const LnFwd p) {
   float mean[R], rstd[R];
 #pragma unroll
   for (int k = 0; k < R; ++k) {
-    float s = 0.0f;
+    P2 s = p2(0.0f, 0.0f);
 #pragma unroll
     for (int i = 0; i < NV; ++i)
 #pragma unroll
-      for (int e = 0; e < VEC; ++e) s += xv[k][i].get(e);
-    mean[k] = ln_row_sum<TPR>(s, red) / (float)p.C;
+      for (int e = 0; e < V::kPairs; ++e) s = p2_add(s, xv[k][i].get(e));
+    mean[k] = ln_row_sum<TPR>(p2_sum(s), red) / (float)p.C;
   }
 #pragma unroll
   for (int k = 0; k < R; ++k) {
-    float s = 0.0f;
+    P2 s = p2(0.0f, 0.0f);
+    const P2 less = p2(-mean[k], VEC == 1 ? 0.0f : -mean[k]);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       if ((i * TPR + sub) * VEC < p.C) {
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) {
-          const float d = xv[k][i].get(e) - mean[k];
-          s = fmaf(d, d, s);
+        for (int e = 0; e < V::kPairs; ++e) {
+          const P2 d = p2_add(xv[k][i].get(e), less);
+          s = p2_fma(d, d, s);
         }
       }
     }
-    rstd[k] = rsqrtf(ln_row_sum<TPR>(s, red) / (float)p.C + p.eps);
+    rstd[k] = rsqrtf(ln_row_sum<TPR>(p2_sum(s), red) / (float)p.C + p.eps);
   }
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
     const int c = (i * TPR + sub) * VEC;
     if (c >= p.C) continue;
-    LnVec<T, VEC> gv, bv;
+    V gv, bv;
     if (p.gamma != nullptr) gv.load(static_cast<const T*>(p.gamma) + c);
     if (p.beta != nullptr) bv.load(static_cast<const T*>(p.beta) + c);
 #pragma unroll
     for (int k = 0; k < R; ++k) {
       const long long row = row0 + k * kGroups;
       if (row >= p.rows) continue;
+      const P2 less = p2(-mean[k], -mean[k]), by = p2(rstd[k], rstd[k]);
 #pragma unroll
-      for (int e = 0; e < VEC; ++e) {
-        float o = (xv[k][i].get(e) - mean[k]) * rstd[k];
-        if (p.gamma != nullptr) o *= gv.get(e);
-        if (p.beta != nullptr) o += bv.get(e);
+      for (int e = 0; e < V::kPairs; ++e) {
+        P2 o = p2_mul(p2_add(xv[k][i].get(e), less), by);
+        if (p.gamma != nullptr && p.beta != nullptr)
+          o = p2_fma(o, gv.get(e), bv.get(e));
+        else if (p.gamma != nullptr)
+          o = p2_mul(o, gv.get(e));
+        else if (p.beta != nullptr)
+          o = p2_add(o, bv.get(e));
         xv[k][i].set(e, o);
       }
       xv[k][i].store(static_cast<T*>(p.y) + row * p.C + c);
@@ -551,8 +639,8 @@ LnShape ln_shape(int C, int elem, bool vec_ok, bool backward) {
 lsrm_status ln_launched() { return cudaGetLastError() == cudaSuccess ? LSRM_OK : LSRM_ERR_CUDA; }
 
 // Rows a thread group takes at once: two where a thread holds 16 bytes of a row, as long as that still
-// leaves every SM a few CTAs (head rows of 32: one row 24.5 us, two or four 20.6, eight 25.7; four rows of
-// 64 bytes a thread 159 us against 92 with one).
+// leaves every SM a few CTAs (head rows of 32, before the packed sums: one row 24.5 us, two or four 20.6, eight
+// 25.7; four rows of 64 bytes a thread 159 us against 92 with one).
 constexpr int kLnRows = 2;
 // of the backward's CTAs (hidden rows of 1024: two rows 142 us, four 140, eight 183; at least 512 threads
 // an SM: 640 cost spills, 148 -> 164 us)
