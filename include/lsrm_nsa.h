@@ -309,9 +309,10 @@ LSRM_API lsrm_status lsrm_nsa_backward(const lsrm_nsa_desc* desc, const int32_t*
  *   delta_a = clamp(pos_k[j][a] - pos_q[i][a], -D, D)
  *   t[i,h,j] = tau q[i,h] . k[j,g] + sum_a table[a][bucket_of[delta_a + D]][h]
  *   lse[i,h] = log sum_j exp(t[i,h,j]);  out[i,h] = sum_j exp(t[i,h,j] - lse[i,h]) v[j,g]
- * A query whose segment has no key (or whose every t is -inf, by a table entry of -inf) gets out = 0
- * and lse = -inf.  Queries and keys may be the same tensors (self attention: off_q = off_k, pos_q =
- * pos_k) or not: one new token against a long past is a segment of one query. */
+ * A query whose segment has no key (or whose every t is -inf, by a table entry of -inf or biases whose
+ * sum over the axes passes fp32's range) gets out = 0 and lse = -inf.  Queries and keys may be the same
+ * tensors (self attention: off_q = off_k, pos_q = pos_k) or not: one new token against a long past is a
+ * segment of one query. */
 typedef struct {
   int64_t n_q_tokens;   /* Nq, 0..2^31-1 */
   int64_t n_k_tokens;   /* Nk, 0..2^31-1 */
