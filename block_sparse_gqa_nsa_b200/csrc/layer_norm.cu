@@ -18,6 +18,7 @@
 #include <climits>
 #include <type_traits>
 
+#include "dependent.cuh"
 #include "lsrm_common.cuh"
 
 namespace lsrm {
@@ -317,6 +318,7 @@ template <typename T, int VEC, int TPR, int NV, int R>
 __global__ void __launch_bounds__(kLnThreads) ln_bwd_kernel(const LnBwd p) {
   static_assert(TPR <= 32, "a lane group");
   __shared__ float cols[kLnWarps][2][32 * VEC];
+  let_dependents();
   constexpr int kGroups = kLnThreads / TPR;
   const int sub = threadIdx.x % TPR;
   LnVec<T, VEC> gv[NV];
@@ -434,6 +436,7 @@ __global__ void __launch_bounds__(NT, NT < 512 ? 512 / NT : 1) ln_bwd_cta_kernel
   constexpr int kWarps = NT / 32;
   static_assert(2 * R <= 32 && (2 * R & (2 * R - 1)) == 0, "the statistics are folded over the lanes");
   __shared__ float red[2][kWarps][2 * R];
+  let_dependents();
   const int c = threadIdx.x * VEC, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const bool have = c < p.C;
   LnVec<T, VEC> gv;
@@ -582,6 +585,7 @@ template <typename T>
 __global__ void __launch_bounds__(1024) ln_bwd_finish_kernel(const float* part, int n, int C, void* dgamma,
                                                              void* dbeta) {
   __shared__ float s[2][32][33];
+  wait_for_previous();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int c = blockIdx.x * 32 + lane;
   float a = 0.0f, b = 0.0f;
@@ -780,8 +784,10 @@ lsrm_status ln_backward(const LnBwd& p, void* dgamma, void* dbeta, int max_ctas,
     }
   }
   if (dgamma == nullptr && dbeta == nullptr) return LSRM_OK;
-  ln_bwd_finish_kernel<T><<<(unsigned)((p.C + 31) / 32), 1024, 0, s>>>(p.part, n, p.C, dgamma, dbeta);
-  return cudaGetLastError() == cudaSuccess ? LSRM_OK : LSRM_ERR_CUDA;
+  return launch_dependent(ln_bwd_finish_kernel<T>, dim3((unsigned)((p.C + 31) / 32)), 1024, s, (const float*)p.part, n,
+                          p.C, dgamma, dbeta)
+             ? LSRM_OK
+             : LSRM_ERR_CUDA;
 }
 
 }  // namespace

@@ -83,6 +83,7 @@ __global__ void __launch_bounds__(32 * NW, FwdCfg<D, NA, NW>::kMinCtas) rp_fwd_k
   float* lut = reinterpret_cast<float*>(ps + kStages * kChunk * NA);
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, tq = lane & 3;
+  let_dependents();
   int unit = blockIdx.x;
   const int split = unit % p.splits;
   unit /= p.splits;
@@ -303,6 +304,7 @@ __global__ void __launch_bounds__(kFewThreads) rp_few_kernel(const Params p) {
   float* tab = reinterpret_cast<float*>(smem_raw + C::kRing);  // [NA][NB][GH]
   uint8_t* bk = reinterpret_cast<uint8_t*>(tab + NA * p.NB * GH);
 
+  let_dependents();
   int unit = blockIdx.x;
   const int split = unit % p.splits;
   unit /= p.splits;
@@ -549,6 +551,7 @@ __global__ void __launch_bounds__(kJoinThreads) rp_join_kernel(const Params p) {
   const int seg = seg_of_tile(p.off_q, p.S, p.Nq, kJoinRows, blockIdx.x, first);
   seg_bounds(p.off_q, seg, p.Nq, qlo, qhi, p.status);
   const int row0 = qlo + ((int)blockIdx.x - first) * kJoinRows;
+  wait_for_previous();
   if ((int)blockIdx.x < first || row0 >= qhi) return;
   const int rows = min(kJoinRows, qhi - row0);
   const size_t stride = (size_t)p.Nq * p.Hq;
@@ -618,8 +621,9 @@ static lsrm_status run_shape(const Params& p, const FwdPlan& f, cudaStream_t s) 
     return LSRM_ERR_UNSUPPORTED;
   }
   if (st != LSRM_OK || f.splits == 1) return st;
-  rp_join_kernel<D><<<(unsigned)(p.Nq / kJoinRows + p.S), kJoinThreads, 0, s>>>(p);
-  return launched();
+  return launch_dependent(rp_join_kernel<D>, dim3((unsigned)(p.Nq / kJoinRows + p.S)), kJoinThreads, s, p)
+             ? LSRM_OK
+             : LSRM_ERR_CUDA;
 }
 
 }  // namespace rp

@@ -13,6 +13,7 @@
 
 #include <climits>
 
+#include "dependent.cuh"
 #include "tc_ptx.cuh"
 
 namespace lsrm {

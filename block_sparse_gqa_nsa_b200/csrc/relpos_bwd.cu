@@ -292,6 +292,7 @@ __global__ void __launch_bounds__(kBThreads, D == 32 ? 4 : 2) rp_dkv_kernel(cons
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, tq = lane & 3;
   const int bins = NA * p.NB;
+  let_dependents();
   int unit = blockIdx.x;
   const int split = unit % p.splits;
   unit /= p.splits;
@@ -620,6 +621,7 @@ __global__ void __launch_bounds__(kBThreads, D == 32 ? 4 : 2) rp_dkv_kernel(cons
 // dtable = the tiles' sums in order: 32 bins a CTA, 32 runs of tiles, joined in shared memory
 __global__ void __launch_bounds__(1024) rp_table_kernel(const Params p, int tiles, int bins) {
   __shared__ float part[32][33];
+  wait_for_previous();
   const int lane = threadIdx.x & 31, run = threadIdx.x >> 5, h = blockIdx.y, b = blockIdx.x * 32 + lane;
   float x = 0.0f;
   if (b < bins) {
@@ -644,6 +646,8 @@ __global__ void __launch_bounds__(kSumThreads) rp_dkv_join_kernel(const Params p
   const int seg = seg_of_tile(p.off_k, p.S, p.Nk, kSumRows, blockIdx.x, first);
   seg_bounds(p.off_k, seg, p.Nk, klo, khi, p.status);
   const int row0 = klo + ((int)blockIdx.x - first) * kSumRows;
+  wait_for_previous();
+  let_dependents();
   if ((int)blockIdx.x < first || row0 >= khi) return;
   const int n = min(kSumRows, khi - row0) * p.Hkv * D / 4;
   const size_t stride = (size_t)p.Nk * p.Hkv * D;
@@ -703,14 +707,15 @@ static lsrm_status run_bwd(const Params& p, const BwdPlan& b, cudaStream_t s) {
   if (p.Nk > 0) {
     if (!b.tc && (st = run_dkv<D, NA>(p, b, s)) != LSRM_OK) return st;
     if (p.splits > 1) {
-      rp_dkv_join_kernel<D><<<(unsigned)(p.Nk / kSumRows + p.S), kSumThreads, 0, s>>>(p);
-      if ((st = launched()) != LSRM_OK) return st;
+      if (!launch_dependent(rp_dkv_join_kernel<D>, dim3((unsigned)(p.Nk / kSumRows + p.S)), kSumThreads, s, p))
+        return LSRM_ERR_CUDA;
     }
   }
   const int bins = NA * p.NB;
-  rp_table_kernel<<<dim3((unsigned)((bins + 31) / 32), (unsigned)p.Hq), 1024, 0, s>>>(
-      p, p.Nk > 0 ? (int)(b.kv_tiles * b.parts()) : 0, bins);
-  return launched();
+  const int tiles = p.Nk > 0 ? (int)(b.kv_tiles * b.parts()) : 0;
+  return launch_dependent(rp_table_kernel, dim3((unsigned)((bins + 31) / 32), (unsigned)p.Hq), 1024, s, p, tiles, bins)
+             ? LSRM_OK
+             : LSRM_ERR_CUDA;
 }
 
 }  // namespace rp

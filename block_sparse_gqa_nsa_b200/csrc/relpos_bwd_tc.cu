@@ -461,6 +461,7 @@ __global__ void __launch_bounds__(kTcThreads, CTAS)
   float* hist = reinterpret_cast<float*>(boff + top + 1);
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  let_dependents();
   int unit = blockIdx.x;
   const int split = unit % p.splits;
   unit /= p.splits;

@@ -260,7 +260,7 @@ def test_differences():
 
 
 @pytest.mark.parametrize("lens_q,lens_k", [([100, 260], None), ([300, 410], None), ([40, 23] * 50, None),
-                                           ([1, 1, 2], [900, 40, 700])])
+                                           ([1, 1, 2], [900, 40, 700]), ([1, 2], [7000, 5000]), ([600], None)])
 def test_captured_and_other_stream(lens_q, lens_k):
     c = Case(lens_q, lens_k, heads=8, kv_heads=2, dim=64)
     want = {**c.forward()}
