@@ -466,7 +466,7 @@ struct BwdPlan {
   long long dq_tiles, kv_tiles, short_ctas;
   int parts() const { return splits > g ? splits / g : 1; }  // table sums per (key tile, head)
 };
-constexpr int kExactKeys = 256;
+constexpr int kExactKeys = 128;
 
 int bwd_tc_ctas(int D, int NA, int maxd, int nb);  // CTAs of rp_dkv_tc_kernel an SM holds, 0: too large
 
@@ -476,7 +476,7 @@ constexpr int kFewRows = 24;
 
 // Short segments' kernels: while a segment is a tile of queries or so, enough of them fill the GPU, and
 // the tables of a group's heads fit.  Segments of 64 tokens, 32 heads of 32 on 2 KV heads, forward and backward:
-// 64 of them 50 and 213 us, by the kernels of longer segments 35 and 179; 128 of them 53 and 292 against 64 and 306.
+// 64 of them 54 and 154 us, by the kernels of longer segments 37 and 129; 128 of them 56 and 206 against 66 and 214.
 inline bool short_kernels(const lsrm_relpos_desc& d) {
   const long long S = d.n_segs, mean_q = (d.n_q_tokens + S - 1) / S, mean_k = (d.n_k_tokens + S - 1) / S;
   return mean_q <= 64 && mean_k <= 64 && short_tables(d) <= kShTables && 3 * S * d.n_kv_heads >= 4 * kSms;
@@ -507,7 +507,9 @@ inline FwdPlan fwd_plan(const lsrm_relpos_desc& d) {
     f.ctas = (Nq / f.rows + S) * d.n_q_heads;
     busy = ((mean_q + f.rows - 1) / f.rows) * S * d.n_q_heads;
     chunks = (mean_k + 63) / 64;
-    // the CTAs that an SM holds of the 256-row kernel (one token count, 1024: 34 us; twice as many 38)
+    // As many as an SM holds.  Of the 256-row kernel two: 512 queries against 4096 keys, 32 heads of 32, 76 us (one
+    // 110, four 91), 1024 tokens 33 (33, 39); of 64 and 128 rows three: 16 segments of up to 64 queries against 512
+    // keys 41 to 43 us (eight 47 to 52).
     want = (f.rows == 256 ? 2 : 3) * kSms, most = chunks / 4;
   }
   long long sp = busy > 0 && busy < want ? want / busy : 1;
@@ -526,7 +528,12 @@ inline BwdPlan bwd_plan(const lsrm_relpos_desc& d) {
   const long long mean_q = (d.n_q_tokens + S - 1) / S, mean_k = (d.n_k_tokens + S - 1) / S;
   b.g = (int)G;
   b.exact = mean_k <= kExactKeys || mean_q <= 64;
-  b.tc = !b.exact && mean_q > 128 ? bwd_tc_ctas(d.head_dim, d.n_axes, d.max_distance, d.n_buckets) : 0;
+  // From what length 128-row tiles fill up enough, whole backward of eight segments: 16 heads of 64, two axes, 128
+  // tokens 66 us (64-row kernels 59), 192 tokens 51 (101); 32 heads of 32, three axes, 320 tokens 200 us (186), 512
+  // tokens 351 (434).
+  b.tc = !b.exact && mean_q > (d.head_dim == 64 ? 128 : 320)
+             ? bwd_tc_ctas(d.head_dim, d.n_axes, d.max_distance, d.n_buckets)
+             : 0;
   const int rows = b.tc ? 128 : 64;
   b.shrt = short_kernels(d);
   b.short_ctas = short_ctas(d);
@@ -539,7 +546,7 @@ inline BwdPlan bwd_plan(const lsrm_relpos_desc& d) {
     // The time in chunks of work: CTAs that an SM runs one after the other (whole ones while there are few,
     // later they even out) times a CTA's chunks and 2.5 for its beginning and end.  More splits only where they
     // win 2%, as their sums have to be joined.  1024 tokens, 32 heads of 32: 16 splits 178 us, 32 splits 192; 4096
-    // tokens: 16 splits 2247 us, 8 splits 2312; 8 x 320 tokens: 16 splits 205 us, 4 splits 231.
+    // tokens: 16 splits 2247 us, 8 splits 2312; 8 x 320 tokens: 16 splits 205 us, 4 splits 231 (all on three axes).
     double best = 0.0;
     for (long long c = 1; c <= 64 * G && c <= G * (qchunks > 1 ? qchunks : 1); c = c < G ? c + 1 : c + G) {
       if (c < G && G % c) continue;

@@ -9,16 +9,16 @@
 //   * rp_dkv_kernel: keys of one KV head a CTA, the queries of its heads streaming: dk, dv and the
 //     table's gradient.
 // Both passes take 64-row tiles and mma.sync: with segments of up to a few hundred tokens, 128-row tiles of
-// tcgen05 are half empty (8 segments of 192 tokens, 32 heads of 32: 119 us, by relpos_bwd_tc.cu 127; of 512
-// tokens 508 against 418).  Many short segments have a dq pass of their own (relpos_short.cu).  What bounds the
+// tcgen05 are half empty (bwd_plan has the measured borders).  Many short segments have a dq pass of their own (relpos_short.cu).  What bounds the
 // passes is the per-score work (exponential, look-ups, and in the key pass the table's sums: 256 ragged blocks of
-// up to 64 tokens, 32 heads of 32: 132 us, 71M warp instructions at 1.9 a clock), not the tensor pipe (6%).
+// up to 64 tokens, 32 heads of 32: 129 us at 1.8 warp instructions a clock), not the tensor pipe (7%).
 //
 // Delta.  sum_d dO o with the forward's out is off by that output's bf16 rounding, which a gradient
 // that adds up a whole row of dS (the table's) or few keys (short segments) would show.  With D~ that
 // value, the row sum of P (dP - D~) is exactly Delta - D~, so the dq pass adds up what it computes
 // anyway and hands the exact Delta to the key pass.  Its own dq takes the correction - (Delta - D~) P K
-// where segments are short (kExact: one more product); past kExactKeys keys it is below dq's rounding.
+// where segments are short (kExact: one more product).  Delta - D~ is at most 2^-9 of sum |dO o|, and both o and
+// P K are averages over the keys, so past kExactKeys keys the term is a small part of dq's own rounding.
 //
 // The table's gradient: every thread has its own column of NA x buckets sums in shared memory, so
 // the sums need no atomics; a tile that lies on one distance adds its sum once (kept in a register

@@ -407,7 +407,7 @@ __global__ void __launch_bounds__(kTcThreads, 2)
 // axes, one column per axis for the two threads of a key, who work on different axes at any time and change
 // over in turns.  That halves the sums (32 buckets, two axes: 68 -> 34 KB) and lets two CTAs share an SM,
 // which the work behind every score's look-ups needs: dk, dv and table of six frames of 1370 tokens (16 heads
-// of 64, two axes) 698 -> 552 us, 1024 tokens of three axes (32 heads of 32, whole backward) 226 -> 178 us.
+// of 64, two axes) 698 -> 552 us, 1024 tokens of three axes (32 heads of 32, whole backward) 226 -> 192 us.
 // Where two CTAs do not fit in any case, a CTA has the registers of both, own columns and a third stage
 // (64 buckets, whole backward: 987 us; turns without company: 1125 us).
 template <int D, int NA, int CTAS>

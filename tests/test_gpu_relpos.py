@@ -132,6 +132,9 @@ FORWARD = {
     "long_frames": dict(lens_q=[640], dim=64, axes=2, places="frames", maxd=7, buckets=8),
     "long_widest": dict(lens_q=[330], axes=3, maxd=1023, buckets=64, dim=64, places="scattered"),
     "long_odd_buckets": dict(lens_q=[400, 300], axes=3, buckets=7, maxd=9, places="scattered"),
+    "middle64": dict(lens_q=[200, 192, 130, 7], dim=64, axes=2, places="scattered", heads=6, kv_heads=2),
+    "middle32": dict(lens_q=[300, 180, 150, 3], axes=3, places="scattered", maxd=60),
+    "middle_rows": dict(lens_q=[330, 329], lens_k=[129, 140], axes=2, places="scattered"),
     # the key pass with two CTAs an SM and several heads, and where one CTA's sums fill the shared memory
     "long_turns": dict(lens_q=[520, 300], heads=8, kv_heads=2, axes=3, places="scattered", maxd=40),
     "long_turns64": dict(lens_q=[290, 310], heads=6, kv_heads=1, axes=2, places="frames", maxd=20, dim=64),
