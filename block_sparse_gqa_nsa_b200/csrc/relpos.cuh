@@ -459,14 +459,13 @@ struct FwdPlan {
 };
 struct BwdPlan {
   int tc;       // the tensor-memory kernels of 128 rows a CTA: CTAs of the key pass an SM holds, or 0
-  bool exact;   // short segments: the exact Delta in dq as well
   bool shrt;    // short segments' dq kernel
   int splits;   // of the key pass over heads and query chunks: a divisor of G, or a multiple of it
   int g;
   long long dq_tiles, kv_tiles, short_ctas;
   int parts() const { return splits > g ? splits / g : 1; }  // table sums per (key tile, head)
 };
-constexpr int kExactKeys = 128;
+constexpr int kTcKeys = 128;  // tensor-memory kernels of the backward past this many keys
 
 int bwd_tc_ctas(int D, int NA, int maxd, int nb);  // CTAs of rp_dkv_tc_kernel an SM holds, 0: too large
 
@@ -527,11 +526,10 @@ inline BwdPlan bwd_plan(const lsrm_relpos_desc& d) {
   const long long S = d.n_segs, G = d.n_q_heads / d.n_kv_heads;
   const long long mean_q = (d.n_q_tokens + S - 1) / S, mean_k = (d.n_k_tokens + S - 1) / S;
   b.g = (int)G;
-  b.exact = mean_k <= kExactKeys || mean_q <= 64;
   // From what length 128-row tiles fill up enough, whole backward of eight segments: 16 heads of 64, two axes, 128
   // tokens 66 us (64-row kernels 59), 192 tokens 51 (101); 32 heads of 32, three axes, 320 tokens 200 us (186), 512
   // tokens 351 (434).
-  b.tc = !b.exact && mean_q > (d.head_dim == 64 ? 128 : 320)
+  b.tc = mean_k > kTcKeys && mean_q > (d.head_dim == 64 ? 128 : 320)
              ? bwd_tc_ctas(d.head_dim, d.n_axes, d.max_distance, d.n_buckets)
              : 0;
   const int rows = b.tc ? 128 : 64;

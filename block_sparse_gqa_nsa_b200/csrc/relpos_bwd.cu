@@ -16,9 +16,9 @@
 // Delta.  sum_d dO o with the forward's out is off by that output's bf16 rounding, which a gradient
 // that adds up a whole row of dS (the table's) or few keys (short segments) would show.  With D~ that
 // value, the row sum of P (dP - D~) is exactly Delta - D~, so the dq pass adds up what it computes
-// anyway and hands the exact Delta to the key pass.  Its own dq takes the correction - (Delta - D~) P K
-// where segments are short (kExact: one more product).  Delta - D~ is at most 2^-9 of sum |dO o|, and both o and
-// P K are averages over the keys, so past kExactKeys keys the term is a small part of dq's own rounding.
+// anyway and hands the exact Delta to the key pass.  Its own dq takes the correction - (Delta - D~) P K, a product
+// more: in rows with nearly all weight on one key dS nearly cancels, and without it such a row of dq is off by several
+// times its size (512 keys, scores of deviation 8), however many the keys.
 //
 // The table's gradient: every thread has its own column of NA x buckets sums in shared memory, so
 // the sums need no atomics; a tile that lies on one distance adds its sum once (kept in a register
@@ -50,7 +50,7 @@ struct BwdCfg {
   }
 };
 
-template <int D, int NA, bool kExact>
+template <int D, int NA>
 __global__ void __launch_bounds__(kBThreads, D == 32 ? 3 : 2) rp_dq_kernel(const Params p) {
   using C = BwdCfg<D, NA>;
   constexpr int kRows = 64 * MT;
@@ -154,16 +154,13 @@ __global__ void __launch_bounds__(kBThreads, D == 32 ? 3 : 2) rp_dq_kernel(const
       }
       row[mt][i] = small ? l2 : lse[mt][i];
     }
-  float dq[MT][D / 8][4], pk[kExact ? MT : 1][kExact ? D / 8 : 1][4];
+  float dq[MT][D / 8][4], pk[MT][D / 8][4];
 #pragma unroll
   for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
     for (int n = 0; n < D / 8; ++n)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        dq[mt][n][e] = 0.0f;
-        if (kExact) pk[kExact ? mt : 0][kExact ? n : 0][e] = 0.0f;
-      }
+      for (int e = 0; e < 4; ++e) dq[mt][n][e] = pk[mt][n][e] = 0.0f;
 
   for (int c = 0; c < chunks; ++c) {
     cp_async_wait<1>();
@@ -228,7 +225,7 @@ __global__ void __launch_bounds__(kBThreads, D == 32 ? 3 : 2) rp_dq_kernel(const
             }
             p0 = ex2(p0);
             p1 = ex2(p1);
-            if (kExact) pa[mt][n >> 1][(n & 1) * 2 + i] = pack2(p0, p1);
+            pa[mt][n >> 1][(n & 1) * 2 + i] = pack2(p0, p1);
             float d0 = dp[mt][n][2 * i], d1 = dp[mt][n][2 * i + 1];
             fadd2_acc(d0, d1, -delta[mt][i], -delta[mt][i]);
             fmul2(d0, d1, d0, d1, p0, p1);
@@ -247,10 +244,8 @@ __global__ void __launch_bounds__(kBThreads, D == 32 ? 3 : 2) rp_dq_kernel(const
           for (int mt = 0; mt < MT; ++mt) {
             mma16816(dq[mt][dc], sa[mt][j], b);
             mma16816(dq[mt][dc + 1], sa[mt][j], b + 2);
-            if (kExact) {
-              mma16816(pk[kExact ? mt : 0][kExact ? dc : 0], pa[mt][j], b);
-              mma16816(pk[kExact ? mt : 0][kExact ? dc + 1 : 0], pa[mt][j], b + 2);
-            }
+            mma16816(pk[mt][dc], pa[mt][j], b);
+            mma16816(pk[mt][dc + 1], pa[mt][j], b + 2);
           }
         }
     }
@@ -266,14 +261,10 @@ __global__ void __launch_bounds__(kBThreads, D == 32 ? 3 : 2) rp_dq_kernel(const
       if (tq == 0) p.delta[at] = delta[mt][i] + more;
       uint16_t* to = p.dq + at * D + 2 * tq;
 #pragma unroll
-      for (int n = 0; n < D / 8; ++n) {
-        float x = dq[mt][n][2 * i], y = dq[mt][n][2 * i + 1];
-        if (kExact) {
-          x = fmaf(-more, pk[kExact ? mt : 0][kExact ? n : 0][2 * i], x);
-          y = fmaf(-more, pk[kExact ? mt : 0][kExact ? n : 0][2 * i + 1], y);
-        }
-        *reinterpret_cast<uint32_t*>(to + n * 8) = pack2(x * p.scale, y * p.scale);
-      }
+      for (int n = 0; n < D / 8; ++n)
+        *reinterpret_cast<uint32_t*>(to + n * 8) =
+            pack2(fmaf(-more, pk[mt][n][2 * i], dq[mt][n][2 * i]) * p.scale,
+                  fmaf(-more, pk[mt][n][2 * i + 1], dq[mt][n][2 * i + 1]) * p.scale);
     }
 }
 
@@ -675,11 +666,11 @@ static bool allow_smem(K kernel, size_t bytes) {
          cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes) == cudaSuccess;
 }
 
-template <int D, int NA, bool kExact>
+template <int D, int NA>
 static lsrm_status run_dq(const Params& p, const BwdPlan& b, cudaStream_t s) {
   const size_t bytes = BwdCfg<D, NA>::smem_dq(p.maxd);
-  if (!allow_smem(rp_dq_kernel<D, NA, kExact>, bytes)) return LSRM_ERR_CUDA;
-  rp_dq_kernel<D, NA, kExact><<<(unsigned)(b.dq_tiles * p.Hq), kBThreads, bytes, s>>>(p);
+  if (!allow_smem(rp_dq_kernel<D, NA>, bytes)) return LSRM_ERR_CUDA;
+  rp_dq_kernel<D, NA><<<(unsigned)(b.dq_tiles * p.Hq), kBThreads, bytes, s>>>(p);
   return launched();
 }
 template <int D, int NA>
@@ -700,8 +691,7 @@ static lsrm_status run_bwd(const Params& p, const BwdPlan& b, cudaStream_t s) {
     if ((st = launch_bwd_tc(p, D, NA, b, s)) != LSRM_OK) return st;
   }
   if (!b.tc && p.Nq > 0) {
-    st = b.shrt ? launch_short(p, D, NA, b.short_ctas, true, s)
-         : b.exact ? run_dq<D, NA, true>(p, b, s) : run_dq<D, NA, false>(p, b, s);
+    st = b.shrt ? launch_short(p, D, NA, b.short_ctas, true, s) : run_dq<D, NA>(p, b, s);
     if (st != LSRM_OK) return st;
   }
   if (p.Nk > 0) {

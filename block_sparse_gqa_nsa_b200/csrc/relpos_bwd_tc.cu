@@ -3,7 +3,8 @@
 // segments and the joins; relpos_tc.cuh what a thread-per-row layout buys).
 //
 //   * rp_dq_tc_kernel: a tile of 128 queries of one head, keys in chunks of 64:
-//       S = Q K^T, dP = dO V^T (tensor memory) -> dS (bf16, tensor memory) -> dQ += dS K;
+//       S = Q K^T, dP = dO V^T (tensor memory) -> P, dS (bf16, tensor memory) -> dQ += dS K, PK += P K, which
+//       Delta's correction takes;
 //   * rp_dkv_tc_kernel: a tile of 128 keys of one KV head, the queries of its heads in chunks of 64:
 //       S^T = K Q^T, dP^T = V dO^T -> P^T, dS^T (bf16, tensor memory) -> dV += P^T dO, dK += dS^T Q, and
 //       the table's gradient.
@@ -17,9 +18,9 @@
 // Against the mma.sync kernels, which they replace on long segments, the operands need no shared-memory
 // reads by the warps that compute, and runs of columns on one position share look-ups and sums.
 //
-// Tensor memory (256 columns): dq  S 64 | dP 64 | dS 32 | dQ D;  dkv at d = 32  S 64 | dP 64 | P 32 | dS 32 |
-// dV 32 | dK 32, at d = 64  S 64 (P over it) | dP 64 (dS over it) | dV 64 | dK 64, where each half's P lies over
-// that half's own columns and the next scores wait for the products.
+// Tensor memory (256 columns), in both: at d = 32  S 64 | dP 64 | P 32 | dS 32 | two sums of 32 (PK and dQ, dV and dK),
+// at d = 64  S 64 (P over it) | dP 64 (dS over it) | two sums of 64, where each half's P lies over that half's own
+// columns and the next scores wait for the products.
 #include "relpos_tc.cuh"
 
 namespace lsrm {
@@ -98,7 +99,11 @@ __device__ __forceinline__ float huge_row(const Params& p, const float* lut, boo
 template <int D>
 struct DqTc : TcTile<D> {
   static constexpr int kStages = 3;
-  static constexpr int kColS = 0, kColDp = 64, kColDs = 128, kColDq = 160;
+  static constexpr bool kAlias = D == 64;
+  static constexpr int kColS = 0, kColDp = 64;
+  static constexpr int kColP = kAlias ? 0 : 128, kColDs = kAlias ? 64 : 160;
+  static constexpr int kHalf = kAlias ? 32 : 16;  // columns from one half's operand to the other's
+  static constexpr int kColPk = kAlias ? 128 : 192, kColDq = kColPk + D;
   static_assert(kColDq + D <= 256, "tensor memory");
 };
 template <int D, int NA>
@@ -225,12 +230,17 @@ __global__ void __launch_bounds__(kTcThreads, 2)
           mma_ss(tmem + C::kColDp + 32 * hf, odesc + 2 * i, vdesc + at + 2 * i, C::kIdescHalf, i > 0 ? 1u : 0u);
         mma_commit(&S.s_full[hf]);
       };
-      auto issue_dq = [&](int c, int hf) {
+      auto issue_sums = [&](int c, int hf) {
         const uint64_t at = (uint64_t)((c % C::kStages) * kStep + hf * kHalfStep);
+        const uint32_t first_add = c == 0 && hf == 0 ? 0u : 1u;
 #pragma unroll
         for (int i = 0; i < 2; ++i)
-          mma_ts(tmem + C::kColDq, tmem + C::kColDs + hf * 16 + i * 8, ksum + at + i * (16 * C::kRowBytes >> 4),
-                 C::kIdescSum, (c == 0 && hf == 0 && i == 0) ? 0u : 1u);
+          mma_ts(tmem + C::kColPk, tmem + C::kColP + hf * C::kHalf + i * 8, ksum + at + i * (16 * C::kRowBytes >> 4),
+                 C::kIdescSum, i == 0 ? first_add : 1u);
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+          mma_ts(tmem + C::kColDq, tmem + C::kColDs + hf * C::kHalf + i * 8, ksum + at + i * (16 * C::kRowBytes >> 4),
+                 C::kIdescSum, i == 0 ? first_add : 1u);
         mma_commit(&S.done[hf]);
       };
       for (int c = 0; ok && c < chunks; ++c) {
@@ -238,15 +248,24 @@ __global__ void __launch_bounds__(kTcThreads, 2)
         for (int hf = 0; hf < 2; ++hf) {
           if (c > 0 && !wait_bar(&S.p_full[hf], (c - 1) & 1, abort, p.status)) { ok = false; break; }
           tc_fence_after();
-          issue_scores(c, hf);  // S and dP were released with dS(c - 1)
-          if (c > 0) issue_dq(c - 1, hf);
+          if (!C::kAlias) issue_scores(c, hf);  // S and dP were released with dS(c - 1)
+          if (c > 0) issue_sums(c - 1, hf);
         }
-        if (ok && c > 0) mma_commit(&S.kv_empty[(c - 1) % C::kStages]);
+        if (!ok) break;
+        if (c > 0) mma_commit(&S.kv_empty[(c - 1) % C::kStages]);
+        if (C::kAlias) {
+          for (int hf = 0; hf < 2; ++hf) {
+            // the next scores overwrite the operands of the products, so those have to be done
+            if (c > 0 && !wait_bar(&S.done[hf], (c - 1) & 1, abort, p.status)) { ok = false; break; }
+            tc_fence_after();
+            issue_scores(c, hf);
+          }
+        }
       }
       for (int hf = 0; ok && hf < 2; ++hf) {
         if (!wait_bar(&S.p_full[hf], (chunks - 1) & 1, abort, p.status)) { ok = false; break; }
         tc_fence_after();
-        issue_dq(chunks - 1, hf);
+        issue_sums(chunks - 1, hf);
       }
       // every MMA issued so far must finish before the CTA can release tensor and shared memory
       mma_commit(&S.drain);
@@ -307,7 +326,7 @@ __global__ void __launch_bounds__(kTcThreads, 2)
       const int st = c % C::kStages, left = khi - klo - c * kTcCols;
       if (!wait_bar_w(&S.kv_full[st], (c / C::kStages) & 1, abort, p.status) ||
           !wait_bar_w(&S.s_full[half], c & 1, abort, p.status) ||
-          (c > 0 && !wait_bar_w(&S.done[half], (c - 1) & 1, abort, p.status))) {  // dS is free
+          (!C::kAlias && c > 0 && !wait_bar_w(&S.done[half], (c - 1) & 1, abort, p.status))) {  // P and dS are free
         ok = false;
         break;
       }
@@ -333,28 +352,27 @@ __global__ void __launch_bounds__(kTcThreads, 2)
 #pragma unroll
           for (int e = 0; e < 16; ++e) x[e] = fmaf(x[e] - rconst, kLog2e, -corr);
         }
+        if (left < col + 16) {  // no key: P = 0, and dP may be anything
+          keep_branch();
+#pragma unroll
+          for (int e = 0; e < 16; ++e)
+            if (col + e >= left) x[e] = -INFINITY, d[e] = 0;
+        }
         float s0 = 0.0f, s1 = 0.0f;
+        uint32_t pp[8], pd[8];
 #pragma unroll
         for (int e = 0; e < 16; e += 2) {
           const float p0 = ex2(x[e]), p1 = ex2(x[e + 1]);
           float d0 = __uint_as_float(d[e]), d1 = __uint_as_float(d[e + 1]);
           fadd2_acc(d0, d1, -delta, -delta);
-          fmul2(x[e], x[e + 1], d0, d1, p0, p1);
-        }
-        if (left < col + 16) {
-          keep_branch();
-#pragma unroll
-          for (int e = 0; e < 16; ++e)
-            if (col + e >= left) x[e] = 0.0f;
-        }
-        uint32_t pk[8];
-#pragma unroll
-        for (int e = 0; e < 16; e += 2) {
-          fadd2_acc(s0, s1, x[e], x[e + 1]);
-          pk[e / 2] = pack2(x[e], x[e + 1]);
+          fmul2(d0, d1, d0, d1, p0, p1);
+          fadd2_acc(s0, s1, d0, d1);
+          pp[e / 2] = pack2(p0, p1);
+          pd[e / 2] = pack2(d0, d1);
         }
         rest += s0 + s1;
-        tmem_st8(tbase + C::kColDs + half * 16 + g * 8, pk);
+        tmem_st8(tbase + C::kColP + half * C::kHalf + g * 8, pp);
+        tmem_st8(tbase + C::kColDs + half * C::kHalf + g * 8, pd);
       }
       tmem_st_wait();
       tc_fence_before();
@@ -366,27 +384,32 @@ __global__ void __launch_bounds__(kTcThreads, 2)
     tc_fence_after();
     S.rest[half][r] = rest;
     ok = eb.sync() && ok;
+    const float more = S.rest[0][r] + S.rest[1][r];  // Delta less the one of the saved out
     if (half == 0 && valid) {
-      p.delta[at] = delta + S.rest[0][r] + S.rest[1][r];
+      p.delta[at] = delta + more;
       p.lse2[at] = l2;
       p.corr[at] = corr;
     }
     // each thread half of the row's dq
 #pragma unroll 1
     for (int i = 0; i < D / 32; ++i) {
-      uint32_t o[16];
+      uint32_t o[16], k[16];
       const int col = half * (D / 2) + i * 16;
 #pragma unroll
-      for (int e = 0; e < 16; ++e) o[e] = 0;
+      for (int e = 0; e < 16; ++e) o[e] = k[e] = 0;
       if (ok && chunks > 0) {
         tmem_ld16(tbase + C::kColDq + col, o);
         tmem_wait16(o);
+        tmem_ld16(tbase + C::kColPk + col, k);
+        tmem_wait16(k);
       }
       if (!valid) continue;
+      float x[16];
+#pragma unroll
+      for (int e = 0; e < 16; ++e) x[e] = fmaf(-more, __uint_as_float(k[e]), __uint_as_float(o[e])) * p.scale;
       uint32_t u[8];
 #pragma unroll
-      for (int e = 0; e < 8; ++e)
-        u[e] = pack2(__uint_as_float(o[2 * e]) * p.scale, __uint_as_float(o[2 * e + 1]) * p.scale);
+      for (int e = 0; e < 8; ++e) u[e] = pack2(x[2 * e], x[2 * e + 1]);
       uint4* dst = reinterpret_cast<uint4*>(p.dq + at * D + col);
       dst[0] = make_uint4(u[0], u[1], u[2], u[3]);
       dst[1] = make_uint4(u[4], u[5], u[6], u[7]);
