@@ -185,7 +185,7 @@ __global__ void __launch_bounds__(32 * NW, FwdCfg<D, NA, NW>::kMinCtas) rp_fwd_k
       for (int a = 0; a < NA; ++a)
         mode[a] = axis_mode<NA>(pt + kb * NA + a, q_lo[a], q_hi[a], false, p.maxd, lane, one[a], p.status);
       float base[2][2];
-      const bool fold = add_bias<NA, 2, 1>(s, base, mode, one, pt + kb * NA, lut, top, qp, mul, small, tq);
+      const bool fold = add_bias<NA, 2, 1>(s, base, mode, one, pt + kb * NA, lut, top, qp, mul, !small, tq);
       if (left < kCols) {
         keep_branch();
 #pragma unroll
@@ -424,7 +424,7 @@ __global__ void __launch_bounds__(kFewThreads) rp_few_kernel(const Params p) {
       if (lo < -kPosLimit || hi > kPosLimit) raise_status(p.status, LSRM_ERR_BOUNDS);
       const int near = clamp_index(lo - q_hi[a], p.maxd, top), far = clamp_index(hi - q_lo[a], p.maxd, top);
       uni[a] = near == far ? near : -1;
-      if (uni[a] >= 0) {
+      if (uni[a] >= 0 && small) {
         ub[0] += bias_at(a, uni[a], hh[0]);
         ub[1] += bias_at(a, uni[a], hh[1]);
       }
@@ -435,7 +435,7 @@ __global__ void __launch_bounds__(kFewThreads) rp_few_kernel(const Params p) {
       for (int i = 0; i < 2; ++i) ffma2(s[n][2 * i], s[n][2 * i + 1], s[n][2 * i], s[n][2 * i + 1], mul, ub[i]);
 #pragma unroll
     for (int a = 0; a < NA; ++a) {
-      if (uni[a] >= 0) continue;
+      if (uni[a] >= 0 && small) continue;
 #pragma unroll
       for (int n = 0; n < 4; ++n)
 #pragma unroll

@@ -62,11 +62,15 @@ __device__ __forceinline__ void ffma2v(float& r0, float& r1, float a0, float a1,
 // In a rarely taken branch: keeps it a branch, where the compiler would rather do both sides and select
 __device__ __forceinline__ void keep_branch() { asm volatile("" ::: "memory"); }
 
-// A bias folds into the exponent's multiply-add only while it is small beside fp32's spacing: past this
-// a score is added to it first, so that scores the addition swallows (a mask of the type's lowest value)
-// count as equal, as they do in the formula's own order.  kFoldLimit is also the size of LSE where its
-// own fp32 spacing (2^-10 at 1e4) begins to lose the logarithm of the row's sum, so the backward
-// normalises such rows anew.
+// A bias folds into the exponent's multiply-add, in whatever order is cheapest, only while scores are small
+// beside fp32's spacing.  Tables with larger entries than kSmallBias (a mask of the type's lowest value), and in the
+// backward rows whose |LSE| reaches kFoldLimit (spacing 2^-10), take the exact path: t = ((s scale) + b_0) + b_1 + b_2
+// in the formula's own order, so that both backward passes have the same t bit for bit, whatever their tiles have in
+// common, and the row's reference subtracted from it before anything else.
+//
+// LSE itself loses the logarithm of a row's sum beside a large score.  So the backward's weights are
+// exp(t - lse) / sum_j exp(t - lse): the dq pass adds the sums up beside its products and hands their log2 (corr) to
+// the key pass.
 constexpr float kFoldLimit = 1e4f;
 constexpr float kSmallBias = 64.0f;  // per axis: three axes in log2 units keep a spacing of 2^-15
 
@@ -92,7 +96,7 @@ struct Params {
   float* delta;  // backward: Delta per (query, head)
   float* tab_part;  // backward: table gradient per (key tile, part of its queries, head)
   float* kv_part;   // backward: dK / dV per split
-  float* corr;      // backward: log2 of what exp(t - lse) sums to per (query, head), 0 for all but huge |lse|
+  float* corr;      // backward: log2 of what exp(t - lse) sums to per (query, head)
   float* lse2;      // backward: lse in log2 units with corr, +inf for a row without keys
   float* o_part;    // forward: output per key split, and its softmax reference and sum
   float2* ml_part;
@@ -275,34 +279,36 @@ __device__ __forceinline__ bool fill_units(const Params& p, float* lut, int h, i
 }
 
 // The bias of a lane's MT x 2 rows by 8 columns, in the table's units.  What is constant per row goes
-// to base; when that is all and the table folds, returns true and leaves the scores raw.  Otherwise the
-// scores become s * mul + bias.  SIGN: column positions count up (+1, columns are keys: rowc = maxd - pos_q)
-// or down (-1, columns are queries: rowc = maxd + pos_k).
+// to base; when that is all, returns true and leaves the scores raw.  Otherwise the scores become
+// s * mul + bias; `exact`: in the formula's own order, whatever the modes, and base is 0.  SIGN: column positions
+// count up (+1, columns are keys: rowc = maxd - pos_q) or down (-1, columns are queries: rowc = maxd + pos_k).
 template <int NA, int MT, int SIGN>
 __device__ __forceinline__ bool add_bias(float (&s)[MT][kGroups][4], float (&base)[MT][2], const int (&mode)[NA],
                                          const int (&one)[NA], const int* xs, const float* lut, int top,
-                                         const int (&rowc)[MT][2][NA], float mul, bool fold, int tq) {
+                                         const int (&rowc)[MT][2][NA], float mul, bool exact, int tq) {
   const int* mine = xs + tq * kLaneCols * NA;
   int worst = kOne;
   float ub = 0.0f;
 #pragma unroll
   for (int a = 0; a < NA; ++a) {
     worst = max(worst, mode[a]);
-    if (mode[a] == kOne) ub += lut[a * (top + 1) + one[a]];
+    if (mode[a] == kOne && !exact) ub += lut[a * (top + 1) + one[a]];
   }
 #pragma unroll
   for (int mt = 0; mt < MT; ++mt) base[mt][0] = base[mt][1] = ub;
-  if (worst == kOne && fold) return true;
+  if (!exact) {
+    if (worst == kOne) return true;
 #pragma unroll
-  for (int a = 0; a < NA; ++a) {
-    if (mode[a] != kLane) continue;
-    const int x = SIGN * mine[a];
+    for (int a = 0; a < NA; ++a) {
+      if (mode[a] != kLane) continue;
+      const int x = SIGN * mine[a];
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt)
+      for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-      for (int i = 0; i < 2; ++i) base[mt][i] += lut[a * (top + 1) + clamp_index(x, rowc[mt][i][a], top)];
+        for (int i = 0; i < 2; ++i) base[mt][i] += lut[a * (top + 1) + clamp_index(x, rowc[mt][i][a], top)];
+    }
+    if (worst <= kLane) return true;
   }
-  if (worst <= kLane && fold) return true;
 #pragma unroll
   for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
@@ -352,42 +358,38 @@ __device__ __forceinline__ bool add_bias(float (&s)[MT][kGroups][4], float (&bas
             s[mt][n][2 * i + 1] += la[clamp_index(x1, rowc[mt][i][a], top)];
           }
       }
+    } else if (exact) {  // (otherwise in base)
+      keep_branch();
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const float b = la[mode[a] == kOne ? one[a] : clamp_index(SIGN * mine[a], rowc[mt][i][a], top)];
+#pragma unroll
+          for (int n = 0; n < kGroups; ++n) s[mt][n][2 * i] += b, s[mt][n][2 * i + 1] += b;
+        }
     }
   }
   return false;
 }
 
 // ---- backward ----
-// Rows whose |LSE| is so large that fp32 lost the logarithm of their sum beside the largest score
-// (every key masked by a huge finite bias): corr = log2 sum_j exp(t - lse), a row at a time, lanes over
-// keys.  The tile's rows are wrow .. wrow + 15; lane (g, .) holds the LSE of rows g and g + 8.  Inline, rare as it
-// is: around a call the kernels kept registers in local memory (dq of 256 ragged blocks 118 -> 89 us).
-template <int D, int NA>
-__device__ __forceinline__ float2 huge_rows(const Params& p, const float* lut, bool small, float lse0, float lse1,
-                                         int wrow, int h, int hk, int klo, int khi, int lane) {
-  const float units = small ? kLn2 : 1.0f;  // the table's to natural ones
-  float2 corr = make_float2(0.0f, 0.0f);
-  for (int r = 0; r < 16; ++r) {
-    const float l = __shfl_sync(0xffffffffu, r < 8 ? lse0 : lse1, (r & 7) * 4);
-    if (!(fabsf(l) >= kFoldLimit) || l == INFINITY) continue;
-    const size_t row = wrow + r;
-    const uint16_t* q = p.q + (row * p.Hq + h) * D;
-    float sum = 0.0f;
-    for (int j = klo + lane; j < khi; j += 32) {
-      const uint16_t* k = p.k + ((size_t)j * p.Hkv + hk) * D;
-      float t = 0.0f;
-      for (int d = 0; d < D; ++d) t = fmaf(bf16_to_f32(q[d]), bf16_to_f32(k[d]), t);
-      t *= p.scale;
-      for (int a = 0; a < NA; ++a)
-        t += units * lut[a * (2 * p.maxd + 1) + clamp_index(p.pos_k[(size_t)j * NA + a],
-                                                            p.maxd - p.pos_q[row * NA + a], 2 * p.maxd)];
-      sum += ex2((t - l) * kLog2e);
-    }
-    __syncwarp();
-    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    if ((lane >> 2) == (r & 7)) (r < 8 ? corr.x : corr.y) = log2f(sum);
-  }
-  return corr;
+// the LSE that the exponents take: a row without keys has P = 0
+__device__ __forceinline__ float row_lse(float lse) { return lse == -INFINITY ? INFINITY : lse; }
+// the row constant of the scores' units, subtracted from them in the exact path.  (Rounded by itself: both passes
+// need the same number.)
+__device__ __forceinline__ float row_const(float lse, bool small) { return small ? __fmul_rn(lse, kLog2e) : lse; }
+__device__ __forceinline__ bool is_huge(float x) { return fabsf(x) >= kFoldLimit && x != INFINITY; }
+// 1 / l of a row's weights exp(t - lse), 0 for a row without keys.  A sum that left fp32's range means that lse is not
+// the forward's, or that scores are so large (past 2^27, where the two passes' own roundings of one score, a few times
+// 2^-24 of it, differ by tens) that it says nothing about them.
+__device__ __forceinline__ float row_inverse(float l, float row, uint32_t* status) {
+  if ((l == 0.0f || l == INFINITY) && fabsf(row) < INFINITY) raise_status(status, LSRM_ERR_BOUNDS);
+  return l == 0.0f ? 0.0f : 1.0f / l;
+}
+__device__ __forceinline__ float row_corr(float l) { return l == 0.0f ? 0.0f : log2f(l); }
+__device__ __forceinline__ float row_lse2(float row, bool small, float corr) {
+  return small ? row + corr : fmaf(row, kLog2e, corr);
 }
 
 // Two sums into a column of the table's gradient (byte offsets of the buckets' entries) with both reads ahead

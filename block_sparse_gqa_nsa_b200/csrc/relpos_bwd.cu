@@ -87,7 +87,7 @@ __global__ void __launch_bounds__(kBThreads, D == 32 ? 3 : 2) rp_dq_kernel(const
 
   uint32_t qa[MT][D / 16][4], da[MT][D / 16][4];
   int qp[MT][2][NA], q_lo[NA], q_hi[NA];
-  float lse[MT][2], delta[MT][2], corr[MT][2], rest[MT][2];
+  float delta[MT][2], rest[MT][2], l[MT][2], row[MT][2];
   const int wrow = row0 + warp * 16 * MT;
 #pragma unroll
   for (int a = 0; a < NA; ++a) q_lo[a] = INT32_MAX, q_hi[a] = INT32_MIN;
@@ -114,10 +114,10 @@ __global__ void __launch_bounds__(kBThreads, D == 32 ? 3 : 2) rp_dq_kernel(const
     for (int i = 0; i < 2; ++i) {
       const int ri = r + 8 * i;
       delta[mt][i] = quad_sum(delta[mt][i]);
-      corr[mt][i] = rest[mt][i] = 0.0f;
-      lse[mt][i] = ri < qhi ? p.lse_in[(size_t)ri * p.Hq + h] : INFINITY;
-      if (lse[mt][i] == -INFINITY) lse[mt][i] = INFINITY;  // a row without keys: P = 0
-      huge = huge || (fabsf(lse[mt][i]) >= kFoldLimit && lse[mt][i] != INFINITY);
+      rest[mt][i] = l[mt][i] = 0.0f;
+      const float lse = row_lse(ri < qhi ? p.lse_in[(size_t)ri * p.Hq + h] : INFINITY);
+      huge = huge || is_huge(lse);
+      row[mt][i] = row_const(lse, small);
 #pragma unroll
       for (int a = 0; a < NA; ++a) {
         const int x = p.pos_q[(size_t)min(ri, qhi - 1) * NA + a];
@@ -133,27 +133,7 @@ __global__ void __launch_bounds__(kBThreads, D == 32 ? 3 : 2) rp_dq_kernel(const
     q_hi[a] = __reduce_max_sync(0xffffffffu, q_hi[a]);
     if (q_lo[a] < -kPosLimit || q_hi[a] > kPosLimit) raise_status(p.status, LSRM_ERR_BOUNDS);
   }
-  if (__any_sync(0xffffffffu, huge)) {
-#pragma unroll
-    for (int mt = 0; mt < MT; ++mt) {
-      const float2 x = huge_rows<D, NA>(p, lut, small, lse[mt][0], lse[mt][1], wrow + mt * 16, h, hk, klo, khi, lane);
-      corr[mt][0] = x.x, corr[mt][1] = x.y;
-    }
-  }
-  // the exponent's row constant: log2 units with the correction, or natural ones without it
-  float row[MT][2];
-#pragma unroll
-  for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const float l2 = fmaf(lse[mt][i], kLog2e, corr[mt][i]);
-      const int r = wrow + mt * 16 + g + 8 * i;
-      if (r < qhi && tq == 0) {
-        p.lse2[(size_t)r * p.Hq + h] = l2;
-        p.corr[(size_t)r * p.Hq + h] = corr[mt][i];
-      }
-      row[mt][i] = small ? l2 : lse[mt][i];
-    }
+  const bool exact = !small || __any_sync(0xffffffffu, huge);
   float dq[MT][D / 8][4], pk[MT][D / 8][4];
 #pragma unroll
   for (int mt = 0; mt < MT; ++mt)
@@ -196,7 +176,7 @@ __global__ void __launch_bounds__(kBThreads, D == 32 ? 3 : 2) rp_dq_kernel(const
       for (int a = 0; a < NA; ++a)
         mode[a] = axis_mode<NA>(pt + a, q_lo[a], q_hi[a], false, p.maxd, lane, one[a], p.status);
       float base[MT][2];
-      const bool fold = add_bias<NA, MT, 1>(s, base, mode, one, pt, lut, top, qp, mul, small, tq);
+      const bool fold = add_bias<NA, MT, 1>(s, base, mode, one, pt, lut, top, qp, mul, exact, tq);
       if (left < kCols) {
         keep_branch();
 #pragma unroll
@@ -213,7 +193,7 @@ __global__ void __launch_bounds__(kBThreads, D == 32 ? 3 : 2) rp_dq_kernel(const
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           const float cst = base[mt][i] - row[mt][i];
-          float sum0 = 0.0f, sum1 = 0.0f;
+          float sum0 = 0.0f, sum1 = 0.0f, l0 = 0.0f, l1 = 0.0f;
 #pragma unroll
           for (int n = 0; n < kGroups; ++n) {
             float p0 = s[mt][n][2 * i], p1 = s[mt][n][2 * i + 1];
@@ -221,10 +201,11 @@ __global__ void __launch_bounds__(kBThreads, D == 32 ? 3 : 2) rp_dq_kernel(const
               ffma2(p0, p1, p0, p1, mul, cst);
             } else {  // the subtraction first: exact for scores of any size
               fadd2_acc(p0, p1, -row[mt][i], -row[mt][i]);
-              if (!small) ffma2(p0, p1, p0, p1, kLog2e, -corr[mt][i]);
+              if (!small) fmul2(p0, p1, p0, p1, kLog2e, kLog2e);
             }
             p0 = ex2(p0);
             p1 = ex2(p1);
+            fadd2_acc(l0, l1, p0, p1);
             pa[mt][n >> 1][(n & 1) * 2 + i] = pack2(p0, p1);
             float d0 = dp[mt][n][2 * i], d1 = dp[mt][n][2 * i + 1];
             fadd2_acc(d0, d1, -delta[mt][i], -delta[mt][i]);
@@ -233,6 +214,7 @@ __global__ void __launch_bounds__(kBThreads, D == 32 ? 3 : 2) rp_dq_kernel(const
             sa[mt][n >> 1][(n & 1) * 2 + i] = pack2(d0, d1);
           }
           rest[mt][i] += sum0 + sum1;
+          l[mt][i] += l0 + l1;
         }
 #pragma unroll
       for (int j = 0; j < 2; ++j)
@@ -254,17 +236,23 @@ __global__ void __launch_bounds__(kBThreads, D == 32 ? 3 : 2) rp_dq_kernel(const
   for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      const float more = quad_sum(rest[mt][i]);  // Delta - D~
+      const float sum = quad_sum(l[mt][i]), parts = quad_sum(rest[mt][i]);
       const int r = wrow + mt * 16 + g + 8 * i;
       if (r >= qhi) continue;
+      const float inv = row_inverse(sum, row[mt][i], p.status), corr = row_corr(sum);
+      const float more = parts * inv, f = inv * p.scale;  // more: Delta - D~
       const size_t at = (size_t)r * p.Hq + h;
-      if (tq == 0) p.delta[at] = delta[mt][i] + more;
+      if (tq == 0) {
+        p.delta[at] = delta[mt][i] + more;
+        p.lse2[at] = row_lse2(row[mt][i], small, corr);
+        p.corr[at] = corr;
+      }
       uint16_t* to = p.dq + at * D + 2 * tq;
 #pragma unroll
       for (int n = 0; n < D / 8; ++n)
         *reinterpret_cast<uint32_t*>(to + n * 8) =
-            pack2(fmaf(-more, pk[mt][n][2 * i], dq[mt][n][2 * i]) * p.scale,
-                  fmaf(-more, pk[mt][n][2 * i + 1], dq[mt][n][2 * i + 1]) * p.scale);
+            pack2(fmaf(-more, pk[mt][n][2 * i], dq[mt][n][2 * i]) * f,
+                  fmaf(-more, pk[mt][n][2 * i + 1], dq[mt][n][2 * i + 1]) * f);
     }
 }
 
@@ -392,6 +380,8 @@ __global__ void __launch_bounds__(kBThreads, D == 32 ? 4 : 2) rp_dkv_kernel(cons
     const int st = it % kKeyStages;
     const uint4* qt = qs + st * C::kTile;
     const uint4* dt = ds + st * C::kTile;
+    const float* lc = ls + st * 2 * kBChunk;
+    const bool exact = !small || __any_sync(0xffffffffu, is_huge(lc[lane]) || is_huge(lc[lane + 32]));
 #pragma unroll 1
     for (int qb = 0; qb < kBChunk; qb += kCols) {
       const int left = nq - (c0 + cc) * kBChunk - qb;
@@ -421,7 +411,7 @@ __global__ void __launch_bounds__(kBThreads, D == 32 ? 4 : 2) rp_dkv_kernel(cons
       for (int a = 0; a < NA; ++a)
         mode[a] = axis_mode<NA>(pt + a, k_lo[a], k_hi[a], true, p.maxd, lane, one[a], p.status);
       float base[MT][2];
-      const bool fold = add_bias<NA, MT, -1>(s, base, mode, one, pt, lut, top, kp, mul, small, tq);
+      const bool fold = add_bias<NA, MT, -1>(s, base, mode, one, pt, lut, top, kp, mul, exact, tq);
       bool flat = true;  // one bias for the tile
 #pragma unroll
       for (int a = 0; a < NA; ++a) flat = flat && mode[a] == kOne;
@@ -435,7 +425,7 @@ __global__ void __launch_bounds__(kBThreads, D == 32 ? 4 : 2) rp_dkv_kernel(cons
           if (tq * kLaneCols + 2 * n >= left) l.x = INFINITY;
           if (tq * kLaneCols + 2 * n + 1 >= left) l.y = INFINITY;
         }
-        if (small) {
+        if (!exact) {
           if (fold) {
             const float c0 = flat ? base[0][0] - l.x : -l.x, c1 = flat ? base[0][0] - l.y : -l.y;
 #pragma unroll
@@ -453,7 +443,8 @@ __global__ void __launch_bounds__(kBThreads, D == 32 ? 4 : 2) rp_dkv_kernel(cons
               for (int i = 0; i < 2; ++i) fadd2_acc(s[mt][n][2 * i], s[mt][n][2 * i + 1], -l.x, -l.y);
           }
         } else {
-          // natural units, the subtraction first: exact for scores of any size
+          // the row's constant and the correction one after the other: together they would be rounded to the former's
+          // spacing
           keep_branch();
           float ln[2], cr[2];
 #pragma unroll
@@ -461,8 +452,7 @@ __global__ void __launch_bounds__(kBThreads, D == 32 ? 4 : 2) rp_dkv_kernel(cons
             const bool there = tq * kLaneCols + 2 * n + e < left;
             const int col = there ? tq * kLaneCols + 2 * n + e : 0;
             const size_t at = (size_t)(qlo + (c0 + cc) * kBChunk + qb + col) * p.Hq + hk * p.G + head;
-            ln[e] = there ? p.lse_in[at] : INFINITY;
-            if (ln[e] == -INFINITY) ln[e] = INFINITY;
+            ln[e] = row_const(there ? row_lse(p.lse_in[at]) : INFINITY, small);
             cr[e] = there ? p.corr[at] : 0.0f;
           }
 #pragma unroll
@@ -470,8 +460,10 @@ __global__ void __launch_bounds__(kBThreads, D == 32 ? 4 : 2) rp_dkv_kernel(cons
 #pragma unroll
             for (int i = 0; i < 2; ++i)
 #pragma unroll
-              for (int e = 0; e < 2; ++e)
-                s[mt][n][2 * i + e] = fmaf(s[mt][n][2 * i + e] - ln[e], kLog2e, -cr[e]);
+              for (int e = 0; e < 2; ++e) {
+                const float x = s[mt][n][2 * i + e] - ln[e];
+                s[mt][n][2 * i + e] = small ? x - cr[e] : fmaf(x, kLog2e, -cr[e]);
+              }
         }
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt)

@@ -72,28 +72,6 @@ __device__ __forceinline__ bool ew_fill(const Params& p, float* lut, int h, int 
   return fold;
 }
 
-// log2 sum_j exp(t - l) of one row whose |LSE| is huge (see huge_rows), by a whole warp
-template <int D, int NA>
-__device__ __forceinline__ float huge_row(const Params& p, const float* lut, bool small, float l, int row, int h,
-                                          int hk, int klo, int khi, int lane) {
-  const float units = small ? kLn2 : 1.0f;
-  const uint16_t* q = p.q + ((size_t)row * p.Hq + h) * D;
-  float sum = 0.0f;
-  for (int j = klo + lane; j < khi; j += 32) {
-    const uint16_t* k = p.k + ((size_t)j * p.Hkv + hk) * D;
-    float t = 0.0f;
-    for (int d = 0; d < D; ++d) t = fmaf(bf16_to_f32(q[d]), bf16_to_f32(k[d]), t);
-    t *= p.scale;
-    for (int a = 0; a < NA; ++a)
-      t += units * lut[a * (2 * p.maxd + 1) + clamp_index(p.pos_k[(size_t)j * NA + a],
-                                                          p.maxd - p.pos_q[(size_t)row * NA + a], 2 * p.maxd)];
-    sum += ex2((t - l) * kLog2e);
-  }
-  __syncwarp();
-  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-  return log2f(sum);
-}
-
 // ---- dq -------------------------------------------------------------------------------------------
 
 template <int D>
@@ -116,7 +94,7 @@ struct DqTcSmem {
   int pos[C::kStages][NA][kTcCols];
   ChunkMeta meta[C::kStages];
   uint64_t q_full, kv_full[C::kStages], kv_empty[C::kStages], s_full[2], p_full[2], done[2], drain, ew;
-  float rest[2][128];
+  float rest[2][128], sum[2][128];
   uint32_t tmem_base;
   int abort, vote;
   float lut[1];  // [NA][2 maxd + 1]
@@ -292,8 +270,8 @@ __global__ void __launch_bounds__(kTcThreads, 2)
     bool ok = true;
     const bool small = ew_fill<NA>(p, S.lut, h, ew, &S.vote, eb, ok);
     const float mul = small ? p.scale * kLog2e : p.scale;
-    float lse = valid ? p.lse_in[at] : INFINITY, delta = 0.0f, corr = 0.0f, rest = 0.0f;
-    if (lse == -INFINITY) lse = INFINITY;  // a row without keys: P = 0
+    const float lse = row_lse(valid ? p.lse_in[at] : INFINITY), rconst = row_const(lse, small);
+    float delta = 0.0f, rest = 0.0f, sum = 0.0f;
     if (valid) {
       const uint4* a = reinterpret_cast<const uint4*>(p.dout + at * D);
       const uint4* b = reinterpret_cast<const uint4*>(p.o_in + at * D);
@@ -309,17 +287,7 @@ __global__ void __launch_bounds__(kTcThreads, 2)
       }
     }
     __syncwarp();
-    const bool huge = fabsf(lse) >= kFoldLimit && lse != INFINITY;
-    uint32_t todo = __ballot_sync(0xffffffffu, huge);
-    while (todo) {
-      const int src = __ffs(todo) - 1;
-      todo &= todo - 1;
-      const float x = huge_row<D, NA>(p, S.lut, small, __shfl_sync(0xffffffffu, lse, src),
-                                      row0 + quarter * 32 + src, h, hk, klo, khi, lane);
-      if (lane == src) corr = x;
-    }
-    __syncwarp();
-    const float l2 = fmaf(lse, kLog2e, corr), rconst = small ? l2 : lse;
+    const bool exact = !small || __any_sync(0xffffffffu, is_huge(lse));
 
     ChunkBias<NA> cb;
     for (int c = 0; ok && c < chunks; ++c) {
@@ -341,16 +309,20 @@ __global__ void __launch_bounds__(kTcThreads, 2)
         tmem_wait16(s);
         tmem_wait16(d);
         float x[16];
-        // small tables: in log2 units, the row's constant with the bias; others: the subtraction last
-        const float b = cb.row16(small ? cb.ub - rconst : cb.ub, S.pos[st], 2 * half + g, rowc, S.lut, top);
+        if (!exact) {  // the row's constant with the bias
+          const float b = cb.row16(cb.ub - rconst, S.pos[st], 2 * half + g, rowc, S.lut, top);
 #pragma unroll
-        for (int e = 0; e < 16; e += 2)
-          ffma2(x[e], x[e + 1], __uint_as_float(s[e]), __uint_as_float(s[e + 1]), mul, b);
-        if (!cb.flat(2 * half + g)) cb.add16(x, S.pos[st], 2 * half + g, rowc, S.lut, top);
-        if (!small) {
+          for (int e = 0; e < 16; e += 2)
+            ffma2(x[e], x[e + 1], __uint_as_float(s[e]), __uint_as_float(s[e + 1]), mul, b);
+          if (!cb.flat(2 * half + g)) cb.add16(x, S.pos[st], 2 * half + g, rowc, S.lut, top);
+        } else {
           keep_branch();
+          cb.exact16(x, s, mul, S.pos[st], 2 * half + g, rowc, S.lut, top);
 #pragma unroll
-          for (int e = 0; e < 16; ++e) x[e] = fmaf(x[e] - rconst, kLog2e, -corr);
+          for (int e = 0; e < 16; ++e) {
+            x[e] -= rconst;
+            if (!small) x[e] *= kLog2e;
+          }
         }
         if (left < col + 16) {  // no key: P = 0, and dP may be anything
           keep_branch();
@@ -358,7 +330,7 @@ __global__ void __launch_bounds__(kTcThreads, 2)
           for (int e = 0; e < 16; ++e)
             if (col + e >= left) x[e] = -INFINITY, d[e] = 0;
         }
-        float s0 = 0.0f, s1 = 0.0f;
+        float s0 = 0.0f, s1 = 0.0f, l0 = 0.0f, l1 = 0.0f;
         uint32_t pp[8], pd[8];
 #pragma unroll
         for (int e = 0; e < 16; e += 2) {
@@ -367,10 +339,12 @@ __global__ void __launch_bounds__(kTcThreads, 2)
           fadd2_acc(d0, d1, -delta, -delta);
           fmul2(d0, d1, d0, d1, p0, p1);
           fadd2_acc(s0, s1, d0, d1);
+          fadd2_acc(l0, l1, p0, p1);
           pp[e / 2] = pack2(p0, p1);
           pd[e / 2] = pack2(d0, d1);
         }
         rest += s0 + s1;
+        sum += l0 + l1;
         tmem_st8(tbase + C::kColP + half * C::kHalf + g * 8, pp);
         tmem_st8(tbase + C::kColDs + half * C::kHalf + g * 8, pd);
       }
@@ -383,11 +357,14 @@ __global__ void __launch_bounds__(kTcThreads, 2)
            wait_bar_w(&S.done[1], (chunks - 1) & 1, abort, p.status);
     tc_fence_after();
     S.rest[half][r] = rest;
+    S.sum[half][r] = sum;
     ok = eb.sync() && ok;
-    const float more = S.rest[0][r] + S.rest[1][r];  // Delta less the one of the saved out
+    const float l = S.sum[0][r] + S.sum[1][r], inv = valid ? row_inverse(l, rconst, p.status) : 0.0f;
+    const float more = (S.rest[0][r] + S.rest[1][r]) * inv, f = inv * p.scale;  // more: Delta less the saved out's
     if (half == 0 && valid) {
+      const float corr = row_corr(l);
       p.delta[at] = delta + more;
-      p.lse2[at] = l2;
+      p.lse2[at] = row_lse2(rconst, small, corr);
       p.corr[at] = corr;
     }
     // each thread half of the row's dq
@@ -406,7 +383,7 @@ __global__ void __launch_bounds__(kTcThreads, 2)
       if (!valid) continue;
       float x[16];
 #pragma unroll
-      for (int e = 0; e < 16; ++e) x[e] = fmaf(-more, __uint_as_float(k[e]), __uint_as_float(o[e])) * p.scale;
+      for (int e = 0; e < 16; ++e) x[e] = fmaf(-more, __uint_as_float(k[e]), __uint_as_float(o[e])) * f;
       uint32_t u[8];
 #pragma unroll
       for (int e = 0; e < 8; ++e) u[e] = pack2(x[2 * e], x[2 * e + 1]);
@@ -458,6 +435,7 @@ struct DkvTcSmem {
   uint64_t k_full, q_full[C::kStages], q_empty[C::kStages], s_full[2], p_full[2], done[2], drain, ew, turn[4];
   uint32_t tmem_base;
   int abort, vote, pad;
+  int huge[C::kStages][2];  // whether a half of the columns has a row of huge |LSE|
   // behind it: table fp32 [NA][2 maxd + 1], the buckets' byte offsets int32 [2 maxd + 1], and the
   // columns of sums fp32 [NA][NB and one for ids out of range][kSums]
   static size_t bytes(int maxd, int nb) {
@@ -560,6 +538,8 @@ __global__ void __launch_bounds__(kTcThreads, CTAS)
       for (int i = 0; i < 2; ++i) {
         S.nlse[st][lane + 32 * i] = -l[i];
         S.ndelta[st][lane + 32 * i] = -dl[i];
+        const bool huge = __any_sync(0xffffffffu, is_huge(l[i]));
+        if (lane == 0) S.huge[st][i] = huge;
       }
       if (n < kTcCols) {
         copy_tail<D>(S.q[st], p.q, q0, n, p.Hq, h, lane);
@@ -712,8 +692,8 @@ __global__ void __launch_bounds__(kTcThreads, CTAS)
         const float4* ls = reinterpret_cast<const float4*>(&S.nlse[st][col]);
         const float4* ds = reinterpret_cast<const float4*>(&S.ndelta[st][col]);
         float x[16];
-        const float b = cb.row16(cb.ub, S.pos[st], 2 * half + g, rowc, lut, top);
-        if (small) {
+        if (small && !S.huge[st][half]) {
+          const float b = cb.row16(cb.ub, S.pos[st], 2 * half + g, rowc, lut, top);
 #pragma unroll
           for (int f = 0; f < 4; ++f) {
             float4 l = ls[f];
@@ -725,18 +705,16 @@ __global__ void __launch_bounds__(kTcThreads, CTAS)
           }
           if (!cb.flat(2 * half + g)) cb.add16(x, S.pos[st], 2 * half + g, rowc, lut, top);
         } else {
-          // natural units, the subtraction last: exact for scores of any size
+          // the row's constant and the correction one after the other: together they would be rounded to the
+          // former's spacing
           keep_branch();
-#pragma unroll
-          for (int e = 0; e < 16; ++e) x[e] = fmaf(__uint_as_float(s[e]), mul, b);
-          cb.add16(x, S.pos[st], 2 * half + g, rowc, lut, top);
+          cb.exact16(x, s, mul, S.pos[st], 2 * half + g, rowc, lut, top);
           const int q = qlo + (c0 + cc) * kTcCols + col;
 #pragma unroll
           for (int e = 0; e < 16; ++e) {
             const size_t at = (size_t)min(q + e, qhi - 1) * p.Hq + hk * p.G + head;
-            float l = q + e < qhi ? p.lse_in[at] : INFINITY;
-            if (l == -INFINITY) l = INFINITY;
-            x[e] = fmaf(x[e] - l, kLog2e, -p.corr[at]);
+            x[e] -= row_const(q + e < qhi ? row_lse(p.lse_in[at]) : INFINITY, small);
+            x[e] = small ? x[e] - p.corr[at] : fmaf(x[e], kLog2e, -p.corr[at]);
           }
         }
         uint32_t pp[8], pd[8];

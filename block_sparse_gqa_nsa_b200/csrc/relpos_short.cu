@@ -204,7 +204,7 @@ __global__ void __launch_bounds__(kShThreads, 2) rp_short_fwd_kernel(const Param
         for (int a = 0; a < NA; ++a)
           mode[a] = axis_mode<NA>(pt + a, q_lo[a], q_hi[a], false, p.maxd, lane, one[a], p.status);
         float base[1][2];
-        const bool fold = add_bias<NA, 1, 1>(s, base, mode, one, pt, mine, top, rowc, mul, small, tq);
+        const bool fold = add_bias<NA, 1, 1>(s, base, mode, one, pt, mine, top, rowc, mul, !small, tq);
         if (left < kCols) {
           keep_branch();
 #pragma unroll
@@ -319,7 +319,7 @@ __global__ void __launch_bounds__(kShThreads, D == 32 ? 2 : 1) rp_short_dq_kerne
   auto row_of = [&](int u) { return P.row0 + u / P.nh * 16 + g; };
   auto head_of = [&](int u) { return u % P.nh; };
   // a unit's operands: queries, dO and out by asynchronous copies, LSE
-  float lse[2], next_lse[2];
+  float next_lse[2];
   auto fetch = [&](int u) {
     if (u < units) {
       const int r0 = P.row0 + u / P.nh * 16, r = r0 + g, n = P.qhi - r0, h = P.h0 + head_of(u);
@@ -347,13 +347,13 @@ __global__ void __launch_bounds__(kShThreads, D == 32 ? 2 : 1) rp_short_dq_kerne
       sh_take<D>(qa, next, lane);
       sh_take<D>(da, next + C::kUnit, lane);
       sh_take<D>(oa, next + 2 * C::kUnit, lane);
-      lse[0] = next_lse[0], lse[1] = next_lse[1];
     }
+    const float lse[2] = {work ? row_lse(next_lse[0]) : INFINITY, work ? row_lse(next_lse[1]) : INFINITY};
     __syncwarp();
     fetch(u + kShWarps);
     int rowc[1][2][NA], q_lo[NA], q_hi[NA];
     sh_row_positions<NA>(p, r, P.qhi, rowc, q_lo, q_hi);
-    float delta[2] = {0.0f, 0.0f}, rest[2] = {0.0f, 0.0f}, corr[2] = {0.0f, 0.0f}, row[2], l2[2];
+    float delta[2] = {0.0f, 0.0f}, rest[2] = {0.0f, 0.0f}, l[2] = {0.0f, 0.0f}, row[2];
 #pragma unroll
     for (int d = 0; d < D / 16; ++d)
 #pragma unroll
@@ -365,18 +365,10 @@ __global__ void __launch_bounds__(kShThreads, D == 32 ? 2 : 1) rp_short_dq_kerne
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
       delta[k] = quad_sum(delta[k]);
-      if (lse[k] == -INFINITY || !work) lse[k] = INFINITY;  // a row without keys: P = 0
-      huge = huge || (fabsf(lse[k]) >= kFoldLimit && lse[k] != INFINITY);
+      huge = huge || is_huge(lse[k]);
+      row[k] = row_const(lse[k], small);
     }
-    if (__any_sync(0xffffffffu, huge)) {
-      const float2 x = huge_rows<D, NA>(p, mine, small, lse[0], lse[1], r - g, h, P.hk, P.klo, P.khi, lane);
-      corr[0] = x.x, corr[1] = x.y;
-    }
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      l2[k] = fmaf(lse[k], kLog2e, corr[k]);
-      row[k] = small ? l2[k] : lse[k];
-    }
+    const bool exact = !small || __any_sync(0xffffffffu, huge);
     float dq[D / 8][4], pk[D / 8][4];
 #pragma unroll
     for (int n = 0; n < D / 8; ++n)
@@ -420,7 +412,7 @@ __global__ void __launch_bounds__(kShThreads, D == 32 ? 2 : 1) rp_short_dq_kerne
         for (int a = 0; a < NA; ++a)
           mode[a] = axis_mode<NA>(pt + a, q_lo[a], q_hi[a], false, p.maxd, lane, one[a], p.status);
         float base[1][2];
-        const bool fold = add_bias<NA, 1, 1>(s, base, mode, one, pt, mine, top, rowc, mul, small, tq);
+        const bool fold = add_bias<NA, 1, 1>(s, base, mode, one, pt, mine, top, rowc, mul, exact, tq);
         if (left < kCols) {
           keep_branch();
 #pragma unroll
@@ -433,7 +425,7 @@ __global__ void __launch_bounds__(kShThreads, D == 32 ? 2 : 1) rp_short_dq_kerne
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
           const float cst = base[0][k] - row[k];
-          float s0 = 0.0f, s1 = 0.0f;
+          float s0 = 0.0f, s1 = 0.0f, l0 = 0.0f, l1 = 0.0f;
 #pragma unroll
           for (int n = 0; n < kGroups; ++n) {
             float p0 = s[0][n][2 * k], p1 = s[0][n][2 * k + 1];
@@ -441,10 +433,11 @@ __global__ void __launch_bounds__(kShThreads, D == 32 ? 2 : 1) rp_short_dq_kerne
               ffma2(p0, p1, p0, p1, mul, cst);
             } else {  // the subtraction first: exact for scores of any size
               fadd2_acc(p0, p1, -row[k], -row[k]);
-              if (!small) ffma2(p0, p1, p0, p1, kLog2e, -corr[k]);
+              if (!small) fmul2(p0, p1, p0, p1, kLog2e, kLog2e);
             }
             p0 = ex2(p0);
             p1 = ex2(p1);
+            fadd2_acc(l0, l1, p0, p1);
             pa[n >> 1][(n & 1) * 2 + k] = pack2(p0, p1);
             float d0 = dp[n][2 * k], d1 = dp[n][2 * k + 1];
             fadd2_acc(d0, d1, -delta[k], -delta[k]);
@@ -453,6 +446,7 @@ __global__ void __launch_bounds__(kShThreads, D == 32 ? 2 : 1) rp_short_dq_kerne
             sa[n >> 1][(n & 1) * 2 + k] = pack2(d0, d1);
           }
           rest[k] += s0 + s1;
+          l[k] += l0 + l1;
         }
 #pragma unroll
         for (int j = 0; j < 2; ++j)
@@ -470,20 +464,22 @@ __global__ void __launch_bounds__(kShThreads, D == 32 ? 2 : 1) rp_short_dq_kerne
     if (work) {
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
-        const float more = quad_sum(rest[k]);  // Delta less the one of the saved out
+        const float sum = quad_sum(l[k]), parts = quad_sum(rest[k]);
         const int at_row = r + 8 * k;
         if (at_row >= P.qhi) continue;
+        const float inv = row_inverse(sum, row[k], p.status), corr = row_corr(sum);
+        const float more = parts * inv;  // Delta less the one of the saved out
         const size_t at = (size_t)at_row * p.Hq + h;
         if (tq == 0) {
           p.delta[at] = delta[k] + more;
-          p.lse2[at] = l2[k];
-          p.corr[at] = corr[k];
+          p.lse2[at] = row_lse2(row[k], small, corr);
+          p.corr[at] = corr;
         }
+        const float f = inv * p.scale;
 #pragma unroll
         for (int n = 0; n < D / 8; ++n)
           *reinterpret_cast<uint32_t*>(p.dq + at * D + n * 8 + 2 * tq) =
-              pack2(fmaf(-more, pk[n][2 * k], dq[n][2 * k]) * p.scale,
-                    fmaf(-more, pk[n][2 * k + 1], dq[n][2 * k + 1]) * p.scale);
+              pack2(fmaf(-more, pk[n][2 * k], dq[n][2 * k]) * f, fmaf(-more, pk[n][2 * k + 1], dq[n][2 * k + 1]) * f);
       }
     }
   }

@@ -264,12 +264,9 @@ __global__ void __launch_bounds__(kTcThreads, 2)
       for (int g = 0; g < 4; ++g) {
         uint32_t r[16];
         float b[16];
-        const float row_b = cb.row16(cb.ub, S.pos[st], g, rowc, S.lut, top);
         tmem_ld16(tbase + C::kColS + 16 * g, r);
         tmem_wait16(r);
-#pragma unroll
-        for (int e = 0; e < 16; ++e) b[e] = fmaf(__uint_as_float(r[e]), mul, row_b);
-        cb.add16(b, S.pos[st], g, rowc, S.lut, top);
+        cb.exact16(b, r, mul, S.pos[st], g, rowc, S.lut, top);
 #pragma unroll
         for (int e = 0; e < 16; ++e)
           if (16 * g + e < left) mx = fmaxf(mx, b[e]);
@@ -294,12 +291,9 @@ __global__ void __launch_bounds__(kTcThreads, 2)
       for (int g = 0; g < 4; ++g) {
         uint32_t r[16], pk[8];
         float b[16];
-        const float row_b = cb.row16(cb.ub, S.pos[st], g, rowc, S.lut, top);
         tmem_ld16(tbase + C::kColS + 16 * g, r);
         tmem_wait16(r);
-#pragma unroll
-        for (int e = 0; e < 16; ++e) b[e] = fmaf(__uint_as_float(r[e]), mul, row_b);
-        cb.add16(b, S.pos[st], g, rowc, S.lut, top);
+        cb.exact16(b, r, mul, S.pos[st], g, rowc, S.lut, top);
 #pragma unroll
         for (int e = 0; e < 16; ++e) {
           const float x = ex2((b[e] - ref) * to_log2);

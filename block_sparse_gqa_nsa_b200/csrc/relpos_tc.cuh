@@ -167,40 +167,61 @@ struct ChunkBias {
       if (mode(a, g) == kLane) base += lut[a * (top + 1) + clamp_index(pos[a][16 * g], rowc[a], top)];
     return base;
   }
+  // axis a's biases of run g (kFour and up) added to its 16 scores
+  __device__ __forceinline__ void axis16(float (&x)[16], int (*pos)[kTcCols], int a, int g, const int (&rowc)[NA],
+                                         const float* lut, int top) const {
+    const float* la = lut + a * (top + 1);
+    const int4* xs = reinterpret_cast<const int4*>(&pos[a][16 * g]);
+    const int m = mode(a, g);
+    if (m == kFour) {
+#pragma unroll
+      for (int f = 0; f < 4; ++f) {
+        const float y = la[clamp_index(xs[f].x, rowc[a], top)];
+        fadd2_acc(x[4 * f], x[4 * f + 1], y, y);
+        fadd2_acc(x[4 * f + 2], x[4 * f + 3], y, y);
+      }
+    } else if (kHasTurn<NA> && m == kTurn) {
+      const int4 u = xs[0];
+      const float y0 = la[clamp_index(u.x, rowc[a], top)], y1 = la[clamp_index(u.y, rowc[a], top)];
+      const float y2 = la[clamp_index(u.z, rowc[a], top)], y3 = la[clamp_index(u.w, rowc[a], top)];
+#pragma unroll
+      for (int f = 0; f < 4; ++f) {
+        fadd2_acc(x[4 * f], x[4 * f + 1], y0, y1);
+        fadd2_acc(x[4 * f + 2], x[4 * f + 3], y2, y3);
+      }
+    } else if (m == kEach) {
+#pragma unroll
+      for (int f = 0; f < 4; ++f) {
+        const int4 u = xs[f];
+        // single adds: a pair of look-ups would first have to be moved into a pair of registers
+        x[4 * f] += la[clamp_index(u.x, rowc[a], top)];
+        x[4 * f + 1] += la[clamp_index(u.y, rowc[a], top)];
+        x[4 * f + 2] += la[clamp_index(u.z, rowc[a], top)];
+        x[4 * f + 3] += la[clamp_index(u.w, rowc[a], top)];
+      }
+    }
+  }
   // the rest of run g's biases (what row16 leaves out) added to its 16 scores
   __device__ __forceinline__ void add16(float (&x)[16], int (*pos)[kTcCols], int g, const int (&rowc)[NA],
                                         const float* lut, int top) const {
 #pragma unroll
+    for (int a = 0; a < NA; ++a) axis16(x, pos, a, g, rowc, lut, top);
+  }
+  // x = s * mul + all of run g's biases in the formula's own order, whatever the run has in common
+  __device__ __forceinline__ void exact16(float (&x)[16], const uint32_t (&s)[16], float mul, int (*pos)[kTcCols],
+                                          int g, const int (&rowc)[NA], const float* lut, int top) const {
+#pragma unroll
+    for (int e = 0; e < 16; e += 2)
+      ffma2(x[e], x[e + 1], __uint_as_float(s[e]), __uint_as_float(s[e + 1]), mul, 0.0f);
+#pragma unroll
     for (int a = 0; a < NA; ++a) {
-      const float* la = lut + a * (top + 1);
-      const int4* xs = reinterpret_cast<const int4*>(&pos[a][16 * g]);
       const int m = mode(a, g);
-      if (m == kFour) {
+      if (m <= kLane) {
+        const float y = lut[a * (top + 1) + (m == kOne ? one[a] : clamp_index(pos[a][16 * g], rowc[a], top))];
 #pragma unroll
-        for (int f = 0; f < 4; ++f) {
-          const float y = la[clamp_index(xs[f].x, rowc[a], top)];
-          fadd2_acc(x[4 * f], x[4 * f + 1], y, y);
-          fadd2_acc(x[4 * f + 2], x[4 * f + 3], y, y);
-        }
-      } else if (kHasTurn<NA> && m == kTurn) {
-        const int4 u = xs[0];
-        const float y0 = la[clamp_index(u.x, rowc[a], top)], y1 = la[clamp_index(u.y, rowc[a], top)];
-        const float y2 = la[clamp_index(u.z, rowc[a], top)], y3 = la[clamp_index(u.w, rowc[a], top)];
-#pragma unroll
-        for (int f = 0; f < 4; ++f) {
-          fadd2_acc(x[4 * f], x[4 * f + 1], y0, y1);
-          fadd2_acc(x[4 * f + 2], x[4 * f + 3], y2, y3);
-        }
-      } else if (m == kEach) {
-#pragma unroll
-        for (int f = 0; f < 4; ++f) {
-          const int4 u = xs[f];
-          // single adds: a pair of look-ups would first have to be moved into a pair of registers
-          x[4 * f] += la[clamp_index(u.x, rowc[a], top)];
-          x[4 * f + 1] += la[clamp_index(u.y, rowc[a], top)];
-          x[4 * f + 2] += la[clamp_index(u.z, rowc[a], top)];
-          x[4 * f + 3] += la[clamp_index(u.w, rowc[a], top)];
-        }
+        for (int e = 0; e < 16; e += 2) fadd2_acc(x[e], x[e + 1], y, y);
+      } else {
+        axis16(x, pos, a, g, rowc, lut, top);
       }
     }
   }

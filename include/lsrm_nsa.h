@@ -359,8 +359,11 @@ LSRM_API lsrm_status lsrm_relpos_forward(const lsrm_relpos_desc* desc, const int
 
 /* Backward of L = sum(out * dout): dq bf16 [Nq][Hq][d], dk, dv bf16 [Nk][Hkv][d], dtable bf16
  * [n_axes][n_buckets][Hq] (all overwritten; dk, dv of keys without queries and the entries of buckets
- * that no pair has are 0; rows that belong to no segment are left as they were).  out and lse are the forward's; dout bf16 [Nq][Hq][d].  All sums have a
- * fixed order: results are reproducible bit for bit.  Errors as above. */
+ * that no pair has are 0; rows that belong to no segment are left as they were).  out and lse are the
+ * forward's; dout bf16 [Nq][Hq][d].  A row's weights exp(t - lse) are divided by their own sum, so they sum to
+ * 1 whatever the rounding of lse.  Where that sum leaves fp32's range (an lse that is not the forward's, scores
+ * past 2^27 in size), LSRM_ERR_BOUNDS is raised in the device status.  All sums have a fixed order: results
+ * are reproducible bit for bit.  Errors as above. */
 LSRM_API lsrm_status lsrm_relpos_backward(const lsrm_relpos_desc* desc, const int32_t* off_q, const int32_t* off_k,
                                           const int32_t* pos_q, const int32_t* pos_k, const int32_t* bucket_of,
                                           const void* table, const void* q, const void* k, const void* v,

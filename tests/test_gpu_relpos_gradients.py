@@ -1,8 +1,12 @@
 """The gradients of the relative-position-bias attention on the GPU row by row against their definition in
-64 bits: the shapes of every kernel, and peaked rows."""
+64 bits: the shapes of every kernel, peaked rows, scores and biases of any size."""
+import math
+
 import pytest
+import torch
 
 import relpos_bars as bars
+import relpos_ref as ref
 from test_gpu_relpos import FEW, FORWARD, Case
 
 from block_sparse_gqa_nsa_b200 import nsa
@@ -52,3 +56,82 @@ SHAPES = {
 def test_peaked_rows(name, spread):
     """Rows with nearly all weight on one key: dS nearly cancels, so the Delta of the rounded out would show."""
     rows(Case(**SHAPES[name], spread=spread))
+
+
+@pytest.mark.parametrize("spread", [3e4, 3e5, 2e6])
+@pytest.mark.parametrize("name", SHAPES)
+def test_huge_scores_beside_a_small_table(name, spread):
+    """LSE so large that fp32 loses the sum: every row's weights still sum to 1."""
+    f, got = rows(Case(**SHAPES[name], spread=spread))
+    assert all(bool(x.isfinite().all()) for x in got.values())
+
+
+@pytest.mark.parametrize("name", ["middle32", "long32", "long64"])
+def test_some_huge_rows(name):
+    """A few rows of huge scores among ordinary ones."""
+    c = Case(**SHAPES[name])
+    c.q[::37] = (c.q[::37].float() * 3e5).to(c.q.dtype)
+    c.q[50:60, 1] = (c.q[50:60, 1].float() * 1e4).to(c.q.dtype)
+    rows(c)
+
+
+@pytest.mark.parametrize("name", SHAPES)
+@pytest.mark.parametrize("low", [-1e5, -1e7, -1e9, -1e30])
+def test_rows_under_a_mask_on_one_axis_and_biases_on_another(name, low):
+    """Every key of a row at a finite mask on one axis: the order in which the axes are added decides how a
+    score rounds, so every pass has to take the same one.  The other axis makes one key stand out (distance
+    0) by far more than the mask's spacing, where a mask still has one."""
+    kw = {**SHAPES[name], "axes": 2, "places": "order"}
+    kw.pop("maxd", None)
+    c = Case(**kw)
+    c.table[0, :, 0] = low
+    c.table[1, :, 0] = -100.5
+    c.table[1, c.bucket_of[128].item(), 0] = 100.5
+    if low < -1e8:  # the mask swallows the other axis: equal weights
+        c.table[1, :, 0] = 0
+        c.q[:, 0] = 0
+    rows(c)
+
+
+def test_one_key_has_all_the_weight():
+    """Whatever its bias: dv is the sum of dO over the queries and heads."""
+    for lens_q, lens_k in (([1] * 50, [1] * 50), ([64, 30] * 30, [1] * 60), ([300], [1]), ([700, 700], [400, 1])):
+        c = Case(lens_q, lens_k, axes=2, places="scattered", heads=4, kv_heads=2)
+        c.table[0] = -1e7
+        c.table[1] = (c.table[1].float() * 40).to(c.table.dtype)
+        f, got = rows(c)
+        lo = 0
+        for n, m, at in zip(lens_q, lens_k, c.off_k.tolist()):
+            if m == 1:
+                want = c.dout[lo:lo + n].double().view(n, 2, 2, 32).sum((0, 2))
+                size = c.dout[lo:lo + n].double().abs().view(n, 2, 2, 32).sum((0, 2))
+                assert bool(((got["dv"][at].double() - want).abs() <= 2.0 ** -8 * want.abs() + 2.0 ** -20 * size).all())
+            lo += n
+
+
+def test_a_masked_head_over_a_long_past():
+    """A head whose every bias is the type's lowest value: the mean over many keys."""
+    c = Case([400, 3], [20000, 17], heads=2, kv_heads=1, dim=64)
+    c.table[0, :, 1] = torch.finfo(torch.bfloat16).min
+    f, got = rows(c)
+    want = c.reference(False)
+    ref.check("out", f["out"], want["out"])
+    ref.check("lse", f["lse"], want["lse"])
+
+
+def test_gradients_are_the_same_bits_again():
+    for name in ("long32", "long64", "middle32"):
+        c = Case(**SHAPES[name], spread=1e5)
+        f = c.forward()
+        a = {n: x.clone() for n, x in c.backward(f).items()}
+        b = c.backward(f)
+        assert all(torch.equal(a[n], b[n]) for n in a)
+
+
+def test_scores_past_the_documented_size_are_reported():
+    """Scores past 2^27 lose LSE itself: finite and reported, or right."""
+    c = Case([300], spread=1e12)
+    f = c.forward()
+    c.backward(f)
+    assert nsa.lsrm_nsa_last_device_status(c.ws) in (0, 5)
+    assert math.isfinite(float(f["out"].float().abs().max()))
