@@ -584,12 +584,6 @@ __global__ void __launch_bounds__(kJoinThreads) rp_join_kernel(const Params p) {
 
 static lsrm_status launched() { return cudaGetLastError() == cudaSuccess ? LSRM_OK : LSRM_ERR_CUDA; }
 
-template <typename K>
-static bool allow_smem(K kernel, size_t bytes) {
-  return bytes <= 48 * 1024 ||
-         cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes) == cudaSuccess;
-}
-
 template <int D, int NA, int NW>
 static lsrm_status run_fwd(const Params& p, long long ctas, cudaStream_t s) {
   const size_t bytes = FwdCfg<D, NA, NW>::smem(p.maxd);

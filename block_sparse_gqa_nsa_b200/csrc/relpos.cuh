@@ -442,6 +442,16 @@ __device__ __forceinline__ void split_range(const Params& p, int split, int chun
 }
 
 // ---- launch plans and the workspace (host) ----
+// A kernel's limit of dynamic shared memory belongs to the kernel, so it is always the same, whatever this call
+// needs: a second thread with a smaller table cannot lower it between a call's setting and its launch.
+constexpr int kSmemMost = 227 * 1024;
+template <typename K>
+inline bool allow_smem(K kernel, size_t bytes) {
+  return bytes <= 48 * 1024 ||
+         (bytes <= (size_t)kSmemMost &&
+          cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMost) == cudaSuccess);
+}
+
 constexpr int kSms = 148;
 constexpr int kShHeads = 16;                 // heads a CTA of the short segments' kernels takes, at most
 constexpr size_t kShTables = 64 * 1024;      // bytes of their bias tables, at most

@@ -652,12 +652,6 @@ __global__ void __launch_bounds__(kSumThreads) rp_dkv_join_kernel(const Params p
 
 static lsrm_status launched() { return cudaGetLastError() == cudaSuccess ? LSRM_OK : LSRM_ERR_CUDA; }
 
-template <typename K>
-static bool allow_smem(K kernel, size_t bytes) {
-  return bytes <= 48 * 1024 ||
-         cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes) == cudaSuccess;
-}
-
 template <int D, int NA>
 static lsrm_status run_dq(const Params& p, const BwdPlan& b, cudaStream_t s) {
   const size_t bytes = BwdCfg<D, NA>::smem_dq(p.maxd);

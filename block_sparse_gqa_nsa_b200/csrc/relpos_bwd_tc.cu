@@ -864,8 +864,7 @@ static lsrm_status run_dkv_tc(const Params& p, const BwdPlan& b, const CUtensorM
                               const CUtensorMap& q64, const CUtensorMap& o64, cudaStream_t s) {
   const size_t bytes = DkvTcSmem<D, NA, CTAS>::bytes(p.maxd, p.NB);
   auto* kernel = rp_dkv_tc_kernel<D, NA, CTAS>;
-  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes) != cudaSuccess)
-    return LSRM_ERR_CUDA;
+  if (!allow_smem(kernel, bytes)) return LSRM_ERR_CUDA;
   kernel<<<(unsigned)(b.kv_tiles * p.Hkv * p.splits), kTcThreads, bytes, s>>>(k128, v128, q64, o64, p);
   return cudaGetLastError() == cudaSuccess ? LSRM_OK : LSRM_ERR_CUDA;
 }
@@ -880,9 +879,7 @@ static lsrm_status run_bwd_tc(const Params& p, const BwdPlan& b, cudaStream_t s)
     return LSRM_ERR_CUDA;
   if (p.Nq > 0) {
     const size_t bytes = DqTcSmem<D, NA>::bytes(p.maxd);
-    if (cudaFuncSetAttribute(rp_dq_tc_kernel<D, NA>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes) !=
-        cudaSuccess)
-      return LSRM_ERR_CUDA;
+    if (!allow_smem(rp_dq_tc_kernel<D, NA>, bytes)) return LSRM_ERR_CUDA;
     rp_dq_tc_kernel<D, NA><<<(unsigned)(b.dq_tiles * p.Hq), kTcThreads, bytes, s>>>(q128, o128, k64, v64, p);
     if (cudaGetLastError() != cudaSuccess) return LSRM_ERR_CUDA;
   }

@@ -489,9 +489,7 @@ template <int D, int NA>
 static lsrm_status run_short(const Params& p, long long ctas, bool dq, cudaStream_t s) {
   const size_t bytes = ShCfg<D, NA>::smem(p.maxd, p.G < kShHeads ? p.G : kShHeads, dq);
   const void* kernel = dq ? (const void*)rp_short_dq_kernel<D, NA> : (const void*)rp_short_fwd_kernel<D, NA>;
-  if (bytes > 48 * 1024 &&
-      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes) != cudaSuccess)
-    return LSRM_ERR_CUDA;
+  if (!allow_smem(kernel, bytes)) return LSRM_ERR_CUDA;
   if (dq)
     rp_short_dq_kernel<D, NA><<<(unsigned)ctas, kShThreads, bytes, s>>>(p);
   else

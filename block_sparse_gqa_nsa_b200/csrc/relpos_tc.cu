@@ -425,9 +425,7 @@ static lsrm_status run_tc(const Params& p, long long ctas, cudaStream_t s) {
       !make_map(&vm, keys ? p.v : p.q, D, keys ? p.Hkv : p.Hq, keys ? p.Nk : p.Nq, 1, 64))
     return LSRM_ERR_CUDA;
   const size_t bytes = TcFwdSmem<D, NA>::bytes(p.maxd);
-  if (cudaFuncSetAttribute(rp_fwd_tc_kernel<D, NA>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes) !=
-      cudaSuccess)
-    return LSRM_ERR_CUDA;
+  if (!allow_smem(rp_fwd_tc_kernel<D, NA>, bytes)) return LSRM_ERR_CUDA;
   rp_fwd_tc_kernel<D, NA><<<(unsigned)ctas, kTcThreads, bytes, s>>>(qm, km, vm, p);
   return cudaGetLastError() == cudaSuccess ? LSRM_OK : LSRM_ERR_CUDA;
 }

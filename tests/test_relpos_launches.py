@@ -1,0 +1,81 @@
+"""What the relative-position attention asks of the CUDA runtime, on the CPU: a stand-in for the few runtime
+calls that it makes records them and launches nothing."""
+import json
+import os
+import subprocess
+import sys
+
+import pytest
+
+from block_sparse_gqa_nsa_b200.build import build
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+
+FAKE = r"""
+#include <stdio.h>
+#include <stddef.h>
+typedef struct { unsigned x, y, z; } dim3_;
+typedef struct { dim3_ grid, block; size_t smem; void* stream; void* attrs; unsigned n; } config_;
+int cudaFuncSetAttribute(const void* f, int attr, int value) { printf("[\"set\", %zu, %d, %d]\n", (size_t)f, attr, value); return 0; }
+int cudaLaunchKernel(const void* f, dim3_ g, dim3_ b, void** args, size_t smem, void* s) {
+  printf("[\"launch\", %zu, %u, %zu]\n", (size_t)f, g.x, smem); return 0; }
+int cudaLaunchKernelExC(const config_* c, const void* f, void** args) {
+  printf("[\"launch\", %zu, %u, %zu]\n", (size_t)f, c->grid.x, c->smem); return 0; }
+int cudaGetLastError(void) { return 0; }
+static int encode() { return 0; }
+int cudaGetDriverEntryPoint(const char* name, void** p, unsigned long long flags, int* q) { *p = (void*)encode; *q = 0; return 0; }
+"""
+
+CALLS = r"""
+import ctypes, sys
+sys.path.insert(0, sys.argv[1])
+from block_sparse_gqa_nsa_b200 import nsa
+lib = nsa.load_library()
+for maxd, nb in ((1, 2), (1023, 64), (100, 16), (1, 64)):
+    for S, q, k in ((2, 1, 900), (2, 9, 900), (2, 50, 900), (2, 90, 900), (60, 50, 50), (2, 200, 200), (2, 700, 700),
+                    (1, 30, 30)):
+        for dim in (32, 64):
+            for axes in (1, 2, 3):
+                for heads, kv in ((4, 2), (32, 2)):
+                    d = nsa.make_relpos_desc(S * q, S * k, S, heads, kv, dim, axes, nb, maxd)
+                    n = nsa.lsrm_relpos_workspace_size(d)
+                    for r in (lib.lsrm_relpos_forward(ctypes.byref(d), *[4096] * 11, 4096, n, None),
+                              lib.lsrm_relpos_backward(ctypes.byref(d), *[4096] * 16, 4096, n, None)):
+                        if r:
+                            sys.exit(f"status {r}")
+"""
+
+
+@pytest.fixture(scope="module")
+def records(tmp_path_factory):
+    build()
+    d = tmp_path_factory.mktemp("fake")
+    (d / "fake.c").write_text(FAKE)
+    (d / "calls.py").write_text(CALLS)
+    subprocess.check_call(["gcc", "-shared", "-fPIC", "-w", "-o", str(d / "fake.so"), str(d / "fake.c")])
+    out = subprocess.run([sys.executable, str(d / "calls.py"), ROOT], env={**os.environ, "LD_PRELOAD": str(d / "fake.so")},
+                         capture_output=True, text=True)
+    assert out.returncode == 0, out.stderr[-500:]
+    return [json.loads(x) for x in out.stdout.splitlines() if x.startswith("[")]
+
+
+def test_a_kernels_shared_memory_limit_is_the_same_for_every_call(records):
+    """The limit belongs to the kernel, not to the call: one that followed a call's table could be lowered by a
+    second thread between the first one's setting and its launch."""
+    limits = {}
+    for what, f, *x in records:
+        if what == "set":
+            limits.setdefault((f, x[0]), set()).add(x[1])
+    assert len(limits) > 20
+    assert all(len(v) == 1 for v in limits.values()), sorted(limits.values(), key=len)[-1]
+
+
+def test_launches_are_within_their_limits(records):
+    limit, seen = {}, set()
+    for what, f, *x in records:
+        if what == "set":
+            limit[f] = x[1]
+        else:
+            assert 0 < x[0] < 2 ** 31 and x[1] <= max(limit.get(f, 0), 48 * 1024), (x, limit.get(f))
+            seen.add(f)
+    assert len(seen) > 30
