@@ -23,6 +23,10 @@ namespace {
 
 bool on(const void* p, size_t a) { return ((uintptr_t)p % a) == 0; }
 
+// the layer norm's column counters go a CTA past the row's end; more rows than this are more than 2^31 - 1 CTAs
+constexpr int32_t kLnMostWidth = 1 << 30;
+constexpr int64_t kLnMostRows = (int64_t)1 << 40;
+
 lsrm_status check_relpos(const lsrm_relpos_desc* d) {
   if (d == nullptr) return LSRM_ERR_INVALID_ARG;
   if (d->n_q_tokens < 0 || d->n_k_tokens < 0 || d->n_segs < 1) return LSRM_ERR_INVALID_ARG;
@@ -202,6 +206,7 @@ lsrm_status lsrm_layer_norm_forward(int64_t rows, int32_t width, int32_t dtype, 
                                     float* mean_or_null, float* rstd_or_null, void* stream) {
   if (rows < 0 || width < 1 || (dtype != LSRM_BF16 && dtype != LSRM_F32) || !(eps >= 0.0f) || isinf(eps))
     return LSRM_ERR_INVALID_ARG;
+  if (width > kLnMostWidth || rows > kLnMostRows) return LSRM_ERR_UNSUPPORTED;
   if (rows == 0) return LSRM_OK;
   const size_t el = dtype == LSRM_BF16 ? 2 : 4;
   if (x == nullptr || y == nullptr) return LSRM_ERR_INVALID_ARG;
@@ -213,7 +218,7 @@ lsrm_status lsrm_layer_norm_forward(int64_t rows, int32_t width, int32_t dtype, 
 }
 
 size_t lsrm_layer_norm_workspace_size(int64_t rows, int32_t width) {
-  if (rows < 0 || width < 1) return 0;
+  if (rows < 0 || width < 1 || width > kLnMostWidth || rows > kLnMostRows) return 0;
   return rp::up256((size_t)ln_max_ctas(rows, width) * 2 * (size_t)width * 4);
 }
 
@@ -222,6 +227,7 @@ lsrm_status lsrm_layer_norm_backward(int64_t rows, int32_t width, int32_t dtype,
                                      void* dgamma_or_null, void* dbeta_or_null, void* ws, size_t ws_bytes,
                                      void* stream) {
   if (rows < 0 || width < 1 || (dtype != LSRM_BF16 && dtype != LSRM_F32)) return LSRM_ERR_INVALID_ARG;
+  if (width > kLnMostWidth || rows > kLnMostRows) return LSRM_ERR_UNSUPPORTED;
   const size_t el = dtype == LSRM_BF16 ? 2 : 4;
   if (rows > 0 && (dy == nullptr || x == nullptr || mean == nullptr || rstd == nullptr || dx == nullptr))
     return LSRM_ERR_INVALID_ARG;

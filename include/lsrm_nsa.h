@@ -376,14 +376,15 @@ LSRM_API lsrm_status lsrm_relpos_backward(const lsrm_relpos_desc* desc, const in
  *   mean = sum(x) / C;  rstd = 1 / sqrt(sum((x - mean)^2) / C + eps);  y = (x - mean) rstd gamma + beta
  * in fp32.  gamma_or_null / beta_or_null [C] (NULL: 1 / 0); mean_or_null, rstd_or_null fp32 [rows]
  * (what the backward needs).  y may be x.  rows >= 0, width >= 1, eps >= 0 and finite, else
- * LSRM_ERR_INVALID_ARG; more than 2^31 - 1 CTAs: LSRM_ERR_UNSUPPORTED. */
+ * LSRM_ERR_INVALID_ARG; rows of more than 2^30 elements or more than 2^31 - 1 CTAs: LSRM_ERR_UNSUPPORTED. */
 enum { LSRM_BF16 = 0, LSRM_F32 = 1 };
 LSRM_API lsrm_status lsrm_layer_norm_forward(int64_t rows, int32_t width, int32_t dtype, const void* x,
                                              const void* gamma_or_null, const void* beta_or_null, float eps, void* y,
                                              float* mean_or_null, float* rstd_or_null, void* stream);
 
 /* Bytes of device workspace of lsrm_layer_norm_backward (any type; nothing in it needs initialising
- * or is kept between calls; calls that may overlap on the GPU need one each); 0 for rows < 0 or width < 1. */
+ * or is kept between calls; calls that may overlap on the GPU need one each); 0 for rows and widths that the
+ * call does not take. */
 LSRM_API size_t lsrm_layer_norm_workspace_size(int64_t rows, int32_t width);
 
 /* Backward: with xh = (x - mean) rstd and g = dy gamma, dx = rstd (g - mean(g) - xh mean(g xh)),
