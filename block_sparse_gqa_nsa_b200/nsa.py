@@ -386,7 +386,7 @@ def relpos_workspace(desc: RelposDesc, device=None, stream=None) -> torch.Tensor
     n = lsrm_relpos_workspace_size(desc)
     if n == 0:
         raise NsaError("lsrm_relpos_workspace_size", 1)
-    ws = torch.empty(n, dtype=torch.uint8, device=device or "cuda")
+    ws = torch.empty(n, dtype=torch.uint8, device="cuda" if device is None else device)
     lsrm_relpos_workspace_init(desc, ws, stream)
     return ws
 
@@ -476,7 +476,7 @@ def layer_norm_workspace(rows: int, width: int, device=None) -> torch.Tensor:
     n = lsrm_layer_norm_workspace_size(rows, width)
     if n == 0:
         raise NsaError("lsrm_layer_norm_workspace_size", 1)
-    return torch.empty(n, dtype=torch.uint8, device=device or "cuda")
+    return torch.empty(n, dtype=torch.uint8, device="cuda" if device is None else device)
 
 
 def lsrm_layer_norm_backward(dy, x, gamma, mean, rstd, dx, dgamma, dbeta, ws, stream=None):

@@ -1,6 +1,7 @@
 """Host side of the layer norm: rows of more elements than the kernels' 32-bit column counters reach, and more rows
 than a grid has CTAs, are refused (no call here launches anything)."""
 import pytest
+import torch
 
 from block_sparse_gqa_nsa_b200 import nsa
 from block_sparse_gqa_nsa_b200.build import build
@@ -35,3 +36,21 @@ def test_most_rows(lib, rows):
 
 def test_no_rows_of_any_width(lib):
     assert lib.lsrm_layer_norm_forward(0, MOST, 0, None, None, None, 1e-6, None, None, None, None) == 0
+
+
+@pytest.mark.parametrize("make", [lambda device: nsa.layer_norm_workspace(4, 8, device),
+                                  lambda device: nsa.relpos_workspace(nsa.make_relpos_desc(4, 4, 1, 2, 2, 32, 1, 8, 8),
+                                                                      device)])
+def test_workspaces_are_made_on_the_device_that_was_named(lib, make, monkeypatch):
+    """Device 0 by its number is that device, not the current one."""
+    asked = []
+
+    def empty(n, dtype, device):
+        asked.append(device)
+        return torch.zeros(n, dtype=dtype)
+
+    monkeypatch.setattr(nsa.torch, "empty", empty)
+    monkeypatch.setattr(nsa, "lsrm_relpos_workspace_init", lambda *a: None)
+    for given, want in ((0, 0), (1, 1), (None, "cuda"), ("cuda:1", "cuda:1")):
+        make(given)
+        assert asked[-1] == want, given
