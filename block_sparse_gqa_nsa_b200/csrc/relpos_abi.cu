@@ -37,13 +37,14 @@ lsrm_status check_relpos(const lsrm_relpos_desc* d) {
   if (!(d->scale >= 0.0f) || isinf(d->scale)) return LSRM_ERR_INVALID_ARG;
   if (d->head_dim != 32 && d->head_dim != 64) return LSRM_ERR_UNSUPPORTED;
   if (d->n_q_tokens > (int64_t)INT32_MAX || d->n_k_tokens > (int64_t)INT32_MAX) return LSRM_ERR_UNSUPPORTED;
+  if (d->n_q_heads > 65535) return LSRM_ERR_UNSUPPORTED;  // before the plans, which try splits of a group's heads
   // tiles of every kernel in one grid dimension (the finest: one query token a tile and a KV head)
   const rp::FwdPlan f = rp::fwd_plan(*d);
   const rp::BwdPlan b = rp::bwd_plan(*d);
   const long long most = INT32_MAX;
   if (f.ctas > most || b.short_ctas > most || b.dq_tiles * d->n_q_heads > most ||
       b.kv_tiles * d->n_kv_heads * b.splits > most || d->n_segs > most / 2 || d->n_q_tokens + d->n_segs > most ||
-      d->n_k_tokens + d->n_segs > most || d->n_q_heads > 65535)
+      d->n_k_tokens + d->n_segs > most)
     return LSRM_ERR_UNSUPPORTED;
   return LSRM_OK;
 }

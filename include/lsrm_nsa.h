@@ -317,7 +317,7 @@ typedef struct {
   int64_t n_q_tokens;   /* Nq, 0..2^31-1 */
   int64_t n_k_tokens;   /* Nk, 0..2^31-1 */
   int32_t n_segs;       /* S >= 1 */
-  int32_t n_q_heads;    /* Hq, multiple of n_kv_heads */
+  int32_t n_q_heads;    /* Hq, multiple of n_kv_heads, at most 65535 */
   int32_t n_kv_heads;   /* Hkv >= 1 */
   int32_t head_dim;     /* d in {32, 64} */
   int32_t n_axes;       /* position axes, 1..3 */
@@ -349,7 +349,7 @@ LSRM_API lsrm_status lsrm_relpos_log_buckets(int32_t n_buckets, int32_t max_dist
  * must not overlap inputs.  Rows that belong to no segment are left as they were.  Segment bounds, positions or bucket ids outside their
  * ranges raise LSRM_ERR_BOUNDS in the device status (the bounds and distances are clipped, such a
  * bucket counts as bias 0); nothing outside the arrays is read or written.  Errors:
- * LSRM_ERR_INVALID_ARG (descriptor, null or misaligned pointer), LSRM_ERR_UNSUPPORTED (head_dim; a
+ * LSRM_ERR_INVALID_ARG (descriptor, null or misaligned pointer), LSRM_ERR_UNSUPPORTED (head_dim, heads; a
  * problem of more than 2^31 - 1 CTAs), LSRM_ERR_WORKSPACE (missing, not 256-byte aligned, or fewer
  * than lsrm_relpos_workspace_size bytes). */
 LSRM_API lsrm_status lsrm_relpos_forward(const lsrm_relpos_desc* desc, const int32_t* off_q, const int32_t* off_k,

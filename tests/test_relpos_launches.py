@@ -79,3 +79,20 @@ def test_launches_are_within_their_limits(records):
             assert 0 < x[0] < 2 ** 31 and x[1] <= max(limit.get(f, 0), 48 * 1024), (x, limit.get(f))
             seen.add(f)
     assert len(seen) > 30
+
+
+@pytest.mark.timeout(60)
+def test_too_many_heads_are_refused_at_once():
+    """The plans try every split of a group's heads: not of 2^31 of them (ten seconds a call)."""
+    import time
+
+    from block_sparse_gqa_nsa_b200 import nsa
+
+    build()
+    nsa.load_library()
+    for q in (100, 1000):
+        start = time.time()
+        assert nsa.lsrm_relpos_workspace_size(nsa.make_relpos_desc(q, q, 1, 2 ** 31 - 1, 1, 32, 1, 32, 128)) == 0
+        assert time.time() - start < 1
+    assert nsa.lsrm_relpos_workspace_size(nsa.make_relpos_desc(10, 10, 1, 65535, 1, 32, 1, 32, 128)) > 0
+    assert nsa.lsrm_relpos_workspace_size(nsa.make_relpos_desc(10, 10, 1, 65536, 1, 32, 1, 32, 128)) == 0
