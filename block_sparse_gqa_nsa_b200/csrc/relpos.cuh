@@ -485,10 +485,14 @@ int bwd_tc_ctas(int D, int NA, int maxd, int nb);  // CTAs of rp_dkv_tc_kernel a
 // 52 us against 43
 constexpr int kFewRows = 24;
 
-// Short segments' kernels: while a segment is a tile of queries or so, enough of them fill the GPU, and
-// the tables of a group's heads fit.  Segments of 64 tokens, 32 heads of 32 on 2 KV heads, forward and backward:
-// 64 of them 54 and 154 us, by the kernels of longer segments 37 and 129; 128 of them 56 and 206 against 66 and 214.
+// Short segments' kernels: while a segment is a tile of queries or so, enough of them fill the GPU, the tables of a
+// group's heads fit, and the group has heads for the eight warps.  Segments of 64 tokens, 32 heads of 32 on 2 KV heads,
+// forward and backward: 64 of them 54 and 154 us, by the kernels of longer segments 37 and 129; 128 of them 56 and 206
+// against 66 and 214.  Four heads a group, 256 of 40 tokens: 27 and 111 against 29 and 109; heads of their own, 128 of 64
+// tokens: 55 and 144 against 30 and 114.
+constexpr int kShGroup = 4;
 inline bool short_kernels(const lsrm_relpos_desc& d) {
+  if (d.n_q_heads / d.n_kv_heads < kShGroup) return false;
   const long long S = d.n_segs, mean_q = (d.n_q_tokens + S - 1) / S, mean_k = (d.n_k_tokens + S - 1) / S;
   return mean_q <= 64 && mean_k <= 64 && short_tables(d) <= kShTables && 3 * S * d.n_kv_heads >= 4 * kSms;
 }
