@@ -477,7 +477,10 @@ struct BwdPlan {
   long long dq_tiles, kv_tiles, short_ctas;
   int parts() const { return splits > g ? splits / g : 1; }  // table sums per (key tile, head)
 };
-constexpr int kTcKeys = 128;  // tensor-memory kernels of the backward past this many keys
+// The backward's tensor-memory kernels past this many keys, from where a 128-row key tile is as full as two of 64:
+// backward of eight segments, three axes and 32 heads of 32, 512 queries against 64 keys 154 us (64-row kernels 117), 110
+// keys on one axis 93 (100); 16 heads of 64, 300 queries against 80 keys 90 (104), 160 keys 78 (136).
+constexpr int kTcKeys = 64;
 
 int bwd_tc_ctas(int D, int NA, int maxd, int nb);  // CTAs of rp_dkv_tc_kernel an SM holds, 0: too large
 
@@ -543,8 +546,8 @@ inline BwdPlan bwd_plan(const lsrm_relpos_desc& d) {
   const long long mean_q = (d.n_q_tokens + S - 1) / S, mean_k = (d.n_k_tokens + S - 1) / S;
   b.g = (int)G;
   // From what length 128-row tiles fill up enough, whole backward of eight segments: 16 heads of 64, two axes, 128
-  // tokens 66 us (64-row kernels 59), 192 tokens 51 (101); 32 heads of 32, three axes, 320 tokens 200 us (186), 512
-  // tokens 351 (434).
+  // tokens 69 us (64-row kernels 56), 192 tokens 56 (100); 32 heads of 32, three axes, 320 tokens 205 us (194), 384
+  // tokens 232 (289).
   b.tc = mean_k > kTcKeys && mean_q > (d.head_dim == 64 ? 128 : 320)
              ? bwd_tc_ctas(d.head_dim, d.n_axes, d.max_distance, d.n_buckets)
              : 0;

@@ -48,6 +48,9 @@ SHAPES = {
     "long_turns": dict(lens_q=[520, 400], axes=2, places="scattered", maxd=40),
     "cross": dict(lens_q=[400, 330], lens_k=[300, 500], heads=6, dim=64),
     "few": dict(lens_q=[1, 9, 3], lens_k=[700, 64, 2000], heads=16),
+    "past64": dict(lens_q=[340, 400], lens_k=[70, 128]),
+    "past64_dim64": dict(lens_q=[200, 140, 150], lens_k=[65, 128, 66], dim=64, heads=6),
+    "group4": dict(lens_q=[40, 64, 1, 0] * 15, heads=8, kv_heads=2, axes=2, places="scattered"),
 }
 
 
