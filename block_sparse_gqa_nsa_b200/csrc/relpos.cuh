@@ -562,8 +562,9 @@ inline BwdPlan bwd_plan(const lsrm_relpos_desc& d) {
   if (b.tc) {
     // The time in chunks of work: CTAs that an SM runs one after the other (whole ones while there are few,
     // later they even out) times a CTA's chunks and 2.5 for its beginning and end.  More splits only where they
-    // win 2%, as their sums have to be joined.  1024 tokens, 32 heads of 32: 16 splits 178 us, 32 splits 192; 4096
-    // tokens: 16 splits 2247 us, 8 splits 2312; 8 x 320 tokens: 16 splits 205 us, 4 splits 231 (all on three axes).
+    // win 2%, as their sums have to be joined.  Whole backward, 32 heads of 32 on three axes: 1024 tokens 16 splits 177
+    // us, 8 splits 254, 32 splits 188; 8 x 384 tokens 232 us, 16 splits 238, 4 splits 259; 4096 tokens 16 splits 2292 us,
+    // 8 splits 2359 (32 splits would take 2197).
     double best = 0.0;
     for (long long c = 1; c <= 64 * G && c <= G * (qchunks > 1 ? qchunks : 1); c = c < G ? c + 1 : c + G) {
       if (c < G && G % c) continue;
@@ -573,7 +574,7 @@ inline BwdPlan bwd_plan(const lsrm_relpos_desc& d) {
       if (c == 1 || cost < 0.98 * best) best = cost, sp = c;
     }
   } else {
-    // 8 CTAs an SM (256 ragged blocks of up to 64 tokens 350 us; 4 an SM 363)
+    // 8 CTAs an SM (key pass of 256 ragged blocks of up to 64 tokens 134 us; 4 an SM 142)
     sp = busy > 0 ? (8 * kSms + busy - 1) / busy : 1;
     if (sp > 64 * G) sp = 64 * G;
     if (sp < G) {

@@ -9,9 +9,10 @@
 //   * rp_dkv_kernel: keys of one KV head a CTA, the queries of its heads streaming: dk, dv and the
 //     table's gradient.
 // Both passes take 64-row tiles and mma.sync: with segments of up to a few hundred tokens, 128-row tiles of
-// tcgen05 are half empty (bwd_plan has the measured borders).  Many short segments have a dq pass of their own (relpos_short.cu).  What bounds the
-// passes is the per-score work (exponential, look-ups, and in the key pass the table's sums: 256 ragged blocks of
-// up to 64 tokens, 32 heads of 32: 129 us at 1.8 warp instructions a clock), not the tensor pipe (7%).
+// tcgen05 are half empty (bwd_plan has the measured borders).  Many short segments have a dq pass of their own
+// (relpos_short.cu).  What bounds the passes is the per-score work (exponential, look-ups, and in the key pass the
+// table's sums: 256 ragged blocks of up to 64 tokens, 32 heads of 32: 134 us at 1.8 warp instructions a clock), not the
+// tensor pipe (6%).
 //
 // Delta.  sum_d dO o with the forward's out is off by that output's bf16 rounding, which a gradient
 // that adds up a whole row of dS (the table's) or few keys (short segments) would show.  With D~ that

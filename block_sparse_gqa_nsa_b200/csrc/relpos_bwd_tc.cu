@@ -13,8 +13,9 @@
 // plain loads, warp 1 issues the MMAs, warps 2-9 do the scores: two threads a row, 32 columns each.  Each
 // half of the columns is a pipeline of its own (scores, products, barriers), so that with two CTAs an SM
 // four pipelines cover each other's hand-overs between the score warps and the tensor cores (4096 tokens, 32
-// heads of 32: dq 334 us, dk/dv 476; with one pipeline a tile dq went 375 -> 338 and dk/dv 573 -> 483 when it
-// was split).  The score warps are the bound: 2.1 to 2.3 warp instructions a clock and SM, the tensor pipe 14%.
+// heads of 32: dq 365 us, dk/dv 491; before dq had PK, it went 375 -> 338 and dk/dv 573 -> 483 when one pipeline a
+// tile was split).  The score warps are the bound: 2.0 to 2.3 warp instructions a clock and SM, the tensor pipe 13 to
+// 18%.
 // Against the mma.sync kernels, which they replace on long segments, the operands need no shared-memory
 // reads by the warps that compute, and runs of columns on one position share look-ups and sums.
 //

@@ -7,8 +7,8 @@
 // positions are brought to shared memory once, the bias tables of all its heads are filled side by side,
 // and the warps walk the (head, 16 queries) units, each fetching the next unit's operands while it works on
 // its own.  Longer segments stream their keys in blocks of 64, again for each round of units.
-// 256 ragged blocks of up to 64 tokens, 32 heads of 32, three axes: forward 67 us, dq 90; a CTA a head took 85
-// and 146.  Bound by instructions (2.3 and 1.9 a clock and SM), most of them around a score: the exponential,
+// 256 ragged blocks of up to 64 tokens, 32 heads of 32, three axes: forward 70 us, dq 99; a CTA a head took 85
+// and 146.  Bound by instructions (2.1 and 2.0 a clock and SM), most of them around a score: the exponential,
 // three look-ups, the tile's edges.
 #include "relpos.cuh"
 

@@ -312,7 +312,9 @@ LSRM_API lsrm_status lsrm_nsa_backward(const lsrm_nsa_desc* desc, const int32_t*
  * A query whose segment has no key (or whose every t is -inf, by a table entry of -inf or biases whose
  * sum over the axes passes fp32's range) gets out = 0 and lse = -inf.  Queries and keys may be the same
  * tensors (self attention: off_q = off_k, pos_q = pos_k) or not: one new token against a long past is a
- * segment of one query. */
+ * segment of one query.  Kernels are chosen by the mean lengths of a call's segments, which the host knows
+ * without reading the tables: segments of very different lengths are right together, but faster in a call
+ * for each kind (a prompt of 8192 tokens beside 511 single tokens 1.85 ms, apart 0.85 + 0.06). */
 typedef struct {
   int64_t n_q_tokens;   /* Nq, 0..2^31-1 */
   int64_t n_k_tokens;   /* Nk, 0..2^31-1 */
