@@ -25,7 +25,7 @@ struct ShCfg {
   static constexpr int kUnit = 16 * D / 8;  // pieces of 16 rows
   static constexpr size_t kUnits = (size_t)kShWarps * 3 * kUnit * 16;  // dq: the next queries, dO and out of a warp
   static size_t smem(int maxd, int heads, bool dq) {
-    return kRing + (dq ? kUnits : 0) + (size_t)heads * NA * (2 * maxd + 1) * 4;
+    return kRing + (dq ? kUnits : 0) + 16 + (size_t)heads * NA * (2 * maxd + 1) * 4;
   }
 };
 
@@ -53,29 +53,36 @@ __device__ __forceinline__ ShPlace sh_place(const Params& p) {
   return s;
 }
 
-// the bias tables of nh heads [head][axis][2 maxd + 1], as fill_units (one unit system for the CTA)
+// the bias tables of nh heads [head][axis][2 maxd + 1], each in its own units as fill_units has them (the key pass
+// takes the heads one by one, and has to come to the same scores).  Returns the heads with large tables; the word in
+// front of the tables collects them.
 template <int NA>
-__device__ __forceinline__ bool sh_fill(const Params& p, float* lut, int h0, int nh, int tid) {
+__device__ __forceinline__ uint32_t sh_fill(const Params& p, float* lut, int h0, int nh, int tid) {
   const int n = 2 * p.maxd + 1;
-  bool small = true;
+  uint32_t* word = reinterpret_cast<uint32_t*>(lut) - 1;
+  if (tid == 0) *word = 0;
+  __syncthreads();
+  uint32_t large = 0;
   for (int i = tid; i < n * nh; i += kShThreads) {
     const int d = i / nh, hh = i % nh;
     const int b = checked_bucket(p, d);
 #pragma unroll
     for (int a = 0; a < NA; ++a) {
       const float x = b < 0 ? 0.0f : bf16_to_f32(p.table[((size_t)a * p.NB + b) * p.Hq + h0 + hh]);
-      small = small && (fabsf(x) <= kSmallBias || x == -INFINITY);
+      if (!(fabsf(x) <= kSmallBias || x == -INFINITY)) large |= 1u << hh;
       lut[(hh * NA + a) * n + d] = x;
     }
   }
-  const bool fold = __syncthreads_and(small);
-  if (fold) {  // every thread scales the entries that it wrote
-    for (int i = tid; i < n * nh; i += kShThreads)
+  large = __reduce_or_sync(0xffffffffu, large);
+  if (large != 0 && (tid & 31) == 0) atomicOr(word, large);
+  __syncthreads();
+  large = *word;
+  for (int i = tid; i < n * nh; i += kShThreads)  // every thread scales the entries that it wrote
+    if (!(large >> (i % nh) & 1))
 #pragma unroll
       for (int a = 0; a < NA; ++a) lut[(i % nh * NA + a) * n + i / nh] *= kLog2e;
-  }
   __syncthreads();
-  return fold;
+  return large;
 }
 
 // rows g and g + 8 of a 16-row tile of one head as an A operand, zeros past the segment
@@ -129,7 +136,7 @@ __global__ void __launch_bounds__(kShThreads, 2) rp_short_fwd_kernel(const Param
   extern __shared__ __align__(16) unsigned char smem_raw[];
   uint4* ring = reinterpret_cast<uint4*>(smem_raw);  // [2][K, V]
   int* ps = reinterpret_cast<int*>(ring + 4 * C::kTile);
-  float* lut = reinterpret_cast<float*>(smem_raw + C::kRing);
+  float* lut = reinterpret_cast<float*>(smem_raw + C::kRing + 16);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, tq = lane & 3;
   const ShPlace P = sh_place(p);
   if (!P.live) return;
@@ -154,14 +161,15 @@ __global__ void __launch_bounds__(kShThreads, 2) rp_short_fwd_kernel(const Param
   auto row_of = [&](int u) { return P.row0 + u / P.nh * 16 + g; };
   auto head_of = [&](int u) { return u % P.nh; };
   if (warp < units) sh_rows<D>(qa[0], p.q, p, row_of(warp), P.qhi, P.h0 + head_of(warp), lane);
-  const bool small = sh_fill<NA>(p, lut, P.h0, P.nh, tid);
-  const float mul = small ? p.scale * kLog2e : p.scale, to_log2 = small ? 1.0f : kLog2e;
+  const uint32_t large = sh_fill<NA>(p, lut, P.h0, P.nh, tid);
 
   for (int round = 0; round < rounds; ++round) {
     const int u = round * kShWarps + warp;
     const bool work = u < units;
     const int r = row_of(work ? u : 0), hh = head_of(work ? u : 0);
     const float* mine = lut + hh * NA * (top + 1);
+    const bool small = !(large >> hh & 1);
+    const float mul = small ? p.scale * kLog2e : p.scale, to_log2 = small ? 1.0f : kLog2e;
     uint32_t nx[1][D / 16][4];
     if (u + kShWarps < units)
       sh_rows<D>(nx[0], p.q, p, row_of(u + kShWarps), P.qhi, P.h0 + head_of(u + kShWarps), lane);
@@ -297,7 +305,7 @@ __global__ void __launch_bounds__(kShThreads, D == 32 ? 2 : 1) rp_short_dq_kerne
   uint4* ring = reinterpret_cast<uint4*>(smem_raw);  // [2][K, V]
   int* ps = reinterpret_cast<int*>(ring + 4 * C::kTile);
   uint4* next = reinterpret_cast<uint4*>(smem_raw + C::kRing) + (threadIdx.x >> 5) * 3 * C::kUnit;
-  float* lut = reinterpret_cast<float*>(smem_raw + C::kRing + C::kUnits);
+  float* lut = reinterpret_cast<float*>(smem_raw + C::kRing + C::kUnits + 16);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, tq = lane & 3;
   const ShPlace P = sh_place(p);
   if (!P.live) return;
@@ -332,14 +340,15 @@ __global__ void __launch_bounds__(kShThreads, D == 32 ? 2 : 1) rp_short_dq_kerne
     cp_async_commit();
   };
   fetch(warp);
-  const bool small = sh_fill<NA>(p, lut, P.h0, P.nh, tid);
-  const float mul = small ? p.scale * kLog2e : p.scale;
+  const uint32_t large = sh_fill<NA>(p, lut, P.h0, P.nh, tid);
 
   for (int round = 0; round < rounds; ++round) {
     const int u = round * kShWarps + warp;
     const bool work = u < units;
     const int r = row_of(work ? u : 0), hh = head_of(work ? u : 0), h = P.h0 + hh;
     const float* mine = lut + hh * NA * (top + 1);
+    const bool small = !(large >> hh & 1);
+    const float mul = small ? p.scale * kLog2e : p.scale;
     uint32_t qa[D / 16][4], da[D / 16][4], oa[D / 16][4];
     cp_async_wait<0>();
     __syncwarp();

@@ -36,8 +36,13 @@ def test_rows_of_few_queries(name):
     rows(Case(**FEW[name]))
 
 
-# the backward's kernels: short segments, 64-row tiles, and 128-row tiles at both head dims
+# the backward's kernels: many short segments, 64-row tiles, and 128-row tiles at both head dims
 SHAPES = {
+    "many_short": dict(lens_q=[64, 33, 1, 50] * 25, heads=8, kv_heads=2),
+    "many_short64": dict(lens_q=[i * 7 % 65 for i in range(70)], heads=12, kv_heads=3, dim=64, axes=2,
+                         places="scattered", maxd=40),
+    "many_short_bricks": dict(lens_q=[64, 20, 64] * 23, heads=12, kv_heads=3, axes=3, places="bricks", maxd=16,
+                              buckets=16),
     "short": dict(lens_q=[64, 33, 1, 50] * 15, heads=8, kv_heads=2),
     "middle32": dict(lens_q=[300, 200, 77]),
     "middle64": dict(lens_q=[120, 100, 31], dim=64),
@@ -54,6 +59,65 @@ SHAPES = {
 }
 
 
+# what the kernels of many short segments can meet
+MANY = {
+    "wide_group": dict(lens_q=[40, 30] * 51, heads=40, kv_heads=2, axes=1, buckets=8),
+    "long_beside": dict(lens_q=[20, 0, 150, 9, 64] * 40, lens_k=[64, 7, 0, 200, 1] * 40, heads=4, kv_heads=1,
+                        places="scattered"),
+    "outside": dict(lens_q=[33, 12, 60] * 34, lead=5, heads=8, kv_heads=2, axes=3, places="scattered", maxd=7, buckets=7),
+    "few_keys64": dict(lens_q=[50, 41] * 100, lens_k=[1, 2] * 100, heads=4, kv_heads=1, dim=64),
+    "frames": dict(lens_q=[64, 31] * 50, heads=8, kv_heads=2, axes=2, places="frames", maxd=5, buckets=6),
+}
+
+
+@pytest.mark.parametrize("name", MANY)
+def test_many_short_segments(name):
+    c = Case(**MANY[name])
+    c.check()
+    rows(c)
+
+
+@pytest.mark.parametrize("low", [-math.inf, torch.finfo(torch.bfloat16).min, -1e30])
+def test_many_short_segments_under_masks(low):
+    c = Case(lens_q=[40, 23, 64] * 35, heads=8, kv_heads=2, buckets=4, maxd=3)
+    c.table[0, 2:] = low  # keys after the query
+    c.check()
+    rows(c)
+    c.table[0, :, 1] = low  # every key of one head
+    c.check()
+    rows(c)
+
+
+@pytest.mark.parametrize("what", ["off_q", "off_k", "bucket_of", "pos_q", "pos_k"])
+def test_bad_tables_of_many_short_segments(what):
+    c = Case(lens_q=[40, 24, 9] * 35, heads=8, kv_heads=2, axes=2, places="scattered")
+    c.pos_q = c.pos_q.clone()  # not the keys'
+    x = getattr(c, what)
+    keep = x.clone()
+    if what.startswith("off"):
+        x[1], x[2] = 2 ** 31 - 1, -5
+    elif what == "bucket_of":
+        x[:100], x[150:] = 32, -2 ** 31
+    else:
+        x[3], x[20] = 2 ** 31 - 1, -2 ** 31
+    c.backward(c.forward())
+    assert nsa.lsrm_nsa_last_device_status(c.ws) == 5
+    x.copy_(keep)
+    c.check()
+
+
+def test_neighbours_of_many_short_segments_do_not_leak():
+    c = Case([40, 23, 61] * 40, dim=64, heads=4, kv_heads=2 // 2)
+    clean = {n: x.clone() for n, x in c.check()[0].items()}
+    for x in (c.k, c.v, c.q, c.dout):
+        x[40:63] = float("nan")
+    f = c.forward()
+    got = {**f, **c.backward(f)}
+    for n in ("out", "lse", "dq", "dk", "dv"):
+        for part in (slice(0, 40), slice(63, None)):
+            assert torch.equal(got[n][part], clean[n][part]), n
+
+
 @pytest.mark.parametrize("spread", [4.0, 8.0])
 @pytest.mark.parametrize("name", SHAPES)
 def test_peaked_rows(name, spread):
@@ -67,6 +131,15 @@ def test_huge_scores_beside_a_small_table(name, spread):
     """LSE so large that fp32 loses the sum: every row's weights still sum to 1."""
     f, got = rows(Case(**SHAPES[name], spread=spread))
     assert all(bool(x.isfinite().all()) for x in got.values())
+
+
+@pytest.mark.parametrize("spread", [3e5, 2e6])
+@pytest.mark.parametrize("name", SHAPES)
+def test_huge_scores_beside_one_heads_large_table(name, spread):
+    """A head whose table is large is scored in other units than its neighbours, in both passes alike."""
+    c = Case(**SHAPES[name], spread=spread)
+    c.table[0, :, 1] = 100.0
+    rows(c)
 
 
 @pytest.mark.parametrize("name", ["middle32", "long32", "long64"])
