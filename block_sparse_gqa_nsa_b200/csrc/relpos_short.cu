@@ -7,7 +7,7 @@
 // positions are brought to shared memory once, the bias tables of all its heads are filled side by side,
 // and the warps walk the (head, 16 queries) units, each fetching the next unit's operands while it works on
 // its own.  Longer segments stream their keys in blocks of 64, again for each round of units.
-// 256 ragged blocks of up to 64 tokens, 32 heads of 32, three axes: forward 70 us, dq 99; a CTA a head took 85
+// 256 ragged blocks of up to 64 tokens, 32 heads of 32, three axes: forward 71 us, dq 102; a CTA a head took 85
 // and 146.  Bound by instructions (2.1 and 2.0 a clock and SM), most of them around a score: the exponential,
 // three look-ups, the tile's edges.
 #include "relpos.cuh"
@@ -24,8 +24,9 @@ struct ShCfg {
   static constexpr size_t kRing = 2 * ((size_t)2 * kTile * 16 + kShKeys * NA * 4);
   static constexpr int kUnit = 16 * D / 8;  // pieces of 16 rows
   static constexpr size_t kUnits = (size_t)kShWarps * 3 * kUnit * 16;  // dq: the next queries, dO and out of a warp
+  static constexpr size_t kFlags = kShWarps * 4;  // a warp's heads with large tables
   static size_t smem(int maxd, int heads, bool dq) {
-    return kRing + (dq ? kUnits : 0) + 16 + (size_t)heads * NA * (2 * maxd + 1) * 4;
+    return kRing + (dq ? kUnits : 0) + kFlags + (size_t)heads * NA * (2 * maxd + 1) * 4;
   }
 };
 
@@ -54,14 +55,12 @@ __device__ __forceinline__ ShPlace sh_place(const Params& p) {
 }
 
 // the bias tables of nh heads [head][axis][2 maxd + 1], each in its own units as fill_units has them (the key pass
-// takes the heads one by one, and has to come to the same scores).  Returns the heads with large tables; the word in
-// front of the tables collects them.
+// takes the heads one by one, and has to come to the same scores).  Returns the heads with large tables, which the warps
+// collect in the words in front of the tables.
 template <int NA>
 __device__ __forceinline__ uint32_t sh_fill(const Params& p, float* lut, int h0, int nh, int tid) {
   const int n = 2 * p.maxd + 1;
-  uint32_t* word = reinterpret_cast<uint32_t*>(lut) - 1;
-  if (tid == 0) *word = 0;
-  __syncthreads();
+  uint32_t* words = reinterpret_cast<uint32_t*>(lut) - kShWarps;
   uint32_t large = 0;
   for (int i = tid; i < n * nh; i += kShThreads) {
     const int d = i / nh, hh = i % nh;
@@ -74,9 +73,10 @@ __device__ __forceinline__ uint32_t sh_fill(const Params& p, float* lut, int h0,
     }
   }
   large = __reduce_or_sync(0xffffffffu, large);
-  if (large != 0 && (tid & 31) == 0) atomicOr(word, large);
+  if ((tid & 31) == 0) words[tid >> 5] = large;
   __syncthreads();
-  large = *word;
+#pragma unroll
+  for (int w = 0; w < kShWarps; ++w) large |= words[w];
   for (int i = tid; i < n * nh; i += kShThreads)  // every thread scales the entries that it wrote
     if (!(large >> (i % nh) & 1))
 #pragma unroll
@@ -136,7 +136,7 @@ __global__ void __launch_bounds__(kShThreads, 2) rp_short_fwd_kernel(const Param
   extern __shared__ __align__(16) unsigned char smem_raw[];
   uint4* ring = reinterpret_cast<uint4*>(smem_raw);  // [2][K, V]
   int* ps = reinterpret_cast<int*>(ring + 4 * C::kTile);
-  float* lut = reinterpret_cast<float*>(smem_raw + C::kRing + 16);
+  float* lut = reinterpret_cast<float*>(smem_raw + C::kRing + C::kFlags);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, tq = lane & 3;
   const ShPlace P = sh_place(p);
   if (!P.live) return;
@@ -305,7 +305,7 @@ __global__ void __launch_bounds__(kShThreads, D == 32 ? 2 : 1) rp_short_dq_kerne
   uint4* ring = reinterpret_cast<uint4*>(smem_raw);  // [2][K, V]
   int* ps = reinterpret_cast<int*>(ring + 4 * C::kTile);
   uint4* next = reinterpret_cast<uint4*>(smem_raw + C::kRing) + (threadIdx.x >> 5) * 3 * C::kUnit;
-  float* lut = reinterpret_cast<float*>(smem_raw + C::kRing + C::kUnits + 16);
+  float* lut = reinterpret_cast<float*>(smem_raw + C::kRing + C::kUnits + C::kFlags);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, tq = lane & 3;
   const ShPlace P = sh_place(p);
   if (!P.live) return;
